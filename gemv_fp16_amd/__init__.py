@@ -28,6 +28,8 @@ EXPORTS = (
     "gf_gemm_default_config", "gf_gemv_default_config", "gf_status_string",
     "sp24_compress_f16", "gemm_sp_f16_nt", "gemm_sp_f16_nt_cfg", "gf_sp_config_count",
     "gf_sp_config_get", "gf_sp_default_config",
+    "gemm_f16_grouped_nt", "gemm_f16_grouped_nn", "gemm_f16_grouped_tn",
+    "w4_quantize_f16", "w4_dequantize_f16", "gemm_w4_f16_nt", "gemv_w4_f16", "gemm_w4_f16_grouped_nt",
 )
 
 
@@ -98,6 +100,14 @@ def lib() -> ctypes.CDLL:
     L.gemm_sp_f16_nt_cfg.argtypes = [vp, vp, vp, vp, ci, ci, ci, ctypes.POINTER(SpCfg), vp]
     L.gf_sp_config_get.argtypes = [ci, ctypes.POINTER(SpCfg)]
     L.gf_sp_default_config.argtypes = [ci, ci, ci, ctypes.POINTER(SpCfg)]
+    L.gemm_f16_grouped_nt.argtypes = [vp, vp, vp, vp, ci, ci, ci, ci, vp]
+    L.gemm_f16_grouped_nn.argtypes = [vp, vp, vp, vp, ci, ci, ci, ci, vp]
+    L.gemm_f16_grouped_tn.argtypes = [vp, vp, vp, vp, ci, ci, ci, ci, ci, vp]
+    L.w4_quantize_f16.argtypes = [vp, vp, vp, vp, ci, ci, ci, vp]
+    L.w4_dequantize_f16.argtypes = [vp, vp, vp, vp, ci, ci, ci, vp]
+    L.gemm_w4_f16_nt.argtypes = [vp, vp, vp, vp, vp, ci, ci, ci, ci, vp]
+    L.gemv_w4_f16.argtypes = [vp, vp, vp, vp, vp, ci, ci, ci, vp]
+    L.gemm_w4_f16_grouped_nt.argtypes = [vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, vp]
     L.gf_status_string.argtypes = [ci]
     L.gf_status_string.restype = ctypes.c_char_p
     for name in EXPORTS:
@@ -535,3 +545,198 @@ def sp_default_config(M: int, N: int, K: int) -> dict:
     _check(lib().gf_sp_default_config(M, N, K, ctypes.byref(c)), "gf_sp_default_config")
     return c.as_dict()
 
+
+# ---------------------------------------------------------------------------
+# products grouped by expert, 4-bit weights
+# ---------------------------------------------------------------------------
+
+def _same_device(*tensors):
+    """The device all of them (None aside) are on."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError("tensors are on different devices (%s and %s)" % (dev, t.device))
+    return dev
+
+
+def _launch(name, device, stream, *args):
+    """Call the C entry `name` on `stream`, by default the current stream of
+    the tensors' device, with that device current (the null stream is that of
+    the current device)."""
+    import torch
+    fn = getattr(lib(), name)
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    if device.index == torch.cuda.current_device():
+        rc = fn(*args, _stream(stream))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, _stream(stream))
+    if rc:
+        _check(rc, name)
+
+
+def _out(t, shape, dtype, device, stream, name):
+    """The caller's output, checked, or a new one."""
+    import torch
+    if t is None:
+        return _alloc(stream, lambda: torch.empty(shape, dtype=dtype, device=device))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must be %s" % (name, tuple(shape)))
+    return t
+
+
+def _offsets(offsets, E):
+    import torch
+    if offsets.dim() != 1 or offsets.shape[0] != E + 1:
+        raise ValueError("offsets must hold %d entries, one more than there are groups" % (E + 1))
+    return _dev(offsets, torch.int32, "offsets")
+
+
+def gemm_f16_grouped_nt(A, B, offsets, C=None, stream=None):
+    """C[r] = A[r] . B[e]^T for the rows r = offsets[e] .. offsets[e+1]-1 of
+    group e: A (T, K), B (E, N, K), offsets (E+1,) int32 on the device.
+    Returns C (T, N) fp16; rows of no group are left as they were."""
+    import torch
+    if A.dim() != 2 or B.dim() != 3 or A.shape[1] != B.shape[2]:
+        raise ValueError("A must be (T, K) and B (E, N, K)")
+    (T, K), (E, N) = A.shape, B.shape[:2]
+    C = _out(C, (T, N), torch.float16, A.device, stream, "C")
+    _launch("gemm_f16_grouped_nt", _same_device(A, B, offsets, C), stream, _dev(A, torch.float16, "A"),
+            _dev(B, torch.float16, "B"), _dev(C, torch.float16, "C"), _offsets(offsets, E), T, E, N, K)
+    return C
+
+
+def gemm_f16_grouped_nn(A, B, offsets, C=None, stream=None):
+    """C[r] = A[r] . B[e] for the rows r of group e: A (T, K), B (E, K, N).
+    With A the gradient of gemm_f16_grouped_nt's C and B its weights, the
+    gradient of its A.  Returns C (T, N) fp16."""
+    import torch
+    if A.dim() != 2 or B.dim() != 3 or A.shape[1] != B.shape[1]:
+        raise ValueError("A must be (T, K) and B (E, K, N)")
+    (T, K), E, N = A.shape, B.shape[0], B.shape[2]
+    C = _out(C, (T, N), torch.float16, A.device, stream, "C")
+    _launch("gemm_f16_grouped_nn", _same_device(A, B, offsets, C), stream, _dev(A, torch.float16, "A"),
+            _dev(B, torch.float16, "B"), _dev(C, torch.float16, "C"), _offsets(offsets, E), T, E, N, K)
+    return C
+
+
+def gemm_f16_grouped_tn(A, B, offsets, C=None, out_f32=None, stream=None):
+    """C[e] = A_e^T . B_e over the rows of group e: A (T, M), B (T, N).  With
+    A the gradient of gemm_f16_grouped_nt's C and B its A, the gradient of its
+    weights.  Returns C (E, M, N), fp16, or fp32 with out_f32=True (or a C of
+    that type); an empty group's C is zero."""
+    import torch
+    if A.dim() != 2 or B.dim() != 2 or A.shape[0] != B.shape[0]:
+        raise ValueError("A must be (T, M) and B (T, N)")
+    if offsets.dim() != 1 or offsets.shape[0] < 1:
+        raise ValueError("offsets must hold one entry more than there are groups")
+    (T, M), N, E = A.shape, B.shape[1], offsets.shape[0] - 1
+    if out_f32 is None:
+        out_f32 = C is not None and C.dtype == torch.float32
+    dt = torch.float32 if out_f32 else torch.float16
+    C = _out(C, (E, M, N), dt, A.device, stream, "C")
+    _launch("gemm_f16_grouped_tn", _same_device(A, B, offsets, C), stream, _dev(A, torch.float16, "A"),
+            _dev(B, torch.float16, "B"), _dev(C, dt, "C"), _offsets(offsets, E), T, E, M, N, int(bool(out_f32)))
+    return C
+
+
+def _w4_args(Q, S, Z, group, dim):
+    """Checked (pointers of Q, S, Z), leading shape and K of 4-bit weights."""
+    import torch
+    if Q.dim() != dim or S.dim() != dim or (Z is not None and Z.dim() != dim):
+        raise ValueError("Q, S and Z must have %d dimensions" % dim)
+    if group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128")
+    K = 8 * Q.shape[-1]
+    want = tuple(Q.shape[:-1]) + ((K + group - 1) // group,)
+    if tuple(S.shape) != want or (Z is not None and tuple(Z.shape) != want):
+        raise ValueError("S and Z must be %s for K = %d in groups of %d" % (want, K, group))
+    ptrs = (_dev(Q, torch.int32, "Q"), _dev(S, torch.float16, "S"),
+            None if Z is None else _dev(Z, torch.uint8, "Z"))
+    return ptrs, want[:-1], K
+
+
+def w4_quantize_f16(W, group: int = 128, symmetric: bool = False, Q=None, S=None, Z=None, stream=None):
+    """4-bit codes of W (N, K) or (E, N, K) fp16, K % 8 == 0, in groups of
+    `group` (32, 64 or 128) consecutive k.  Returns (Q, S, Z): Q (.., K/8) int32
+    words of 8 codes, S (.., G) fp16 scales, Z (.., G) uint8 zero points, or
+    None when symmetric (zero point 8)."""
+    import torch
+    if W.dim() not in (2, 3) or W.shape[-1] % 8:
+        raise ValueError("W must be (N, K) or (E, N, K) with K a multiple of 8")
+    if group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128")
+    if symmetric and Z is not None:
+        raise ValueError("symmetric codes have no Z")
+    lead, K = tuple(W.shape[:-1]), W.shape[-1]
+    Q = _out(Q, lead + (K // 8,), torch.int32, W.device, stream, "Q")
+    S = _out(S, lead + ((K + group - 1) // group,), torch.float16, W.device, stream, "S")
+    if not symmetric:
+        Z = _out(Z, tuple(S.shape), torch.uint8, W.device, stream, "Z")
+    rows = 1
+    for n in lead:
+        rows *= n
+    _launch("w4_quantize_f16", _same_device(W, Q, S, Z), stream, _dev(W, torch.float16, "W"),
+            _dev(Q, torch.int32, "Q"), _dev(S, torch.float16, "S"),
+            None if Z is None else _dev(Z, torch.uint8, "Z"), rows, K, group)
+    return Q, S, Z
+
+
+def w4_dequantize_f16(Q, S, Z=None, group: int = 128, W=None, stream=None):
+    """The weights (q - z) * s that Q, S and Z stand for, rounded to fp16."""
+    import torch
+    if Q.dim() not in (2, 3):
+        raise ValueError("Q must be (N, K/8) or (E, N, K/8)")
+    ptrs, lead, K = _w4_args(Q, S, Z, group, Q.dim())
+    W = _out(W, tuple(lead) + (K,), torch.float16, Q.device, stream, "W")
+    rows = 1
+    for n in lead:
+        rows *= n
+    _launch("w4_dequantize_f16", _same_device(Q, S, Z, W), stream, *ptrs, _dev(W, torch.float16, "W"),
+            rows, K, group)
+    return W
+
+
+def gemm_w4_f16_nt(A, Q, S, Z=None, C=None, group: int = 128, stream=None):
+    """C = A . W^T (fp32 accumulate, fp16 out) with A (M, K) and the 4-bit
+    weights Q (N, K/8), S, Z of w4_quantize_f16.  Returns C (M, N)."""
+    import torch
+    ptrs, (N,), K = _w4_args(Q, S, Z, group, 2)
+    if A.dim() != 2 or A.shape[1] != K:
+        raise ValueError("A must be (M, %d)" % K)
+    M = A.shape[0]
+    C = _out(C, (M, N), torch.float16, A.device, stream, "C")
+    _launch("gemm_w4_f16_nt", _same_device(A, Q, S, Z, C), stream, _dev(A, torch.float16, "A"), *ptrs,
+            _dev(C, torch.float16, "C"), M, N, K, group)
+    return C
+
+
+def gemv_w4_f16(Q, S, Z, x, y=None, group: int = 128, stream=None):
+    """y = W . x with the 4-bit weights Q (N, K/8), S, Z (or None) and x (K,)."""
+    import torch
+    ptrs, (N,), K = _w4_args(Q, S, Z, group, 2)
+    if x.dim() != 1 or x.shape[0] != K:
+        raise ValueError("x must be (%d,)" % K)
+    y = _out(y, (N,), torch.float16, x.device, stream, "y")
+    _launch("gemv_w4_f16", _same_device(x, Q, S, Z, y), stream, *ptrs, _dev(x, torch.float16, "x"),
+            _dev(y, torch.float16, "y"), N, K, group)
+    return y
+
+
+def gemm_w4_f16_grouped_nt(A, Q, S, Z, offsets, C=None, group: int = 128, stream=None):
+    """gemm_f16_grouped_nt with 4-bit weights: Q (E, N, K/8), S and Z (E, N, G)."""
+    import torch
+    ptrs, (E, N), K = _w4_args(Q, S, Z, group, 3)
+    if A.dim() != 2 or A.shape[1] != K:
+        raise ValueError("A must be (T, %d)" % K)
+    T = A.shape[0]
+    C = _out(C, (T, N), torch.float16, A.device, stream, "C")
+    _launch("gemm_w4_f16_grouped_nt", _same_device(A, Q, S, Z, offsets, C), stream,
+            _dev(A, torch.float16, "A"), *ptrs, _dev(C, torch.float16, "C"), _offsets(offsets, E), T, E, N, K,
+            group)
+    return C

@@ -43,6 +43,7 @@ struct GemmArgs {
     int kt_per_slice;   // K tiles per split-K slice
     int raster;         // 0: plain tile order; > 0: XCD remap + panel of this many rows
     int slices;         // split-K slices (set by launch_gemm); the grid is (tiles, slices)
+    static constexpr bool PER_GROUP = false;   // one product
 };
 
 // 16 zero bytes: the source of direct-to-LDS chunks that lie beyond K.
@@ -644,8 +645,11 @@ __device__ __forceinline__ void mfma_tile(typename Mfma<Cfg::MT>::acc_t (&acc)[C
 // The kernel
 // ---------------------------------------------------------------------------
 
-template <class Cfg, int EPI, bool ALIGNED>
-__global__ __launch_bounds__(Cfg::NT) void gemm_nt_kernel(GemmArgs a)
+// Args: GemmArgs, or a form of it that names one of several products
+// (PER_GROUP; grouped_kernel.hpp): its locate() then picks the workgroup's
+// product and tile, and narrows the operands to it.
+template <class Cfg, int EPI, bool ALIGNED, class Args = GemmArgs>
+__global__ __launch_bounds__(Cfg::NT) void gemm_nt_kernel(Args a)
 {
 #if defined(__HIP_DEVICE_COMPILE__)   // the host pass only needs the launch stub
     typedef Mfma<Cfg::MT> MF;
@@ -662,9 +666,12 @@ __global__ __launch_bounds__(Cfg::NT) void gemm_nt_kernel(GemmArgs a)
     const int wm = wave / Cfg::WN, wn = wave % Cfg::WN;
 
     // ---- which tile, and which K slice ----
+    int tm, tn, slice = 0;
+    if constexpr (Args::PER_GROUP) {
+        if (!a.template locate<Cfg::BM, Cfg::BN>(tm, tn)) return;
+    } else {
     const int tiles_m = ceil_div(a.M, Cfg::BM), tiles_n = ceil_div(a.N, Cfg::BN);
     const int ntiles = tiles_m * tiles_n;
-    int tm, tn, slice = 0;
     int w = blockIdx.x;
     if (a.slices > 1) {
         // Split-K: the grid (tiles, slices) enumerates (slice, tile) work
@@ -684,6 +691,7 @@ __global__ __launch_bounds__(Cfg::NT) void gemm_nt_kernel(GemmArgs a)
     } else {
         tm = w / tiles_n;
         tn = w % tiles_n;
+    }
     }
     const int m0 = tm * Cfg::BM, n0 = tn * Cfg::BN;
 

@@ -1,0 +1,186 @@
+// 4-bit weights: launch choice and C-ABI entry points.
+#include "../../include/gemvfp16.h"
+#include "w4_kernel.hpp"
+
+namespace gf {
+namespace {
+
+constexpr int64_t kW4MaxElems = (int64_t(1) << 31) - 1;
+constexpr int64_t kW4MaxGrid = (int64_t(1) << 31) - 1;
+
+bool w4_aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+bool w4_bad(const void* p, uintptr_t a) { return !p || !w4_aligned(p, a); }
+int w4_status(hipError_t e) { return e == hipSuccess ? GF_OK : GF_ERR_HIP; }
+
+// Sizes and groups of an N x K weight.
+int validate_w4(int N, int K, int group)
+{
+    if (N < 0 || K < 0 || K % 8 != 0) return GF_ERR_INVALID_ARG;
+    if (group != 32 && group != 64 && group != 128) return GF_ERR_INVALID_ARG;
+    if ((int64_t)N * K > kW4MaxElems) return GF_ERR_INVALID_ARG;
+    return GF_OK;
+}
+
+int w4_grid(int64_t items)
+{
+    const int64_t g = (items + 255) / 256;
+    return (int)(g < 65536 ? g : 65536);
+}
+
+template <int GROUP>
+hipError_t quantize(const void* W, void* Q, void* S, void* Z, int64_t N, int K, hipStream_t stream)
+{
+    const int G = ceil_div(K, GROUP);
+    const int64_t items = N * G * (GROUP / 8);
+    if (w4_aligned(W, 16))
+        hipLaunchKernelGGL((w4_quantize_kernel<GROUP, true>), dim3(w4_grid(items)), dim3(256), 0, stream,
+                           (const uint16_t*)W, (uint32_t*)Q, (uint16_t*)S, (uint8_t*)Z, K, G, items);
+    else
+        hipLaunchKernelGGL((w4_quantize_kernel<GROUP, false>), dim3(w4_grid(items)), dim3(256), 0, stream,
+                           (const uint16_t*)W, (uint32_t*)Q, (uint16_t*)S, (uint8_t*)Z, K, G, items);
+    return hipGetLastError();
+}
+
+template <int GROUP>
+hipError_t dequantize(const void* Q, const void* S, const void* Z, void* W, int64_t N, int K, hipStream_t stream)
+{
+    const int G = ceil_div(K, GROUP);
+    const int64_t words = N * (K / 8);
+    if (w4_aligned(W, 16))
+        hipLaunchKernelGGL((w4_dequantize_kernel<GROUP, true>), dim3(w4_grid(words)), dim3(256), 0, stream,
+                           (const uint32_t*)Q, (const uint16_t*)S, (const uint8_t*)Z, (uint16_t*)W, K, G, words);
+    else
+        hipLaunchKernelGGL((w4_dequantize_kernel<GROUP, false>), dim3(w4_grid(words)), dim3(256), 0, stream,
+                           (const uint32_t*)Q, (const uint16_t*)S, (const uint8_t*)Z, (uint16_t*)W, K, G, words);
+    return hipGetLastError();
+}
+
+__global__ void w4_zero_kernel(uint16_t* __restrict__ p, int64_t n)
+{
+    const int64_t stride = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t t = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; t < n; t += stride) p[t] = 0;
+}
+
+template <int GROUP, int MB, int NB, bool QVEC, bool AVEC, bool GROUPED>
+int launch_stream(const W4Args& a, hipStream_t stream)
+{
+    constexpr int WAVES = 8, LDS = WAVES * MB * NB * 256 * 4;
+    auto kern = w4_stream_kernel<GROUP, MB, NB, WAVES, QVEC, AVEC, GROUPED>;
+    static std::atomic<uint64_t> lds_opt_in{0};
+    if (LDS > 64 * 1024) {
+        const hipError_t e = opt_in_lds((const void*)kern, LDS, lds_opt_in, stream);
+        if (e != hipSuccess) return GF_ERR_HIP;
+    }
+    int64_t blocks = ceil_div(a.M, 16 * MB);
+    if (GROUPED) blocks = a.g.T / (16 * MB) + (a.g.E < a.g.T ? a.g.E : a.g.T);
+    const int64_t grid = blocks * ceil_div(a.N, 16 * NB);
+    if (grid > kW4MaxGrid) return GF_ERR_INVALID_ARG;
+    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(WAVES * 64), LDS, stream, a);
+    return w4_status(hipGetLastError());
+}
+
+template <int GROUP, int MB, int NB, bool GROUPED>
+int stream_by_alignment(const W4Args& a, hipStream_t stream)
+{
+    const bool avec = w4_aligned(a.A, 16), qvec = avec && w4_aligned(a.Q, 16) && a.K % 32 == 0;
+    if (qvec) return launch_stream<GROUP, MB, NB, true, true, GROUPED>(a, stream);
+    if (avec) return launch_stream<GROUP, MB, NB, false, true, GROUPED>(a, stream);
+    return launch_stream<GROUP, MB, NB, false, false, GROUPED>(a, stream);
+}
+
+template <int GROUP, bool GROUPED>
+int product(const W4Args& a, hipStream_t stream)
+{
+    const int64_t rows = GROUPED ? (a.g.T + a.g.E - 1) / a.g.E : a.M;
+    if (rows <= 16) return stream_by_alignment<GROUP, 1, 2, GROUPED>(a, stream);
+    return stream_by_alignment<GROUP, 2, 2, GROUPED>(a, stream);
+}
+
+template <bool GROUPED>
+int product_by_group(const W4Args& a, int group, hipStream_t stream)
+{
+    switch (group) {
+    case 32: return product<32, GROUPED>(a, stream);
+    case 64: return product<64, GROUPED>(a, stream);
+    default: return product<128, GROUPED>(a, stream);
+    }
+}
+
+}  // namespace
+}  // namespace gf
+
+using namespace gf;
+
+extern "C" {
+
+int w4_quantize_f16(const void* W, void* Q, void* S, void* Z, int N, int K, int group, void* stream)
+{
+    const int rc = validate_w4(0, K, group);
+    if (rc || N < 0) return GF_ERR_INVALID_ARG;
+    if (N == 0 || K == 0) return GF_OK;
+    if (w4_bad(W, 2) || w4_bad(Q, 4) || w4_bad(S, 2)) return GF_ERR_INVALID_ARG;
+    hipStream_t s = (hipStream_t)stream;
+    switch (group) {
+    case 32: return w4_status(quantize<32>(W, Q, S, Z, N, K, s));
+    case 64: return w4_status(quantize<64>(W, Q, S, Z, N, K, s));
+    default: return w4_status(quantize<128>(W, Q, S, Z, N, K, s));
+    }
+}
+
+int w4_dequantize_f16(const void* Q, const void* S, const void* Z, void* W, int N, int K, int group, void* stream)
+{
+    const int rc = validate_w4(0, K, group);
+    if (rc || N < 0) return GF_ERR_INVALID_ARG;
+    if (N == 0 || K == 0) return GF_OK;
+    if (w4_bad(W, 2) || w4_bad(Q, 4) || w4_bad(S, 2)) return GF_ERR_INVALID_ARG;
+    hipStream_t s = (hipStream_t)stream;
+    switch (group) {
+    case 32: return w4_status(dequantize<32>(Q, S, Z, W, N, K, s));
+    case 64: return w4_status(dequantize<64>(Q, S, Z, W, N, K, s));
+    default: return w4_status(dequantize<128>(Q, S, Z, W, N, K, s));
+    }
+}
+
+int gemm_w4_f16_nt(const void* A, const void* Q, const void* S, const void* Z, void* C, int M, int N, int K,
+                   int group, void* stream)
+{
+    const int rc = validate_w4(N, K, group);
+    if (rc) return rc;
+    if (M < 0 || (int64_t)M * K > kW4MaxElems || (int64_t)M * N > kW4MaxElems) return GF_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return GF_OK;
+    if (w4_bad(C, 2)) return GF_ERR_INVALID_ARG;
+    hipStream_t s = (hipStream_t)stream;
+    if (K == 0) {                                       // the empty sum
+        const int64_t mn = (int64_t)M * N;
+        hipLaunchKernelGGL(w4_zero_kernel, dim3(w4_grid(mn)), dim3(256), 0, s, (uint16_t*)C, mn);
+        return w4_status(hipGetLastError());
+    }
+    if (w4_bad(A, 2) || w4_bad(Q, 4) || w4_bad(S, 2)) return GF_ERR_INVALID_ARG;
+    W4Args a = {(const uint16_t*)A, (const uint32_t*)Q, (const uint16_t*)S, (const uint8_t*)Z, (uint16_t*)C,
+                M, N, K, ceil_div(K, group), {nullptr, 0, 0}};
+    return product_by_group<false>(a, group, s);
+}
+
+int gemv_w4_f16(const void* Q, const void* S, const void* Z, const void* x, void* y, int N, int K, int group,
+                void* stream)
+{
+    return gemm_w4_f16_nt(x, Q, S, Z, y, 1, N, K, group, stream);
+}
+
+int gemm_w4_f16_grouped_nt(const void* A, const void* Q, const void* S, const void* Z, void* C,
+                           const int* offsets, int T, int E, int N, int K, int group, void* stream)
+{
+    const int rc = validate_w4(N, K, group);
+    if (rc) return rc;
+    if (T < 0 || E < 0 || (int64_t)T * K > kW4MaxElems || (int64_t)T * N > kW4MaxElems) return GF_ERR_INVALID_ARG;
+    if (E > 0 && w4_bad(offsets, 4)) return GF_ERR_INVALID_ARG;
+    if (T == 0 || E == 0 || N == 0) return GF_OK;
+    if (w4_bad(C, 2)) return GF_ERR_INVALID_ARG;
+    // K == 0: the kernel never reads A, Q or S, and stores the empty sums of the groups' rows
+    if (K > 0 && (w4_bad(A, 2) || w4_bad(Q, 4) || w4_bad(S, 2))) return GF_ERR_INVALID_ARG;
+    W4Args a = {(const uint16_t*)A, (const uint32_t*)Q, (const uint16_t*)S, (const uint8_t*)Z, (uint16_t*)C,
+                0, N, K, ceil_div(K, group), {offsets, E, T}};
+    return product_by_group<true>(a, group, (hipStream_t)stream);
+}
+
+}  // extern "C"

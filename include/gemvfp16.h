@@ -342,6 +342,87 @@ int gf_sp_config_count(void);
 int gf_sp_config_get(int i, gf_sp_cfg* out);
 int gf_sp_default_config(int M, int N, int K, gf_sp_cfg* out);
 
+/*
+ * Products grouped by expert: the T rows of A and C are sorted by group, and
+ * group e (0 <= e < E) owns rows offsets[e] .. offsets[e + 1] - 1.  offsets:
+ * E + 1 ints in DEVICE memory (4-byte aligned), non-decreasing, within 0 .. T;
+ * a group may be empty.  The host never reads them, so the calls can follow a
+ * router's kernels on a stream, or be captured, without a synchronisation.
+ * Rows before offsets[0] and from offsets[E] on belong to no group and are
+ * left as they were.  Offsets that break the contract give unspecified values
+ * in C, but no access outside the operands.
+ * Every group's part of an operand, and each of A and C as a whole, must be
+ * smaller than 2^31 elements; B as a whole may be larger.  fp32 accumulation,
+ * one rounding at the end; a group's results do not depend on the other
+ * groups' rows or sizes except through the tile the library picks from T / E
+ * (the tile shapes add the same products in the same order).
+ *
+ * gemm_f16_grouped_nt: C[r] = A[r] . B[e]^T for the rows r of group e: A T x K,
+ * B E x N x K, C T x N, all fp16.  The forward product of an expert layer.
+ * gemm_f16_grouped_nn: C[r] = A[r] . B[e]: A T x K, B E x K x N, C T x N.  With
+ * A the gradient of the forward product's C and B its weights, the gradient of
+ * its A.
+ * gemm_f16_grouped_tn: C[e] = A_e^T . B_e, the sum over the rows of group e:
+ * A T x M, B T x N, C E x M x N, fp16 (c_f32 = 0) or float (c_f32 = 1).  With A
+ * the gradient of the forward product's C and B its A, the gradient of its
+ * weights.  Every group's C is written: an empty group gives +0 everywhere.
+ * K == 0 (or an empty group in the tn form) is the empty sum.  The fast path
+ * needs 16-byte aligned A, B, C and each operand's contiguous extent a multiple
+ * of 8 (N in the nt form excepted); anything else runs a masked path with the
+ * same result.
+ * GF_ERR_INVALID_ARG for negative sizes, NULL or misaligned pointers, operands
+ * past the limits, or c_f32 other than 0 or 1.
+ */
+int gemm_f16_grouped_nt(const void* A, const void* B, void* C, const int* offsets, int T, int E, int N,
+                        int K, void* stream);
+int gemm_f16_grouped_nn(const void* A, const void* B, void* C, const int* offsets, int T, int E, int N,
+                        int K, void* stream);
+int gemm_f16_grouped_tn(const void* A, const void* B, void* C, const int* offsets, int T, int E, int M,
+                        int N, int c_f32, void* stream);
+
+/*
+ * 4-bit weights.  A weight W (N x K) is held as
+ *  - Q: N x K/8 32-bit words; word j of a row holds the codes q of k = 8 j ..
+ *    8 j + 7, four bits each, the lowest k in the lowest bits;
+ *  - S: N x G fp16 scales, one for each group of `group` consecutive k (32, 64
+ *    or 128; G = ceil(K / group), the last group may be short);
+ *  - Z: N x G bytes, zero points 0 .. 15, or NULL for 8 everywhere;
+ * and stands for (q - z) * s.  K must be a multiple of 8.  Q is 4-byte
+ * aligned, the fp16 operands 2-byte.
+ *
+ * w4_quantize_f16: codes, scales and zero points of an fp16 W.  With Z, lo and
+ * hi the group's least and largest value and 0: s = fp16((hi - lo) / 15),
+ * z = min(15, rint(-lo / s)); without, s = fp16(max |w| / 7), z = 8.  Then
+ * q = clamp(rint(w / s) + z, 0, 15), the quotient exact and ties to even.
+ * s == 0 gives q = z (0 with Z).  A group that holds an infinity or a NaN gets
+ * s = NaN, so that products with it show it.  Bit-exact, deterministic.
+ * w4_dequantize_f16: W = fp16((q - z) * s), rounded once.
+ * Both take any N >= 0 and address by 64 bits: N may count the rows of several
+ * weights (E x N x K).
+ *
+ * gemm_w4_f16_nt: C = A . W^T with A M x K and C M x N fp16; gemv_w4_f16 is its
+ * single row, y = W . x.  Products a * (q - z) are summed in fp32 within a
+ * group, the groups' sums scaled and added in fp32, and each result rounded
+ * once to fp16: the weights themselves are not rounded.  Results repeat bit
+ * for bit from run to run.
+ * gemm_w4_f16_grouped_nt: gemm_f16_grouped_nt with 4-bit weights, Q E x N x
+ * K/8, S and Z E x N x G; offsets and rows as there.
+ * Entries of Z above 15 are outside the contract (no fault).  The fast path
+ * needs A and Q 16-byte aligned and K % 32 == 0.  M == 0 or N == 0 is a
+ * no-op; K == 0 writes +0.  Each operand (a group's part of Q) must stand for
+ * fewer than 2^31 elements.  GF_ERR_INVALID_ARG for K % 8 != 0, another group
+ * size, negative sizes, NULL or misaligned pointers, or sizes past the limit.
+ */
+int w4_quantize_f16(const void* W, void* Q, void* S, void* Z, int N, int K, int group, void* stream);
+int w4_dequantize_f16(const void* Q, const void* S, const void* Z, void* W, int N, int K, int group,
+                      void* stream);
+int gemm_w4_f16_nt(const void* A, const void* Q, const void* S, const void* Z, void* C, int M, int N, int K,
+                   int group, void* stream);
+int gemv_w4_f16(const void* Q, const void* S, const void* Z, const void* x, void* y, int N, int K, int group,
+                void* stream);
+int gemm_w4_f16_grouped_nt(const void* A, const void* Q, const void* S, const void* Z, void* C,
+                           const int* offsets, int T, int E, int N, int K, int group, void* stream);
+
 /* Static string naming a status code. */
 const char* gf_status_string(int status);
 
