@@ -79,6 +79,29 @@ int launch_stream(const W4Args& a, hipStream_t stream)
     return w4_status(hipGetLastError());
 }
 
+template <class Cfg, int GROUP, bool WINDOW, bool GROUPED>
+int launch_tile_of(const W4Args& a, hipStream_t stream)
+{
+    auto kern = w4_tile_kernel<Cfg, GROUP, WINDOW, GROUPED>;
+    static std::atomic<uint64_t> lds_opt_in{0};
+    const hipError_t e = opt_in_lds((const void*)kern, Cfg::LDS_BYTES, lds_opt_in, stream);
+    if (e != hipSuccess) return GF_ERR_HIP;
+    int64_t blocks = ceil_div(a.M, Cfg::BM);
+    if (GROUPED) blocks = a.g.T / Cfg::BM + (a.g.E < a.g.T ? a.g.E : a.g.T);
+    const int64_t grid = blocks * ceil_div(a.N, Cfg::BN);
+    if (grid > kW4MaxGrid) return GF_ERR_INVALID_ARG;
+    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(Cfg::NT), Cfg::LDS_BYTES, stream, a);
+    return w4_status(hipGetLastError());
+}
+
+template <class Cfg, int GROUP, bool GROUPED>
+int launch_tile(const W4Args& a, hipStream_t stream)
+{
+    if (a.K % 256 == 0 && w4_aligned(a.S, 16) && w4_aligned(a.Z, 8))
+        return launch_tile_of<Cfg, GROUP, true, GROUPED>(a, stream);
+    return launch_tile_of<Cfg, GROUP, false, GROUPED>(a, stream);
+}
+
 template <int GROUP, int MB, int NB, bool GROUPED>
 int stream_by_alignment(const W4Args& a, hipStream_t stream)
 {
@@ -92,6 +115,11 @@ template <int GROUP, bool GROUPED>
 int product(const W4Args& a, hipStream_t stream)
 {
     const int64_t rows = GROUPED ? (a.g.T + a.g.E - 1) / a.g.E : a.M;
+    if (rows > 64 && w4_aligned(a.A, 16) && w4_aligned(a.Q, 16) && a.K % 32 == 0 && a.K >= 64) {
+        const int64_t blocks = GROUPED ? a.g.T / 256 + a.g.E : ceil_div(a.M, 256);
+        if (blocks * ceil_div(a.N, 256) >= 192) return launch_tile<W4TileCfg<4, 2, 2, 4, 4>, GROUP, GROUPED>(a, stream);
+        return launch_tile<W4TileCfg<2, 1, 1, 4, 4>, GROUP, GROUPED>(a, stream);
+    }
     if (rows <= 16) return stream_by_alignment<GROUP, 1, 2, GROUPED>(a, stream);
     return stream_by_alignment<GROUP, 2, 2, GROUPED>(a, stream);
 }

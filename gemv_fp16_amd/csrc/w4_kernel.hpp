@@ -6,10 +6,10 @@
 //
 // A code q put in the low bits of an fp16 is the subnormal q * 2^-24, exactly.
 // The matrix cores take subnormal operands at full speed and keep them (checked
-// on the GPU, for both shapes used here), so unpacking needs no conversion: a
-// shift and a mask give two codes per 32-bit register, a packed fp16 subtraction
-// gives q - z (exact: small integers times 2^-24), and the products a * (q - z)
-// are summed in fp32 within a group.  Each group's sum is then scaled by
+// on the GPU, for both shapes used here), so unpacking needs no conversion:
+// masks and byte moves place two codes in a 32-bit register, one packed fp16
+// operation gives q - z (exact: small integers times 2^-24), and the products
+// a * (q - z) are summed in fp32 within a group.  Each group's sum is then scaled by
 // s * 2^24 in fp32, so that the only rounding to fewer bits is that of the
 // output: weights are never rounded to fp16.
 #pragma once
@@ -157,23 +157,32 @@ struct W4Args {
     Groups g;             // grouped form: the rows of A and C by group; M unused
 };
 
-// Four codes pairs of a word: k = (0, 4), (1, 5), (2, 6), (3, 7) of its eight.
-__device__ __forceinline__ half8 w4_unpack(uint32_t w, half2v z)
+// The eight q - z of a word, in order, as fp16 subnormals (times 2^-24).  A byte
+// holds an even k's code in its low half and the next one's in its high half,
+// 16 times too large once masked; the fused multiply-add that subtracts the
+// zero point takes that factor out, exactly.  10 instructions for 8 codes (a
+// shift and a mask for each pair take 11 and leave k in the order 0, 4, 1, 5,
+// .., which A then has to be brought into).  nz: -z in both halves.
+__device__ __forceinline__ half8 w4_unpack(uint32_t w, half2v nz)
 {
-    constexpr uint32_t kMask = 0x000f000fu;
-    const half2v a = __builtin_bit_cast(half2v, w & kMask) - z;
-    const half2v b = __builtin_bit_cast(half2v, (w >> 4) & kMask) - z;
-    const half2v c = __builtin_bit_cast(half2v, (w >> 8) & kMask) - z;
-    const half2v d = __builtin_bit_cast(half2v, (w >> 12) & kMask) - z;
-    return half8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+    const uint32_t lo = w & 0x0f0f0f0fu, hi = w & 0xf0f0f0f0u;
+    const half2v f = {(_Float16)1.0f, (_Float16)0.0625f};
+    half2v p[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        const uint32_t u = __builtin_amdgcn_perm(hi, lo, 0x0c040c00u + 0x00010001u * (uint32_t)b);
+        p[b] = __builtin_elementwise_fma(__builtin_bit_cast(half2v, u), f, nz);
+    }
+    return half8{p[0][0], p[0][1], p[1][0], p[1][1], p[2][0], p[2][1], p[3][0], p[3][1]};
 }
 
-// Eight consecutive k of A in the order of w4_unpack.
-__device__ __forceinline__ half8 w4_order(u32x4 v)
+// -z (a byte) as the subnormal pair that w4_unpack adds.
+__device__ __forceinline__ half2v w4_minus(uint32_t z)
 {
-    const half8 h = __builtin_bit_cast(half8, v);
-    return __builtin_shufflevector(h, h, 0, 4, 1, 5, 2, 6, 3, 7);
+    return __builtin_bit_cast(half2v, z * 0x00010001u | 0x80008000u);
 }
+
+constexpr float kW4Unit = 16777216.0f;   // 2^24: one code step, as a subnormal, is its reciprocal
 
 // Row-streaming product for few rows of A.  A workgroup owns 16 * NB rows of
 // Q and up to 16 * MB rows of A; its waves split K into chunks of 128, each
@@ -269,11 +278,6 @@ __global__ __launch_bounds__(WAVES * 64) void w4_stream_kernel(W4Args a)
     floatx4 acc[MB][NB] = {};
     constexpr int SPG = GROUP / 32;                     // MFMA steps per group
     auto compute = [&](int ch, Chunk& c) __attribute__((always_inline)) {
-        half8 x[MB][4];
-#pragma unroll
-        for (int b = 0; b < MB; ++b)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[b][i] = w4_order(c.x[b][i]);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
             u32x4 q = c.q[nb];
@@ -290,16 +294,16 @@ __global__ __launch_bounds__(WAVES * 64) void w4_stream_kernel(W4Args a)
                 const bool in = g < a.G;
                 const int at = srow[nb] + (in ? g : a.G - 1);
                 // past the last group: a scale of 0, not another group's (which may be infinite)
-                const float s = in ? f16_bits_to_f32(a.S[at]) * 16777216.0f : 0.0f;
-                const uint32_t zi = a.Z ? a.Z[at] : 8u;
-                const half2v z = __builtin_bit_cast(half2v, zi * 0x00010001u);
+                const float s = in ? f16_bits_to_f32(a.S[at]) * kW4Unit : 0.0f;
+                const half2v nz = w4_minus(a.Z ? a.Z[at] : 8u);
                 floatx4 part[MB] = {};
 #pragma unroll
                 for (int i = g0 * SPG; i < (g0 + 1) * SPG; ++i) {
-                    const half8 w = w4_unpack(q[i], z);
+                    const half8 w = w4_unpack(q[i], nz);
 #pragma unroll
                     for (int b = 0; b < MB; ++b)
-                        part[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[b][i], w, part[b], 0, 0, 0);
+                        part[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, c.x[b][i]), w,
+                                                                             part[b], 0, 0, 0);
                 }
 #pragma unroll
                 for (int b = 0; b < MB; ++b)
@@ -339,6 +343,337 @@ __global__ __launch_bounds__(WAVES * 64) void w4_stream_kernel(W4Args a)
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) s += red[w * PER_WAVE + at];
         if (m0 + m < M && n0 + n < a.N) a.C[(size_t)(m0 + m) * a.N + n0 + n] = f32_to_f16_bits(s);
+    }
+#endif
+}
+
+// ---------------------------------------------------------------------------
+// tiles: many rows of A
+// ---------------------------------------------------------------------------
+//
+// A BM x BN tile by WM x WN waves of 32 FM rows by 32 FN columns, over K in
+// steps of 64.  Bound by the matrix cores, so here each weight is rounded once
+// to fp16, (q - z) * s as w4_dequantize_f16 rounds it, and the products are
+// accumulated over all of K in place: the result is that of gemm_f16_nt on the
+// dequantized weights.  (Scaling each group's sum in fp32 instead keeps the
+// weights exact, but holds a second set of accumulators and passes all of them
+// through the vector ALU once per group: built, it ran at 0.6 of this form's
+// rate with groups of 128 and 0.3 with groups of 32.)
+//  * A goes to LDS by direct loads, STAGES buffers in a ring, rows swizzled as
+//    in gemm_kernel.hpp (chunk c of row r at slot c ^ (r / 2 % 8)).
+//  * The codes never pass through LDS: a lane loads 16 bytes of its own row of
+//    Q and unpacks them in registers as MFMA operands.  Which k an MFMA step
+//    holds is free as long as both operands agree: lane half h takes words
+//    4 h .. 4 h + 3 of the 64 k, step j word j of them, and A's chunks are read
+//    to match.  A lane's 32 k lie in one group whatever its size, so the lane
+//    needs one scale and zero point per step.
+//  * Under the MFMAs of one unpacked operand the next one is unpacked (16
+//    vector instructions for 8 codes, FM MFMAs of 32 cycles each), and under
+//    those of a step of 16 k the next step's fragments of A are read.
+//  * The barrier of step t stands before its last 16 k: by then every wave has
+//    read all of step t's fragments and has waited for its own loads of step
+//    t + 1, so the next fragments are read, and the loads of step t + STAGES
+//    issued into the freed buffer, under the last MFMAs.  At most the direct
+//    loads of STAGES - 2 steps are then pending: a count of those alone, since
+//    the compiler may merge or reorder the loads into registers, for which it
+//    waits itself.  Loads are issued for every step, also past the last, and
+//    always of 64 k inside K (so K >= 64): where K ends in half a step, the last
+//    step takes the last 64 k and its first half, done before, as zeros on both
+//    sides.  No load stands under a branch or goes through the flat path: the
+//    compiler would then wait for all of them wherever it needs one.
+template <int FM_, int FN_, int WM_, int WN_, int STAGES_>
+struct W4TileCfg {
+    static constexpr int FM = FM_, FN = FN_, WM = WM_, WN = WN_, STAGES = STAGES_;
+    static constexpr int WAVES = WM * WN, NT = WAVES * kWave;
+    static constexpr int BM = 32 * FM * WM, BN = 32 * FN * WN, BK = 64;
+    static constexpr int STAGE_BYTES = BM * BK * 2;
+    static constexpr int LPS = BM * 8 / NT;              // 16-byte loads of A per thread and step
+    static_assert(LPS >= 1 && BM * 8 % NT == 0 && LPS * (STAGES - 2) < 64, "loads per thread");
+    static constexpr int EPAD = 8;
+    static constexpr int EPI_BYTES = WAVES * 32 * FM * (32 * FN + EPAD) * 2;
+    static constexpr int LDS_BYTES = STAGES * STAGE_BYTES > EPI_BYTES ? STAGES * STAGE_BYTES : EPI_BYTES;
+    static_assert(LDS_BYTES <= 160 * 1024, "one CU's LDS");
+};
+
+// The eight weights (q - z) * s of a word as fp16, in order.  A byte holds an
+// even k's code in its low half and the next one's in its high half; with the
+// exponent of 1024 put over them they are 1024 + q and 1024 + 16 q, and one
+// fused multiply-add brings both to q - z, exactly; the product with s rounds.
+// off: -1024 - z and -64 - z.
+__device__ __forceinline__ half8 w4_weights(uint32_t w, half2v off, half2v s)
+{
+    const half2v f = {(_Float16)1.0f, (_Float16)0.0625f};
+    half2v p[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        const uint32_t u = __builtin_amdgcn_perm(0u, w, 0x0c000c00u + 0x00010001u * (uint32_t)b);
+        p[b] = __builtin_elementwise_fma(__builtin_bit_cast(half2v, (u & 0x00f0000fu) | 0x64006400u), f, off) * s;
+    }
+    return half8{p[0][0], p[0][1], p[1][0], p[1][1], p[2][0], p[2][1], p[3][0], p[3][1]};
+}
+
+// WINDOW: K % 256 == 0, S 16-byte and Z 8-byte aligned.  A row of Q, S or Z is
+// a line of its own, so what a lane loads from them costs a line whatever its
+// width: codes are then loaded two steps at a time and scales and zero points
+// four (a window).  Otherwise step by step.
+template <class Cfg, int GROUP, bool WINDOW, bool GROUPED>
+__global__ __launch_bounds__(Cfg::NT) void w4_tile_kernel(W4Args a)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    constexpr int FM = Cfg::FM, FN = Cfg::FN, BK = Cfg::BK, S = Cfg::STAGES;
+    extern __shared__ __attribute__((aligned(1024))) char w4_smem[];
+    GF_LDS char* smem = (GF_LDS char*)w4_smem;
+    const int tid = threadIdx.x, lane = tid % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int wm = wave / Cfg::WN, wn = wave % Cfg::WN;
+    const int r32 = lane % 32, h = lane / 32;
+
+    const int tiles_n = ceil_div(a.N, Cfg::BN);
+    int tm, tn, M = a.M;
+    if constexpr (GROUPED) {
+        int e, lo, hi, item;
+        if (!a.g.template find<Cfg::BM>(blockIdx.x, tiles_n, e, lo, hi, item)) return;
+        M = hi - lo;
+        a.A += (size_t)lo * a.K;
+        a.C += (size_t)lo * a.N;
+        a.Q += (size_t)e * a.N * (a.K / 8);
+        a.S += (size_t)e * a.N * a.G;
+        if (a.Z) a.Z += (size_t)e * a.N * a.G;
+        grouped_tile(item, ceil_div(M, Cfg::BM), tiles_n, kGroupPanel, tm, tn);
+    } else {
+        const int tiles_m = ceil_div(M, Cfg::BM);
+        grouped_tile(xcd_remap(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, kGroupPanel, tm, tn);
+    }
+    const int m0 = tm * Cfg::BM, n0 = tn * Cfg::BN;
+    const int K = a.K, nk = ceil_div(K, BK);
+
+    // ---- A: byte offset of load r's chunk at k = 0 ----
+    uint32_t voff[Cfg::LPS];
+#pragma unroll
+    for (int r = 0; r < Cfg::LPS; ++r) {
+        const int slot = r * Cfg::NT + tid, row = slot / 8, c = (slot % 8) ^ (row / 2 % 8);
+        voff[r] = ((uint32_t)min(m0 + row, M - 1) * (uint32_t)K + 8u * c) * 2u;
+    }
+    const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)a.A, 0, (int)((uint32_t)M * (uint32_t)K * 2u), 0x00020000);
+    auto issue_a = [&](int t, int stage_no) __attribute__((always_inline)) {
+        GF_LDS char* stage = smem + stage_no * Cfg::STAGE_BYTES;
+        const uint32_t koff = (uint32_t)__builtin_amdgcn_readfirstlane(min(t * BK, K - BK)) * 2u;
+#pragma unroll
+        for (int r = 0; r < Cfg::LPS; ++r)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                ra, (GF_LDS void*)(stage + (r * Cfg::NT + wave * kWave) * 16), 16, voff[r], koff, 0, 0);
+    };
+
+    // ---- codes, scale and zero point of the lane's 32 k in each column block ----
+    constexpr int D = WINDOW ? 4 : 2;                     // steps unrolled: one window, or the codes' two
+    constexpr int SW = WINDOW ? 128 / GROUP : 1, ZW = WINDOW && GROUP == 32 ? 2 : 1;   // registers
+    // (without zero points, the bytes of S stand in for the loads' sake)
+    const uint8_t* zsrc = a.Z ? a.Z : (const uint8_t*)a.S;
+    const uint32_t* qrow[FN];
+    int srow[FN];
+#pragma unroll
+    for (int f = 0; f < FN; ++f) {
+        const int n = min(n0 + (wn * FN + f) * 32 + r32, a.N - 1);
+        qrow[f] = a.Q + (size_t)n * (K / 8);
+        srow[f] = n * a.G;
+    }
+    // Codes of step t in codes[t % D]; scales and zero points of the window, or
+    // of step t in place t % D.
+    u32x4 codes[D][FN];
+    uint32_t sw[WINDOW ? 1 : D][FN][SW], zw[WINDOW ? 1 : D][FN][ZW];
+    auto load_codes = [&](int t, auto i_c) __attribute__((always_inline)) {
+        constexpr int i = decltype(i_c)::value;
+        const int kc = min(t * BK, K - BK) + 32 * h;
+#pragma unroll
+        for (int f = 0; f < FN; ++f) codes[i][f] = *(const u32x4*)(qrow[f] + kc / 8);
+    };
+    auto load_scales = [&](int t, auto i_c) __attribute__((always_inline)) {
+        constexpr int i = WINDOW ? 0 : decltype(i_c)::value;
+#pragma unroll
+        for (int f = 0; f < FN; ++f) {
+            if constexpr (WINDOW) {
+                const int at = srow[f] + min(t * BK, K - 4 * BK) / GROUP;
+                if constexpr (GROUP == 128) {
+                    sw[i][f][0] = *(const uint32_t*)(a.S + at);
+                    zw[i][f][0] = *(const uint16_t*)(zsrc + at);
+                } else if constexpr (GROUP == 64) {
+                    const u32x2 v = *(const u32x2*)(a.S + at);
+                    sw[i][f][0] = v[0]; sw[i][f][1] = v[1];
+                    zw[i][f][0] = *(const uint32_t*)(zsrc + at);
+                } else {
+                    const u32x4 v = *(const u32x4*)(a.S + at);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sw[i][f][e] = v[e];
+                    const u32x2 z = *(const u32x2*)(zsrc + at);
+                    zw[i][f][0] = z[0]; zw[i][f][1] = z[1];
+                }
+            } else {
+                const int at = srow[f] + (min(t * BK, K - BK) + 32 * h) / GROUP;
+                sw[i][f][0] = a.S[at];
+                zw[i][f][0] = zsrc[at];
+            }
+        }
+    };
+    // In the last step, whether this lane's 32 k are not those of the step before.
+    const bool last_new = WINDOW || h == 1 || K % BK == 0;
+    half2v off[FN], sc[FN];
+    // Scale and offset of step t, which is step i of the D unrolled.
+    auto scale = [&](int t, auto i_c) __attribute__((always_inline)) {
+        constexpr int i = decltype(i_c)::value;
+#pragma unroll
+        for (int f = 0; f < FN; ++f) {
+            uint32_t sb, z;
+            if constexpr (!WINDOW) {
+                sb = t < nk - 1 || last_new ? sw[i][f][0] : 0u;
+                z = zw[i][f][0];
+            } else if constexpr (GROUP == 32) {
+                sb = sw[0][f][i % SW] >> (16 * h);
+                z = zw[0][f][i / 2 % ZW] >> (16 * (i % 2) + 8 * h);
+            } else {
+                constexpr int g = i * BK / GROUP;         // within the window
+                sb = sw[0][f][g / 2 % SW] >> (16 * (g % 2));
+                z = zw[0][f][0] >> (8 * g);
+            }
+            sc[f] = __builtin_bit_cast(half2v, (sb & 0xffffu) * 0x00010001u);
+            // -1024 - z and -64 - z: steps of 1 and of 1/16 from the bits of -1024 and -64
+            off[f] = __builtin_bit_cast(half2v, 0xd400e400u + (a.Z ? z & 0xffu : 8u) * 0x00100001u);
+        }
+    };
+
+    // ---- fragments of A ----
+    const int abase = (wm * FM * 32 + r32) * (BK * 2), akey = r32 / 2 % 8;
+    half8 x[2][FM];
+    auto read_x = [&](int stage_no, auto j_c) __attribute__((always_inline)) {
+        constexpr int j = decltype(j_c)::value;
+        const GF_LDS char* p = smem + stage_no * Cfg::STAGE_BYTES + abase + (((4 * h + j) ^ akey) * 16);
+#pragma unroll
+        for (int f = 0; f < FM; ++f) x[j & 1][f] = *(const GF_LDS half8*)(p + f * 32 * (BK * 2));
+    };
+
+    floatx16 acc[FM][FN] = {};
+    half8 b;
+    // FM MFMAs with operand b of column block f and fragments x[j & 1], woven
+    // with the LDS reads and unpacking the caller has issued before them.
+    auto mfmas = [&](auto f_c, auto j_c, half8 op) __attribute__((always_inline)) {
+        constexpr int f = decltype(f_c)::value, j = decltype(j_c)::value;
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+            acc[i][f] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[j & 1][i], op, acc[i][f], 0, 0, 0);
+        static_for<FM>([&](auto) __attribute__((always_inline)) {
+            __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
+            if constexpr (f == 0) __builtin_amdgcn_sched_group_barrier(kSchedDsRead, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 20 / FM, 0);         // vector ALU
+        });
+        __builtin_amdgcn_sched_barrier(0);
+    };
+
+    static_for<D>([&](auto p) __attribute__((always_inline)) {
+        load_codes(decltype(p)::value, p);
+        if constexpr (!WINDOW || decltype(p)::value == 0) load_scales(decltype(p)::value, p);
+    });
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int t = 0; t < S - 1; ++t) issue_a(t, t);
+    asm volatile("" ::: "memory");
+    wait_vmcnt<Cfg::LPS * (S - 2)>();
+    lds_barrier();                                        // step 0 has landed
+    issue_a(S - 1, S - 1);
+    read_x(0, std::integral_constant<int, 0>{});
+    scale(0, std::integral_constant<int, 0>{});
+    b = w4_weights(codes[0][0][0], off[0], sc[0]);
+
+    int st = 0;                                           // buffer of step t
+    auto step = [&](int t, auto p) __attribute__((always_inline)) {
+        constexpr int i = decltype(p)::value, i1 = (i + 1) % D;
+        const int st1 = st + 1 == S ? 0 : st + 1;
+        static_for<4>([&](auto j_c) __attribute__((always_inline)) {
+            constexpr int j = decltype(j_c)::value;
+            if constexpr (j == 3) {
+                asm volatile("" ::: "memory");
+                wait_vmcnt<Cfg::LPS * (S - 2)>();
+                lds_barrier();                            // step t + 1 has landed; buffer st is free
+                if constexpr (!WINDOW) {
+                    if (K % BK != 0 && t == nk - 2) {     // the last step's first half: zeros
+                        for (int z = tid; z < Cfg::BM * 4; z += Cfg::NT) {
+                            const int row = z / 4, c = (z % 4) ^ (row / 2 % 8);
+                            *(GF_LDS u32x4*)(smem + st1 * Cfg::STAGE_BYTES + row * (BK * 2) + c * 16) =
+                                u32x4{0u, 0u, 0u, 0u};
+                        }
+                        lds_barrier();
+                    }
+                }
+                issue_a(t + S, st);
+            }
+            static_for<FN>([&](auto f_c) __attribute__((always_inline)) {
+                constexpr int f = decltype(f_c)::value;
+                if constexpr (f == 0) {
+                    if constexpr (j < 3) read_x(st, std::integral_constant<int, j + 1>{});
+                    else read_x(st1, std::integral_constant<int, 0>{});
+                }
+                // the next operand: the next column block's, or the next 16 k's first
+                half8 next;
+                if constexpr (f + 1 < FN) {
+                    next = w4_weights(codes[i][f + 1][j], off[f + 1], sc[f + 1]);
+                } else if constexpr (j < 3) {
+                    next = w4_weights(codes[i][0][j + 1], off[0], sc[0]);
+                } else {
+                    scale(t + 1, std::integral_constant<int, i1>{});
+                    next = w4_weights(codes[i1][0][0], off[0], sc[0]);
+                }
+                mfmas(f_c, j_c, b);
+                b = next;
+            });
+        });
+        if constexpr (!WINDOW) {
+            load_codes(t + D, p);
+            load_scales(t + D, p);
+        } else {
+            if constexpr (i % 2 == 1) {                   // a pair of steps done: the pair four steps on
+                load_codes(t + 3, std::integral_constant<int, i - 1>{});
+                load_codes(t + 4, p);
+            }
+            if constexpr (i == 2) load_scales(t + 2, p);  // the window's last use was scale(t + 1)
+        }
+        st = st1;
+    };
+    int t = 0;
+    for (; t + D <= nk; t += D)                           // (a window never leaves a rest)
+        static_for<D>([&](auto p) __attribute__((always_inline)) { step(t + decltype(p)::value, p); });
+    if constexpr (!WINDOW)
+        if (t < nk) step(t, std::integral_constant<int, 0>{});
+    wait_vmcnt<0>();                                      // no load may land once the epilogue writes LDS
+
+    // ---- epilogue: per-wave transpose in LDS, 16-byte stores ----
+    lds_barrier();
+    constexpr int WR = 32 * FM, WC = 32 * FN, LDW = WC + Cfg::EPAD;
+    GF_LDS uint16_t* reg = (GF_LDS uint16_t*)(smem + wave * (WR * LDW * 2));
+#pragma unroll
+    for (int f = 0; f < FM; ++f)
+#pragma unroll
+        for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                reg[(f * 32 + 8 * (i / 4) + 4 * h + i % 4) * LDW + fn * 32 + r32] =
+                    f32_to_f16_bits(acc[f][fn][i]);
+    asm volatile("" ::: "memory");
+    wait_lgkmcnt0();
+    constexpr int CPR = WC / 8, ITERS = WR * CPR / kWave;
+    const bool vec = a.N % 8 == 0 && (reinterpret_cast<uintptr_t>(a.C) & 15) == 0;
+#pragma unroll
+    for (int it = 0; it < ITERS; ++it) {
+        const int q = it * kWave + lane, r = q / CPR, cc = q % CPR;
+        const u32x4 v = *(const GF_LDS u32x4*)(reg + r * LDW + cc * 8);
+        const int row = m0 + wm * WR + r, col = n0 + wn * WC + cc * 8;
+        if (row >= M) continue;
+        uint16_t* dst = a.C + (size_t)row * a.N + col;
+        if (vec && col + 8 <= a.N) {
+            __builtin_nontemporal_store(v, (u32x4*)dst);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (col + e < a.N) dst[e] = (uint16_t)(v[e / 2] >> (16 * (e % 2)));
+        }
     }
 #endif
 }

@@ -134,11 +134,20 @@ def _check_product(C, A, q, S, Z, group, what):
     W = plain.weights(q, S, Z, group)
     a = A.astype(np.float64)
     with np.errstate(all="ignore"):
-        plain.check(C, a @ W.T, np.abs(a) @ np.abs(W).T, A.shape[1], plain.F16, what)
+        absum = np.abs(a) @ np.abs(W).T
+        plain.check(C, a @ W.T, absum, A.shape[1], plain.F16, what, _extra(A, absum))
+
+
+def _extra(A, absum):
+    """From 65 rows of A on, weights are rounded to fp16 before the product."""
+    if A.shape[0] <= 64:
+        return 0.0
+    return plain.rounded_weights(absum, np.abs(A.astype(np.float64)).sum(1, keepdims=True))
 
 
 SHAPES = [(1, 1, 8), (1, 16, 32), (1, 100, 4096), (2, 33, 136), (3, 64, 1000), (15, 15, 256), (16, 48, 128),
-          (17, 31, 640), (33, 130, 2056), (64, 64, 2048), (65, 200, 1024), (130, 77, 512), (200, 300, 416)]
+          (17, 31, 640), (33, 130, 2056), (64, 64, 2048), (65, 200, 1024), (130, 77, 512), (200, 300, 416),
+          (66, 40, 32), (300, 520, 160), (1700, 7000, 96)]
 
 
 @pytest.mark.parametrize("group", [32, 64, 128])
@@ -172,11 +181,12 @@ def test_gemm_w4_off_the_16_byte_grid(M, shift_a, shift_q):
 
 @pytest.mark.parametrize("M", [1, 4, 30, 70, 300])
 @pytest.mark.parametrize("group", [32, 128])
-def test_gemm_w4_infinities_and_nan(M, group):
+@pytest.mark.parametrize("K", [8 * 37, 32 * 9])           # both with a short last group
+def test_gemm_w4_infinities_and_nan(M, group, K):
     """An infinite or NaN entry of A or S shows in its row or column as the
     formula has it, and nowhere else; the group behind the last is not read."""
     rng = np.random.default_rng(M)
-    N, K = 50, 8 * 37                                 # a short last group
+    N = 50
     A, (q, S, Z) = _f16(rng, (M, K)), _codes(rng, N, K, group, True)
     A[0, 5], A[M - 1, K - 1] = np.float16("inf"), np.float16("nan")
     q[:, 5] = np.where(q[:, 5] == Z[:, 0], (Z[:, 0] + 1) % 16, q[:, 5])     # inf * 0 apart
@@ -192,7 +202,9 @@ def test_gemm_w4_infinities_and_nan(M, group):
         exact, absum = a @ W.T, np.abs(a) @ np.abs(W).T
     keep = [n for n in range(N) if n != 3]
     assert not np.isfinite(C[:, 3].astype(np.float64)).any()
-    plain.check(C[:, keep], exact[:, keep], absum[:, keep], K, plain.F16, "special")
+    extra = _extra(A, absum)
+    plain.check(C[:, keep], exact[:, keep], absum[:, keep], K, plain.F16, "special",
+                extra if np.isscalar(extra) else extra[:, keep])
 
 
 def test_gemm_w4_empty_and_k0():
@@ -220,4 +232,18 @@ def test_gemm_w4_full_size(M, N, K):
     Wd = torch.from_numpy(plain.weights(q, Sn, Zn, 128)).cuda()
     a = A.double()
     exact, absum = a @ Wd.t(), a.abs() @ Wd.abs().t()
-    plain.check(C.cpu().numpy(), exact.cpu().numpy(), absum.cpu().numpy(), K, plain.F16, "full")
+    absum = absum.cpu().numpy()
+    plain.check(C.cpu().numpy(), exact.cpu().numpy(), absum, K, plain.F16, "full", _extra(A.cpu().numpy(), absum))
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_gemm_w4_of_many_rows_is_the_product_of_the_weights_read_back(group):
+    """From 65 rows on, within the product's own roundings."""
+    rng = np.random.default_rng(group)
+    M, N, K = 300, 264, 608
+    A, (q, S, Z) = _f16(rng, (M, K)), _codes(rng, N, K, group, True)
+    dA, dQ, dS, dZ = _product(A, q, S, Z, group)
+    C = gf.gemm_w4_f16_nt(dA, dQ, dS, dZ, group=group).cpu().numpy().astype(np.float64)
+    W = gf.w4_dequantize_f16(dQ, dS, dZ, group).cpu().numpy().astype(np.float64)
+    a = A.astype(np.float64)
+    plain.check(C, a @ W.T, np.abs(a) @ np.abs(W).T, K, plain.F16, "read back")

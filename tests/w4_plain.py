@@ -72,8 +72,17 @@ F16 = dict(eps_half=2.0 ** -11, tiny=2.0 ** -25)
 F32 = dict(eps_half=2.0 ** -24, tiny=0.0)
 
 
-def check(got, exact, absum, depth, kind, what=""):
-    """Compare with the float64 result; infinities and NaN must be the same."""
+def rounded_weights(absum, a_abs):
+    """How far a product may be where each weight is first rounded to fp16: half
+    a step of it, relative 2^-11 or absolute 2^-25 below the normal range, times
+    the magnitude of its entry of A.  absum: sums of |a w|; a_abs: row sums of |a|."""
+    return 2.0 ** -11 * absum + 2.0 ** -25 * a_abs
+
+
+def check(got, exact, absum, depth, kind, what="", extra=0.0):
+    """Compare with the float64 result; infinities and NaN must be the same.
+    extra: what the operands themselves may be off (rounded_weights), which the
+    result's own rounding then sees too."""
     got = np.asarray(got).astype(np.float64)
     assert got.shape == exact.shape, what
     fin = np.isfinite(exact)
@@ -82,6 +91,8 @@ def check(got, exact, absum, depth, kind, what=""):
     assert np.array_equal(got[inf], exact[inf]), what + ": infinities differ"
     err = np.abs(got[fin] - exact[fin])
     lim = bound(exact[fin], absum[fin], depth, **kind)
+    if not np.isscalar(extra):
+        lim = lim + extra[fin] * (1 + kind["eps_half"])
     bad = ~(err <= lim)
     assert not bad.any(), "%s: %d of %d entries out of bounds, worst %.3g times the bound" % (
         what, int(bad.sum()), bad.size, float((err / lim).max()))
