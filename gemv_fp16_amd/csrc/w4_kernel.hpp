@@ -347,6 +347,490 @@ __global__ __launch_bounds__(WAVES * 64) void w4_stream_kernel(W4Args a)
 #endif
 }
 
+// The same product where rows of Q, S and Z can be read in wide pieces: K % 256
+// == 0, A and Q 16-byte, S 16-byte and Z 8-byte aligned.
+// What bounds it is not only the bytes: each row that a load touches is a cache
+// line of its own, and a line costs its cycle whether 2 or 64 bytes of it are
+// used.  So the waves take K in blocks of CB chunks of 128 (block b goes to wave
+// b % WAVES), and load a block's scales and zero points with one instruction
+// each; the next block is in flight while one is multiplied.  XLDS: A (few rows,
+// read by every wave through LDS) is copied there once, rows padded by 16 bytes;
+// otherwise each wave loads its own chunks of A one chunk ahead.
+template <int GROUP_, int MB_, int NB_, int WAVES_, int CB_, bool XLDS_>
+struct W4RowsCfg {
+    static constexpr int GROUP = GROUP_, MB = MB_, NB = NB_, WAVES = WAVES_, CB = CB_;
+    static constexpr bool XLDS = XLDS_;
+    static constexpr int BK = 128 * CB;                  // k per block
+    static constexpr int SW = BK / GROUP / 2;            // registers of a block's scales
+    static constexpr int ZW = (BK / GROUP + 3) / 4;      // and zero points
+    static constexpr int RED_BYTES = WAVES * MB * NB * 256 * 4;
+    static constexpr int XPAD = 8;                       // fp16 between rows of A in LDS
+};
+
+// N consecutive 32-bit words (N = 1, 2, 4 or 8), or a 16-bit one for N = 0.
+template <int N>
+__device__ __forceinline__ void load_words(const void* p, uint32_t* v)
+{
+    if constexpr (N == 0) {
+        v[0] = *(const uint16_t*)p;
+    } else if constexpr (N == 1) {
+        v[0] = *(const uint32_t*)p;
+    } else if constexpr (N == 2) {
+        const u32x2 t = *(const u32x2*)p;
+        v[0] = t[0]; v[1] = t[1];
+    } else {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            const u32x4 t = ((const u32x4*)p)[i];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[4 * i + e] = t[e];
+        }
+    }
+}
+
+template <class Cfg, bool GROUPED>
+__global__ __launch_bounds__(Cfg::WAVES * 64) void w4_rows_kernel(W4Args a)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    constexpr int GROUP = Cfg::GROUP, MB = Cfg::MB, NB = Cfg::NB, WAVES = Cfg::WAVES, CB = Cfg::CB;
+    constexpr int GPB = Cfg::BK / GROUP;                 // groups per block
+    extern __shared__ __attribute__((aligned(16))) char w4_smem[];
+    GF_LDS float* red = (GF_LDS float*)w4_smem;
+    GF_LDS char* xs = (GF_LDS char*)w4_smem + Cfg::RED_BYTES;
+
+    const int lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int r16 = lane % 16, c4 = lane / 16;
+    const int tiles_n = ceil_div(a.N, 16 * NB);
+    int tm, tn, M = a.M;
+    if constexpr (GROUPED) {
+        int e, lo, hi, item;
+        if (!a.g.template find<16 * MB>(blockIdx.x, tiles_n, e, lo, hi, item)) return;
+        M = hi - lo;
+        a.A += (size_t)lo * a.K;
+        a.C += (size_t)lo * a.N;
+        a.Q += (size_t)e * a.N * (a.K / 8);
+        a.S += (size_t)e * a.N * a.G;
+        if (a.Z) a.Z += (size_t)e * a.N * a.G;
+        tm = item % ceil_div(M, 16 * MB);
+        tn = item / ceil_div(M, 16 * MB);
+    } else {
+        tm = blockIdx.x / tiles_n;
+        tn = blockIdx.x % tiles_n;
+    }
+    const int m0 = tm * 16 * MB, n0 = tn * 16 * NB;
+    const int K = a.K, nblk = K / Cfg::BK;
+
+    const uint32_t* qrow[NB];
+    int srow[NB];
+    const uint8_t* zsrc = a.Z ? a.Z : (const uint8_t*)a.S;   // without zero points: some bytes to load
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const int n = min(n0 + 16 * b + r16, a.N - 1);
+        qrow[b] = a.Q + (size_t)n * (K / 8) + c4 * 4;
+        srow[b] = n * a.G;
+    }
+    struct Block {
+        u32x4 q[CB][NB];
+        uint32_t s[NB][Cfg::SW], z[NB][Cfg::ZW];
+    };
+    auto load = [&](int blk, Block& v) __attribute__((always_inline)) {
+#pragma unroll
+        for (int c = 0; c < CB; ++c)
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+                v.q[c][b] = __builtin_nontemporal_load((const u32x4*)(qrow[b] + (blk * CB + c) * 16));
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            load_words<Cfg::SW>(a.S + srow[b] + blk * GPB, v.s[b]);
+            load_words<GPB / 4>(zsrc + srow[b] + blk * GPB, v.z[b]);
+        }
+    };
+
+    // A: chunk ch's four fragments (step i: word i of each lane's 32 k with
+    // groups of 128, else k = 32 i .. 32 i + 31)
+    const int koff = GROUP == 128 ? 32 * c4 : 8 * c4;
+    constexpr int kstep = GROUP == 128 ? 8 : 32;
+    const uint16_t* arow[MB];
+#pragma unroll
+    for (int b = 0; b < MB; ++b) arow[b] = a.A + (size_t)min(m0 + 16 * b + r16, M - 1) * K + koff;
+    const GF_LDS char* xrow = xs + min(r16, M - 1) * (K + Cfg::XPAD) * 2 + koff * 2;
+    half8 x[MB][4];
+    auto load_x = [&](int ch, half8 (&v)[MB][4]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int b = 0; b < MB; ++b) {
+                if constexpr (Cfg::XLDS) v[b][i] = *(const GF_LDS half8*)(xrow + (ch * 128 + kstep * i) * 2);
+                else v[b][i] = *(const half8*)(arow[b] + ch * 128 + kstep * i);
+            }
+    };
+
+    floatx4 acc[MB][NB] = {};
+    constexpr int SPG = GROUP / 32, GPC = 128 / GROUP;   // MFMA steps per group, groups per chunk
+    auto multiply = [&](const Block& v, auto c_c) __attribute__((always_inline)) {
+        constexpr int c = decltype(c_c)::value;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            u32x4 q = v.q[c][nb];
+            if constexpr (GROUP < 128) {
+                const u32x2 p = __builtin_amdgcn_permlane32_swap(q[0], q[2], false, false);
+                const u32x2 r = __builtin_amdgcn_permlane32_swap(q[1], q[3], false, false);
+                const u32x2 s = __builtin_amdgcn_permlane16_swap(p[0], r[0], false, false);
+                const u32x2 t = __builtin_amdgcn_permlane16_swap(p[1], r[1], false, false);
+                q = u32x4{s[0], s[1], t[0], t[1]};
+            }
+#pragma unroll
+            for (int g0 = 0; g0 < GPC; ++g0) {
+                const int g = c * GPC + g0;              // within the block
+                const uint16_t sb = (uint16_t)(v.s[nb][g / 2] >> (16 * (g % 2)));
+                const float s = f16_bits_to_f32(sb) * kW4Unit;
+                const half2v nz = w4_minus(a.Z ? (v.z[nb][g / 4] >> (8 * (g % 4))) & 0xffu : 8u);
+                floatx4 part[MB] = {};
+#pragma unroll
+                for (int i = g0 * SPG; i < (g0 + 1) * SPG; ++i) {
+                    const half8 w = w4_unpack(q[i], nz);
+#pragma unroll
+                    for (int b = 0; b < MB; ++b)
+                        part[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[b][i], w, part[b], 0, 0, 0);
+                }
+#pragma unroll
+                for (int b = 0; b < MB; ++b)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[b][nb][i] = fmaf(part[b][i], s, acc[b][nb][i]);
+            }
+        }
+    };
+
+    // Blocks are loaded for a clamped number past the wave's last one, so that
+    // no load stands under a branch.
+    Block v0, v1;
+    const int last = nblk - 1;
+    load(min(wave, last), v0);
+    if constexpr (Cfg::XLDS) {
+        const int per = K / 8, n = M * per;
+        for (int t = threadIdx.x; t < n; t += WAVES * 64) {
+            const int m = t / per, j = t - m * per;
+            *(GF_LDS u32x4*)(xs + m * (K + Cfg::XPAD) * 2 + j * 16) = *(const u32x4*)(a.A + (size_t)m * K + j * 8);
+        }
+        __syncthreads();
+    } else {
+        load_x(min(wave, last) * CB, x);
+    }
+    auto block = [&](int blk, const Block& v) __attribute__((always_inline)) {
+        static_for<CB>([&](auto c_c) __attribute__((always_inline)) {
+            constexpr int c = decltype(c_c)::value;
+            if constexpr (Cfg::XLDS) {
+                load_x(blk * CB + c, x);
+                multiply(v, c_c);
+            } else {
+                half8 next[MB][4];
+                load_x(c + 1 < CB ? blk * CB + c + 1 : min(blk + WAVES, last) * CB, next);
+                multiply(v, c_c);
+#pragma unroll
+                for (int b = 0; b < MB; ++b)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[b][i] = next[b][i];
+            }
+        });
+    };
+    int blk = wave;
+    for (; blk + WAVES <= last; blk += 2 * WAVES) {
+        load(blk + WAVES, v1);
+        block(blk, v0);
+        load(min(blk + 2 * WAVES, last), v0);
+        block(blk + WAVES, v1);
+    }
+    if (blk <= last) block(blk, v0);
+
+    // ---- the waves' sums, in wave order ----
+    constexpr int PER_WAVE = MB * NB * 256;             // floats
+#pragma unroll
+    for (int b = 0; b < MB; ++b)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                red[wave * PER_WAVE + ((b * NB + nb) * 4 + i) * 64 + lane] = acc[b][nb][i];
+    __syncthreads();
+    const int rows = min(16 * MB, M - m0);              // no thread for rows past M
+    for (int t = threadIdx.x; t < rows * 16 * NB; t += WAVES * 64) {
+        const int n = t % (16 * NB), m = t / (16 * NB);            // within the tile
+        const int at = (((m / 16) * NB + n / 16) * 4 + m % 4) * 64 + (m % 16) / 4 * 16 + n % 16;
+        float s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) s += red[w * PER_WAVE + at];
+        if (n0 + n < a.N) a.C[(size_t)(m0 + m) * a.N + n0 + n] = f32_to_f16_bits(s);
+    }
+#endif
+}
+
+// The same product through LDS: K % 512 == 0, N >= 16 and the alignments above.
+// Streaming wants whole cache lines: 33.5 MB of codes read as 16 rows x 64 bytes
+// an instruction take 8.7 us, as whole lines (4 rows x 256 bytes) 6.2 us.  MFMA
+// operands want the former.  So codes, scales and zero points go to LDS by
+// direct loads that read lines, and each wave reads its operands from there: no
+// registers are spent on loads in flight, and no wave waits for another's.
+// The waves split K; a wave's tasks are its blocks of 512 k of one row group
+// after the other (row groups of 16, walked grid-stride), `ring` tasks in flight.
+// The last group takes the last 16 rows, some of them a second time, so that no
+// address needs a bound.
+// A task's buffer: 16 rows of 16 chunks of 16 bytes, chunk c of row n at slot
+// c ^ n (so that the 16 rows read together lie in different banks), then the
+// scales and zero points as 32-bit words, word j of row n at 16 j + n.
+// Each row group ends in one barrier; the sums' slots alternate.
+// XB == 0: A is copied to LDS once (chunk c of row m at slot c ^ m % 8);
+// otherwise each wave keeps its part of up to 16 * MB rows of A in registers, XB
+// blocks' worth.  Grouped: workgroup p of `parts` of expert e walks that expert's
+// row groups, once for every 16 * MB of its rows of A.
+// What is left is the vector ALU's work, so it is kept short: a task's addresses
+// are one scalar offset, a scale multiplies straight from its half of a word
+// (acc is in units of 2^-24 until the end), and a word unpacks in 10
+// instructions, or 9 where A's registers hold k in the order 0, 4, 1, 5, ...
+template <int GROUP_, int MB_, int XB_>
+struct W4BandCfg {
+    static constexpr int GROUP = GROUP_, MB = MB_, XB = XB_, WAVES = 8, BK = 512;
+    static constexpr bool XLDS = XB == 0;
+    static constexpr int SWORDS = BK / GROUP / 2, ZWORDS = BK / GROUP / 4;   // per row
+    // direct loads of a task: 4 of codes, then scales and zero points, which
+    // share one instruction where 16 rows of both fit its 64 lanes
+    static constexpr int SLOADS = GROUP == 128 ? 1 : SWORDS / 4, ZLOADS = GROUP == 128 ? 0 : 1;
+    static constexpr int LOADS = 4 + SLOADS + ZLOADS;
+    static constexpr int TASK_BYTES = 4096 + (SLOADS + ZLOADS) * 256;
+    static constexpr int MAX_RING = 4;
+};
+
+// w4_unpack's values in the order 0, 4, 1, 5, 2, 6, 3, 7.
+__device__ __forceinline__ half8 w4_unpack_pairs(uint32_t w, half2v nz)
+{
+    constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u;
+    const half2v f = {(_Float16)0.0625f, (_Float16)0.0625f};
+    const uint32_t v = w >> 8;
+    const half2v p0 = __builtin_bit_cast(half2v, w & kLo) + nz;
+    const half2v p1 = __builtin_elementwise_fma(__builtin_bit_cast(half2v, w & kHi), f, nz);
+    const half2v p2 = __builtin_bit_cast(half2v, v & kLo) + nz;
+    const half2v p3 = __builtin_elementwise_fma(__builtin_bit_cast(half2v, v & kHi), f, nz);
+    return half8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+}
+
+template <class Cfg, bool GROUPED>
+__global__ __launch_bounds__(Cfg::WAVES * 64) void w4_band_kernel(W4Args a, int ring, int parts)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    constexpr int GROUP = Cfg::GROUP, MB = Cfg::MB, WAVES = Cfg::WAVES, L = Cfg::LOADS;
+    constexpr int GPB = Cfg::BK / GROUP;                  // groups per block
+    extern __shared__ __attribute__((aligned(1024))) char w4_smem[];
+    const int lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int r16 = lane % 16, c4 = lane / 16;
+    const int N = a.N, K = a.K, G = a.G;
+
+    int part = blockIdx.x, rows = a.M;                    // of A, in all
+    if constexpr (GROUPED) {
+        const int e = part / parts;
+        part -= e * parts;
+        int lo, hi;
+        a.g.rows(e, lo, hi);
+        rows = __builtin_amdgcn_readfirstlane(hi - lo);
+        if (rows == 0) return;
+        a.A += (size_t)lo * K;
+        a.C += (size_t)lo * N;
+        a.Q += (size_t)e * N * (K / 8);
+        a.S += (size_t)e * N * G;
+        if (a.Z) a.Z += (size_t)e * N * G;
+    }
+    constexpr int MR = 16 * MB;                           // rows of A in one pass
+    const int red_rows = GROUPED ? MR : a.M;
+    GF_LDS char* tasks = (GF_LDS char*)w4_smem + wave * ring * Cfg::TASK_BYTES;
+    GF_LDS float* red = (GF_LDS float*)((GF_LDS char*)w4_smem + WAVES * ring * Cfg::TASK_BYTES);
+    GF_LDS char* xs = (GF_LDS char*)(red + 2 * WAVES * red_rows * 16);
+
+    const int nblk = K / Cfg::BK;
+    const int b0 = wave * nblk / WAVES, nb = (wave + 1) * nblk / WAVES - b0;   // this wave's blocks
+    const int groups = ceil_div(N, 16);
+    const int ng = (groups - part + parts - 1) / parts;   // row groups of this workgroup
+
+    // ---- per-lane offsets of a task's direct loads, and its operands in LDS ----
+    uint32_t qoff[4], qat[4], xat[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 4 * i + c4;
+        qoff[i] = (uint32_t)r * (uint32_t)(K / 2) + (uint32_t)(r16 ^ r) * 16u;
+        qat[i] = (uint32_t)(r16 * 256 + (((4 * i + c4) ^ r16) * 16));
+    }
+    const __amdgpu_buffer_rsrc_t rq = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)a.Q, 0, (int)((uint32_t)N * (uint32_t)(K / 2)), 0x00020000);
+    // scales and zero points: this lane's word in each load, at group 0 of row group 0
+    const uint8_t* zsrc = a.Z ? a.Z : (const uint8_t*)a.S;
+    const char* szp[Cfg::SLOADS + Cfg::ZLOADS];
+    int szshift[Cfg::SLOADS + Cfg::ZLOADS];
+#pragma unroll
+    for (int i = 0; i < Cfg::SLOADS + Cfg::ZLOADS; ++i) {
+        const bool scales = GROUP == 128 ? c4 < 2 : i < Cfg::SLOADS;
+        szshift[i] = scales ? 1 : 0;
+        const int zword = GROUP == 128 ? 0 : min(c4, Cfg::ZWORDS - 1);
+        szp[i] = scales ? (const char*)(a.S + (size_t)r16 * G + 8 * i + 2 * c4)
+                        : (const char*)(zsrc + (size_t)r16 * G + 4 * zword);
+    }
+
+    // ---- A ----
+    // Step i of a chunk of 128 k holds word i of each lane's 32 k with groups of
+    // 128, else k = 32 i .. 32 i + 31.
+    constexpr int xstep = GROUP == 128 ? 1 : 4;
+    const int xchunk = GROUP == 128 ? 4 * c4 : c4;
+    const int xm = min(r16, rows - 1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        xat[i] = (uint32_t)(xm * K * 2 + ((xchunk + xstep * i) ^ (xm & 7)) * 16 + b0 * (Cfg::BK * 2));
+    if constexpr (Cfg::XLDS) {
+        const int per = K / 8, n = rows * per;            // 16-byte chunks
+        for (int t0 = wave * kWave; t0 < n; t0 += WAVES * kWave) {
+            const int t = min(t0 + lane, n - 1), m = t / per, j = t - m * per;
+            __builtin_amdgcn_global_load_lds((const void*)(a.A + (size_t)m * K + (j ^ (m & 7)) * 8),
+                                             (GF_LDS void*)(xs + t0 * 16), 16, 0, 0);
+        }
+    }
+
+    for (int m0 = 0; m0 < (GROUPED ? rows : 1); m0 += MR) {
+        const int M = GROUPED ? min(rows - m0, MR) : rows;
+        // ---- direct loads of a task ----
+        const int ntasks = ng * nb;
+        int ig = part, ib = 0, islot = 0, issued = 0;     // the next task to issue
+        auto issue = [&]() __attribute__((always_inline)) {
+            GF_LDS char* buf = tasks + islot * Cfg::TASK_BYTES;
+            const int n0 = min(ig * 16, N - 16);
+            const uint32_t so = (uint32_t)__builtin_amdgcn_readfirstlane(n0 * (K / 2) + (b0 + ib) * (Cfg::BK / 2));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rq, (GF_LDS void*)(buf + i * 1024), 16, qoff[i], so, 0, 2);
+            const size_t at = (size_t)n0 * G + (b0 + ib) * GPB;
+#pragma unroll
+            for (int i = 0; i < Cfg::SLOADS + Cfg::ZLOADS; ++i)
+                __builtin_amdgcn_global_load_lds((const void*)(szp[i] + (at << szshift[i])),
+                                                 (GF_LDS void*)(buf + 4096 + i * 256), 4, 0, 0);
+            ++issued;
+            if (++ib == nb) { ib = 0; ig += parts; }
+            if (++islot == ring) islot = 0;
+        };
+        // At most `left` younger tasks' loads stay pending.
+        auto wait_tasks = [&](int left) __attribute__((always_inline)) {
+            left = __builtin_amdgcn_readfirstlane(left);
+            if (left >= 3) wait_vmcnt<3 * L>();
+            else if (left == 2) wait_vmcnt<2 * L>();
+            else if (left == 1) wait_vmcnt<L>();
+            else wait_vmcnt<0>();
+        };
+        const int first = min(ring, ntasks);
+        for (int i = 0; i < first; ++i) issue();
+        half8 xreg[Cfg::XLDS ? 1 : Cfg::XB * 16][MB];
+        if constexpr (!Cfg::XLDS) {
+#pragma unroll
+            for (int b = 0; b < Cfg::XB; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+#pragma unroll
+                    for (int m = 0; m < MB; ++m) {
+                        const half8 v = *(const half8*)(
+                            a.A + (size_t)(m0 + min(16 * m + r16, M - 1)) * K +
+                            min(b0 + b, nblk - 1) * Cfg::BK + (i / 4) * 128 + (xchunk + xstep * (i % 4)) * 8);
+                        xreg[b * 16 + i][m] = __builtin_shufflevector(v, v, 0, 4, 1, 5, 2, 6, 3, 7);
+                    }
+        }
+        if constexpr (Cfg::XLDS) {                        // A has landed: only whole tasks are pending
+            if (first >= 4) wait_vmcnt<4 * L>();
+            else wait_tasks(first);
+            lds_barrier();
+        }
+
+        int done = 0, slot = 0;
+        for (int gi = 0; gi < ng; ++gi) {
+            floatx4 acc[MB] = {};
+            auto block = [&](int b, auto xb_c) __attribute__((always_inline)) {
+                constexpr int xb = decltype(xb_c)::value;
+                wait_tasks(issued - done - 1);
+                asm volatile("" ::: "memory");
+                const GF_LDS char* buf = tasks + slot * Cfg::TASK_BYTES;
+                const GF_LDS uint32_t* sz = (const GF_LDS uint32_t*)(buf + 4096) + r16;
+                uint32_t sw[Cfg::SWORDS], zw[Cfg::ZWORDS];
+#pragma unroll
+                for (int j = 0; j < Cfg::SWORDS; ++j) sw[j] = sz[16 * j];
+#pragma unroll
+                for (int j = 0; j < Cfg::ZWORDS; ++j)
+                    zw[j] = a.Z ? sz[16 * ((GROUP == 128 ? 2 : Cfg::SLOADS * 4) + j)] : 0x08080808u;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {             // chunks of 128 k
+                    u32x4 q = *(const GF_LDS u32x4*)(buf + qat[c]);
+                    if constexpr (GROUP < 128) {
+                        const u32x2 p = __builtin_amdgcn_permlane32_swap(q[0], q[2], false, false);
+                        const u32x2 r = __builtin_amdgcn_permlane32_swap(q[1], q[3], false, false);
+                        const u32x2 s = __builtin_amdgcn_permlane16_swap(p[0], r[0], false, false);
+                        const u32x2 t = __builtin_amdgcn_permlane16_swap(p[1], r[1], false, false);
+                        q = u32x4{s[0], s[1], t[0], t[1]};
+                    }
+                    constexpr int SPG = GROUP / 32, GPC = 128 / GROUP;
+#pragma unroll
+                    for (int g0 = 0; g0 < GPC; ++g0) {
+                        const int g = c * GPC + g0;       // within the block
+                        const _Float16 s = __builtin_bit_cast(_Float16, (uint16_t)(sw[g / 2] >> (16 * (g % 2))));
+                        const half2v nz = -__builtin_bit_cast(half2v, __builtin_amdgcn_perm(
+                            0u, zw[g / 4], 0x0c000c00u + 0x00010001u * (uint32_t)(g % 4)));
+                        floatx4 sum[MB] = {};
+#pragma unroll
+                        for (int i = g0 * SPG; i < (g0 + 1) * SPG; ++i) {
+                            if constexpr (Cfg::XLDS) {
+                                const half8 x = *(const GF_LDS half8*)(xs + xat[i] + b * (Cfg::BK * 2) + c * 256);
+                                sum[0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, w4_unpack(q[i], nz), sum[0], 0, 0, 0);
+                            } else {
+                                const half8 w = w4_unpack_pairs(q[i], nz);
+#pragma unroll
+                                for (int m = 0; m < MB; ++m)
+                                    sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xreg[xb * 16 + 4 * c + i][m], w,
+                                                                                    sum[m], 0, 0, 0);
+                            }
+                        }
+#pragma unroll
+                        for (int m = 0; m < MB; ++m)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) acc[m][i] = fmaf(sum[m][i], (float)s, acc[m][i]);
+                    }
+                }
+                asm volatile("" ::: "memory");
+                wait_lgkmcnt0();                          // the buffer is read: it may be filled again
+                if (issued < ntasks) issue();
+                ++done;
+                if (++slot == ring) slot = 0;
+            };
+            if constexpr (Cfg::XLDS) {
+                for (int b = 0; b < nb; ++b) block(b, std::integral_constant<int, 0>{});
+            } else {
+                static_for<Cfg::XB>([&](auto xb) __attribute__((always_inline)) {
+                    if (decltype(xb)::value < nb) block(decltype(xb)::value, xb);
+                });
+            }
+            // ---- the waves' sums, in wave order ----
+            GF_LDS float* mine = red + (gi & 1) * WAVES * red_rows * 16;
+#pragma unroll
+            for (int m = 0; m < MB; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = 16 * m + 4 * c4 + i;
+                    if (row < M) mine[(wave * red_rows + row) * 16 + r16] = acc[m][i];
+                }
+            lds_barrier();
+            const int n0 = min((part + gi * parts) * 16, N - 16);
+            for (int t = threadIdx.x; t < M * 16; t += WAVES * kWave) {
+                float s = 0.0f;
+#pragma unroll
+                for (int w = 0; w < WAVES; ++w) s += mine[w * red_rows * 16 + t];
+                a.C[(size_t)(m0 + t / 16) * N + n0 + t % 16] = f32_to_f16_bits(s * kW4Unit);
+            }
+        }
+        wait_vmcnt<0>();
+        if constexpr (GROUPED) lds_barrier();             // the next pass reuses the sums' slots
+    }
+#endif
+}
+
 // ---------------------------------------------------------------------------
 // tiles: many rows of A
 // ---------------------------------------------------------------------------
