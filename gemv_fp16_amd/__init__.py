@@ -550,42 +550,47 @@ def sp_default_config(M: int, N: int, K: int) -> dict:
 # products grouped by expert, 4-bit weights
 # ---------------------------------------------------------------------------
 
-def _same_device(*tensors):
-    """The device all of them (None aside) are on."""
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError("tensors are on different devices (%s and %s)" % (dev, t.device))
-    return dev
+# These calls may be all that a decode step does between two launches of a few
+# microseconds, so their checks are kept to plain attribute reads and the
+# arguments go to ctypes as ints.
+
+def _ptr(t, dtype, name):
+    """Address of t, checked as _dev does."""
+    if t.is_cuda and t.dtype is dtype and t.is_contiguous():
+        return t.data_ptr()
+    return _dev(t, dtype, name).value
 
 
-def _launch(name, device, stream, *args):
+def _launch(name, tensors, stream, *args):
     """Call the C entry `name` on `stream`, by default the current stream of
     the tensors' device, with that device current (the null stream is that of
-    the current device)."""
+    the current device).  All tensors must be on one device."""
     import torch
-    fn = getattr(lib(), name)
+    d = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != d:
+            raise ValueError("tensors are on different devices (%s and %s)" % (tensors[0].device, t.device))
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    if device.index == torch.cuda.current_device():
-        rc = fn(*args, _stream(stream))
+        s = torch._C._cuda_getCurrentRawStream(d)
     else:
-        with torch.cuda.device(device):
-            rc = fn(*args, _stream(stream))
+        s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    fn = getattr(_lib or lib(), name)
+    if d == torch._C._cuda_getDevice():
+        rc = fn(*args, s)
+    else:
+        with torch.cuda.device(d):
+            rc = fn(*args, s)
     if rc:
         _check(rc, name)
 
 
-def _out(t, shape, dtype, device, stream, name):
-    """The caller's output, checked, or a new one."""
-    import torch
+def _out(t, like, shape, dtype, stream, name):
+    """The caller's output, checked, or a new one on `like`'s device."""
     if t is None:
-        return _alloc(stream, lambda: torch.empty(shape, dtype=dtype, device=device))
-    if tuple(t.shape) != tuple(shape):
+        if stream is None:
+            return like.new_empty(shape, dtype=dtype)
+        return _alloc(stream, lambda: like.new_empty(shape, dtype=dtype))
+    if t.shape != shape:
         raise ValueError("%s must be %s" % (name, tuple(shape)))
     return t
 
@@ -594,7 +599,7 @@ def _offsets(offsets, E):
     import torch
     if offsets.dim() != 1 or offsets.shape[0] != E + 1:
         raise ValueError("offsets must hold %d entries, one more than there are groups" % (E + 1))
-    return _dev(offsets, torch.int32, "offsets")
+    return _ptr(offsets, torch.int32, "offsets")
 
 
 def gemm_f16_grouped_nt(A, B, offsets, C=None, stream=None):
@@ -604,10 +609,11 @@ def gemm_f16_grouped_nt(A, B, offsets, C=None, stream=None):
     import torch
     if A.dim() != 2 or B.dim() != 3 or A.shape[1] != B.shape[2]:
         raise ValueError("A must be (T, K) and B (E, N, K)")
-    (T, K), (E, N) = A.shape, B.shape[:2]
-    C = _out(C, (T, N), torch.float16, A.device, stream, "C")
-    _launch("gemm_f16_grouped_nt", _same_device(A, B, offsets, C), stream, _dev(A, torch.float16, "A"),
-            _dev(B, torch.float16, "B"), _dev(C, torch.float16, "C"), _offsets(offsets, E), T, E, N, K)
+    (T, K), (E, N, _) = A.shape, B.shape
+    f16 = torch.float16
+    C = _out(C, A, (T, N), f16, stream, "C")
+    _launch("gemm_f16_grouped_nt", (A, B, offsets, C), stream, _ptr(A, f16, "A"), _ptr(B, f16, "B"),
+            _ptr(C, f16, "C"), _offsets(offsets, E), T, E, N, K)
     return C
 
 
@@ -618,10 +624,11 @@ def gemm_f16_grouped_nn(A, B, offsets, C=None, stream=None):
     import torch
     if A.dim() != 2 or B.dim() != 3 or A.shape[1] != B.shape[1]:
         raise ValueError("A must be (T, K) and B (E, K, N)")
-    (T, K), E, N = A.shape, B.shape[0], B.shape[2]
-    C = _out(C, (T, N), torch.float16, A.device, stream, "C")
-    _launch("gemm_f16_grouped_nn", _same_device(A, B, offsets, C), stream, _dev(A, torch.float16, "A"),
-            _dev(B, torch.float16, "B"), _dev(C, torch.float16, "C"), _offsets(offsets, E), T, E, N, K)
+    (T, K), (E, _, N) = A.shape, B.shape
+    f16 = torch.float16
+    C = _out(C, A, (T, N), f16, stream, "C")
+    _launch("gemm_f16_grouped_nn", (A, B, offsets, C), stream, _ptr(A, f16, "A"), _ptr(B, f16, "B"),
+            _ptr(C, f16, "C"), _offsets(offsets, E), T, E, N, K)
     return C
 
 
@@ -638,27 +645,39 @@ def gemm_f16_grouped_tn(A, B, offsets, C=None, out_f32=None, stream=None):
     (T, M), N, E = A.shape, B.shape[1], offsets.shape[0] - 1
     if out_f32 is None:
         out_f32 = C is not None and C.dtype == torch.float32
-    dt = torch.float32 if out_f32 else torch.float16
-    C = _out(C, (E, M, N), dt, A.device, stream, "C")
-    _launch("gemm_f16_grouped_tn", _same_device(A, B, offsets, C), stream, _dev(A, torch.float16, "A"),
-            _dev(B, torch.float16, "B"), _dev(C, dt, "C"), _offsets(offsets, E), T, E, M, N, int(bool(out_f32)))
+    f16, dt = torch.float16, torch.float32 if out_f32 else torch.float16
+    C = _out(C, A, (E, M, N), dt, stream, "C")
+    _launch("gemm_f16_grouped_tn", (A, B, offsets, C), stream, _ptr(A, f16, "A"), _ptr(B, f16, "B"),
+            _ptr(C, dt, "C"), _offsets(offsets, E), T, E, M, N, 1 if out_f32 else 0)
     return C
 
 
-def _w4_args(Q, S, Z, group, dim):
-    """Checked (pointers of Q, S, Z), leading shape and K of 4-bit weights."""
-    import torch
-    if Q.dim() != dim or S.dim() != dim or (Z is not None and Z.dim() != dim):
+def _w4_check(Q, S, Z, group, dim):
+    """Leading shape and K of 4-bit weights with `dim` dimensions."""
+    q = Q.shape
+    if len(q) != dim:
         raise ValueError("Q, S and Z must have %d dimensions" % dim)
     if group not in (32, 64, 128):
         raise ValueError("group must be 32, 64 or 128")
-    K = 8 * Q.shape[-1]
-    want = tuple(Q.shape[:-1]) + ((K + group - 1) // group,)
-    if tuple(S.shape) != want or (Z is not None and tuple(Z.shape) != want):
-        raise ValueError("S and Z must be %s for K = %d in groups of %d" % (want, K, group))
-    ptrs = (_dev(Q, torch.int32, "Q"), _dev(S, torch.float16, "S"),
-            None if Z is None else _dev(Z, torch.uint8, "Z"))
-    return ptrs, want[:-1], K
+    K = 8 * q[-1]
+    lead = q[:-1]
+    want = lead + ((K + group - 1) // group,)
+    if S.shape != want or (Z is not None and Z.shape != want):
+        raise ValueError("S and Z must be %s for K = %d in groups of %d" % (tuple(want), K, group))
+    return lead, K
+
+
+def _w4_ptrs(Q, S, Z):
+    import torch
+    return (_ptr(Q, torch.int32, "Q"), _ptr(S, torch.float16, "S"),
+            None if Z is None else _ptr(Z, torch.uint8, "Z"))
+
+
+def _rows(lead):
+    n = 1
+    for x in lead:
+        n *= x
+    return n
 
 
 def w4_quantize_f16(W, group: int = 128, symmetric: bool = False, Q=None, S=None, Z=None, stream=None):
@@ -673,17 +692,15 @@ def w4_quantize_f16(W, group: int = 128, symmetric: bool = False, Q=None, S=None
         raise ValueError("group must be 32, 64 or 128")
     if symmetric and Z is not None:
         raise ValueError("symmetric codes have no Z")
-    lead, K = tuple(W.shape[:-1]), W.shape[-1]
-    Q = _out(Q, lead + (K // 8,), torch.int32, W.device, stream, "Q")
-    S = _out(S, lead + ((K + group - 1) // group,), torch.float16, W.device, stream, "S")
+    lead, K = W.shape[:-1], W.shape[-1]
+    w = _ptr(W, torch.float16, "W")
+    per_group = lead + ((K + group - 1) // group,)
+    Q = _out(Q, W, lead + (K // 8,), torch.int32, stream, "Q")
+    S = _out(S, W, per_group, torch.float16, stream, "S")
     if not symmetric:
-        Z = _out(Z, tuple(S.shape), torch.uint8, W.device, stream, "Z")
-    rows = 1
-    for n in lead:
-        rows *= n
-    _launch("w4_quantize_f16", _same_device(W, Q, S, Z), stream, _dev(W, torch.float16, "W"),
-            _dev(Q, torch.int32, "Q"), _dev(S, torch.float16, "S"),
-            None if Z is None else _dev(Z, torch.uint8, "Z"), rows, K, group)
+        Z = _out(Z, W, per_group, torch.uint8, stream, "Z")
+    _launch("w4_quantize_f16", (W, Q, S) if Z is None else (W, Q, S, Z), stream, w, *_w4_ptrs(Q, S, Z),
+            _rows(lead), K, group)
     return Q, S, Z
 
 
@@ -692,13 +709,11 @@ def w4_dequantize_f16(Q, S, Z=None, group: int = 128, W=None, stream=None):
     import torch
     if Q.dim() not in (2, 3):
         raise ValueError("Q must be (N, K/8) or (E, N, K/8)")
-    ptrs, lead, K = _w4_args(Q, S, Z, group, Q.dim())
-    W = _out(W, tuple(lead) + (K,), torch.float16, Q.device, stream, "W")
-    rows = 1
-    for n in lead:
-        rows *= n
-    _launch("w4_dequantize_f16", _same_device(Q, S, Z, W), stream, *ptrs, _dev(W, torch.float16, "W"),
-            rows, K, group)
+    lead, K = _w4_check(Q, S, Z, group, Q.dim())
+    ptrs = _w4_ptrs(Q, S, Z)
+    W = _out(W, Q, lead + (K,), torch.float16, stream, "W")
+    _launch("w4_dequantize_f16", (Q, S, W) if Z is None else (Q, S, W, Z), stream, *ptrs,
+            _ptr(W, torch.float16, "W"), _rows(lead), K, group)
     return W
 
 
@@ -706,37 +721,37 @@ def gemm_w4_f16_nt(A, Q, S, Z=None, C=None, group: int = 128, stream=None):
     """C = A . W^T (fp32 accumulate, fp16 out) with A (M, K) and the 4-bit
     weights Q (N, K/8), S, Z of w4_quantize_f16.  Returns C (M, N)."""
     import torch
-    ptrs, (N,), K = _w4_args(Q, S, Z, group, 2)
+    (N,), K = _w4_check(Q, S, Z, group, 2)
     if A.dim() != 2 or A.shape[1] != K:
         raise ValueError("A must be (M, %d)" % K)
-    M = A.shape[0]
-    C = _out(C, (M, N), torch.float16, A.device, stream, "C")
-    _launch("gemm_w4_f16_nt", _same_device(A, Q, S, Z, C), stream, _dev(A, torch.float16, "A"), *ptrs,
-            _dev(C, torch.float16, "C"), M, N, K, group)
+    M, f16 = A.shape[0], torch.float16
+    C = _out(C, A, (M, N), f16, stream, "C")
+    _launch("gemm_w4_f16_nt", (A, Q, S, C) if Z is None else (A, Q, S, C, Z), stream, _ptr(A, f16, "A"),
+            *_w4_ptrs(Q, S, Z), _ptr(C, f16, "C"), M, N, K, group)
     return C
 
 
 def gemv_w4_f16(Q, S, Z, x, y=None, group: int = 128, stream=None):
     """y = W . x with the 4-bit weights Q (N, K/8), S, Z (or None) and x (K,)."""
     import torch
-    ptrs, (N,), K = _w4_args(Q, S, Z, group, 2)
+    (N,), K = _w4_check(Q, S, Z, group, 2)
     if x.dim() != 1 or x.shape[0] != K:
         raise ValueError("x must be (%d,)" % K)
-    y = _out(y, (N,), torch.float16, x.device, stream, "y")
-    _launch("gemv_w4_f16", _same_device(x, Q, S, Z, y), stream, *ptrs, _dev(x, torch.float16, "x"),
-            _dev(y, torch.float16, "y"), N, K, group)
+    f16 = torch.float16
+    y = _out(y, x, (N,), f16, stream, "y")
+    _launch("gemv_w4_f16", (x, Q, S, y) if Z is None else (x, Q, S, y, Z), stream, *_w4_ptrs(Q, S, Z),
+            _ptr(x, f16, "x"), _ptr(y, f16, "y"), N, K, group)
     return y
 
 
 def gemm_w4_f16_grouped_nt(A, Q, S, Z, offsets, C=None, group: int = 128, stream=None):
     """gemm_f16_grouped_nt with 4-bit weights: Q (E, N, K/8), S and Z (E, N, G)."""
     import torch
-    ptrs, (E, N), K = _w4_args(Q, S, Z, group, 3)
+    (E, N), K = _w4_check(Q, S, Z, group, 3)
     if A.dim() != 2 or A.shape[1] != K:
         raise ValueError("A must be (T, %d)" % K)
-    T = A.shape[0]
-    C = _out(C, (T, N), torch.float16, A.device, stream, "C")
-    _launch("gemm_w4_f16_grouped_nt", _same_device(A, Q, S, Z, offsets, C), stream,
-            _dev(A, torch.float16, "A"), *ptrs, _dev(C, torch.float16, "C"), _offsets(offsets, E), T, E, N, K,
-            group)
+    T, f16 = A.shape[0], torch.float16
+    C = _out(C, A, (T, N), f16, stream, "C")
+    _launch("gemm_w4_f16_grouped_nt", (A, Q, S, offsets, C) if Z is None else (A, Q, S, offsets, C, Z), stream,
+            _ptr(A, f16, "A"), *_w4_ptrs(Q, S, Z), _ptr(C, f16, "C"), _offsets(offsets, E), T, E, N, K, group)
     return C
