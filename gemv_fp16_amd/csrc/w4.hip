@@ -27,31 +27,52 @@ int w4_grid(int64_t items)
     return (int)(g < 65536 ? g : 65536);
 }
 
+// How rows of K (padded to whole groups of GROUP) are walked, and the grid.
+W4Walk w4_walk(int64_t N, int K, int group, int& grid)
+{
+    W4Walk w;
+    w.per_row = ceil_div(K, group) * (group / 8);
+    w.rows_at_once = w.per_row >= 256 ? 1 : 256 / w.per_row;
+    w.chunks = ceil_div(w.per_row, 256);
+    w.rows = N;
+    const int64_t iterations = (N + w.rows_at_once - 1) / w.rows_at_once;
+    grid = (int)(iterations < 2048 ? iterations : 2048);  // eight workgroups of 256 to a CU
+    return w;
+}
+
+template <int GROUP, bool ASYM>
+hipError_t quantize(const void* W, void* Q, void* S, void* Z, int64_t N, int K, hipStream_t stream)
+{
+    int grid;
+    const W4Walk w = w4_walk(N, K, GROUP, grid);
+    const int G = ceil_div(K, GROUP);
+    if (w4_aligned(W, 16))
+        hipLaunchKernelGGL((w4_quantize_kernel<GROUP, ASYM, true>), dim3(grid), dim3(256), 0, stream,
+                           (const uint16_t*)W, (uint32_t*)Q, (uint16_t*)S, (uint8_t*)Z, K, G, w);
+    else
+        hipLaunchKernelGGL((w4_quantize_kernel<GROUP, ASYM, false>), dim3(grid), dim3(256), 0, stream,
+                           (const uint16_t*)W, (uint32_t*)Q, (uint16_t*)S, (uint8_t*)Z, K, G, w);
+    return hipGetLastError();
+}
+
 template <int GROUP>
 hipError_t quantize(const void* W, void* Q, void* S, void* Z, int64_t N, int K, hipStream_t stream)
 {
-    const int G = ceil_div(K, GROUP);
-    const int64_t items = N * G * (GROUP / 8);
-    if (w4_aligned(W, 16))
-        hipLaunchKernelGGL((w4_quantize_kernel<GROUP, true>), dim3(w4_grid(items)), dim3(256), 0, stream,
-                           (const uint16_t*)W, (uint32_t*)Q, (uint16_t*)S, (uint8_t*)Z, K, G, items);
-    else
-        hipLaunchKernelGGL((w4_quantize_kernel<GROUP, false>), dim3(w4_grid(items)), dim3(256), 0, stream,
-                           (const uint16_t*)W, (uint32_t*)Q, (uint16_t*)S, (uint8_t*)Z, K, G, items);
-    return hipGetLastError();
+    return Z ? quantize<GROUP, true>(W, Q, S, Z, N, K, stream) : quantize<GROUP, false>(W, Q, S, Z, N, K, stream);
 }
 
 template <int GROUP>
 hipError_t dequantize(const void* Q, const void* S, const void* Z, void* W, int64_t N, int K, hipStream_t stream)
 {
+    int grid;
+    const W4Walk w = w4_walk(N, K, GROUP, grid);
     const int G = ceil_div(K, GROUP);
-    const int64_t words = N * (K / 8);
     if (w4_aligned(W, 16))
-        hipLaunchKernelGGL((w4_dequantize_kernel<GROUP, true>), dim3(w4_grid(words)), dim3(256), 0, stream,
-                           (const uint32_t*)Q, (const uint16_t*)S, (const uint8_t*)Z, (uint16_t*)W, K, G, words);
+        hipLaunchKernelGGL((w4_dequantize_kernel<GROUP, true>), dim3(grid), dim3(256), 0, stream,
+                           (const uint32_t*)Q, (const uint16_t*)S, (const uint8_t*)Z, (uint16_t*)W, K, G, w);
     else
-        hipLaunchKernelGGL((w4_dequantize_kernel<GROUP, false>), dim3(w4_grid(words)), dim3(256), 0, stream,
-                           (const uint32_t*)Q, (const uint16_t*)S, (const uint8_t*)Z, (uint16_t*)W, K, G, words);
+        hipLaunchKernelGGL((w4_dequantize_kernel<GROUP, false>), dim3(grid), dim3(256), 0, stream,
+                           (const uint32_t*)Q, (const uint16_t*)S, (const uint8_t*)Z, (uint16_t*)W, K, G, w);
     return hipGetLastError();
 }
 

@@ -14,6 +14,7 @@
 // output: weights are never rounded to fp16.
 #pragma once
 #include "common.hpp"
+#include "gemv_kernel.hpp"
 #include "grouped_kernel.hpp"
 
 namespace gf {
@@ -25,15 +26,61 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 // quantize and back
 // ---------------------------------------------------------------------------
 
-// Reduction over the LANES neighbouring lanes (4, 8 or 16) that share a group.
+// Rows are walked by whole workgroups, R rows at a time where they are short and
+// in pieces of 256 threads where they are long, grid-stride over the rows: a
+// thread's place in its row is found once, without a division per piece.
+struct W4Walk {
+    int per_row;          // threads a row takes (a multiple of a group's)
+    int rows_at_once;     // R = max(1, 256 / per_row)
+    int chunks;           // pieces of 256 threads that a row takes (1 if R > 1)
+    int64_t rows;
+};
+
+struct W4Place {
+    int64_t row;          // of this thread
+    int j, c, sub;        // word within the row; piece; row within the iteration
+    __device__ __forceinline__ W4Place(const W4Walk& w)
+    {
+        sub = w.rows_at_once > 1 ? (int)threadIdx.x / w.per_row : 0;
+        j = (int)threadIdx.x - sub * w.per_row;
+        c = 0;
+        row = (int64_t)blockIdx.x * w.rows_at_once + sub;
+    }
+    __device__ __forceinline__ bool more(const W4Walk& w) const { return row - sub < w.rows; }   // uniform
+    __device__ __forceinline__ bool live(const W4Walk& w) const
+    {
+        return sub < w.rows_at_once && row < w.rows && j < w.per_row;
+    }
+    __device__ __forceinline__ void next(const W4Walk& w)
+    {
+        if (++c < w.chunks) {
+            j += 256;
+        } else {
+            j -= (w.chunks - 1) * 256;
+            c = 0;
+            row += (int64_t)gridDim.x * w.rows_at_once;
+        }
+    }
+};
+
+// The same value in the LANES neighbouring lanes (4, 8 or 16) that share a group:
+// f over all of them, by lane permutes within a DPP row.
 template <int LANES, class F>
 __device__ __forceinline__ float group_reduce(float v, F f)
 {
-    v = f(v, __shfl_xor(v, 1));
-    v = f(v, __shfl_xor(v, 2));
-    if constexpr (LANES >= 8) v = f(v, __shfl_xor(v, 4));
-    if constexpr (LANES >= 16) v = f(v, __shfl_xor(v, 8));
+    v = f(v, dpp_f32<0xB1>(v));                            // quad_perm [1,0,3,2]
+    v = f(v, dpp_f32<0x4E>(v));                            // quad_perm [2,3,0,1]
+    if constexpr (LANES >= 8) v = f(v, dpp_f32<0x141>(v)); // row_half_mirror
+    if constexpr (LANES >= 16) v = f(v, dpp_f32<0x140>(v));// row_mirror
     return v;
+}
+
+// a / b with r = 1 / b to within a rounding: the first quotient's residual is
+// exact, and the quotient it corrects is the nearest one (Markstein's method).
+__device__ __forceinline__ float w4_quotient(float a, float b, float r)
+{
+    const float q = a * r;
+    return fmaf(fmaf(-q, b, a), r, q);
 }
 
 // One thread holds 8 consecutive k (a word of codes), GROUP / 8 neighbouring
@@ -43,102 +90,150 @@ __device__ __forceinline__ float group_reduce(float v, F f)
 //
 // The code is the quotient w / s rounded to nearest, ties to even, and has to
 // be that of the exact quotient.  w * (1 / s) can fall on the wrong side of a
-// tie, so one correction step follows: the residual w - t s is exact in fp32
-// (w and s have 11 significant bits), and t + residual / s is the exact
-// quotient wherever that is representable, as every tie is; the quotients that
-// are not ties lie further from one than the rounding errors here.
-template <int GROUP, bool VEC>
+// tie, hence the correction: its residual is exact (w and s have 11 significant
+// bits), so it gives the exact quotient wherever that is representable, as every
+// tie is; the quotients that are not ties lie further from one than fp32 rounds.
+// Bound by HBM and the vector ALU alike (2 bytes read and half a byte written
+// for about 10 instructions), so the codes are put together as exact fp32
+// integers, six to a sum, and the zero point is added to all eight at once.
+template <int GROUP, bool ASYM, bool VEC>
 __global__ __launch_bounds__(256) void w4_quantize_kernel(const uint16_t* __restrict__ W,
                                                           uint32_t* __restrict__ Q,
                                                           uint16_t* __restrict__ S, uint8_t* __restrict__ Z,
-                                                          int K, int G, int64_t items)
+                                                          int K, int G, W4Walk walk)
 {
     constexpr int LANES = GROUP / 8;
-    const int per_row = G * LANES;
-    const int64_t stride = (int64_t)gridDim.x * 256;
-    for (int64_t base = (int64_t)blockIdx.x * 256; base < items; base += stride) {
-        const int64_t idx = base + threadIdx.x;
-        const bool live = idx < items;
-        const int64_t row = live ? idx / per_row : 0;
-        const int j = live ? (int)(idx - row * per_row) : 0;
-        const bool some = live && j * 8 < K;
-        uint16_t h[8] = {};
-        if (some) {
-            const uint16_t* p = W + row * K + (int64_t)j * 8;
+    auto load = [&](const W4Place& p) __attribute__((always_inline)) {
+        u32x4 v = {0u, 0u, 0u, 0u};
+        if (p.live(walk) && p.j * 8 < K) {
+            const uint16_t* src = W + p.row * K + (int64_t)p.j * 8;
             if constexpr (VEC) {
-                const u32x4 v = __builtin_nontemporal_load((const u32x4*)p);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) h[i] = (uint16_t)(v[i / 2] >> (16 * (i % 2)));
+                v = __builtin_nontemporal_load((const u32x4*)src);
             } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) h[i] = p[i];
+                for (int i = 0; i < 8; ++i) v[i / 2] |= (uint32_t)src[i] << (16 * (i % 2));
             }
         }
-        float w[8], lo = 0.0f, hi = 0.0f, inf = 0.0f;
+        return v;
+    };
+    W4Place at(walk), ahead(walk);
+    u32x4 v = load(at);
+    for (; at.more(walk); at = ahead) {                   // the next piece is in flight while one is worked on
+        ahead.next(walk);
+        const u32x4 following = load(ahead);
+        const bool live = at.live(walk), some = live && at.j * 8 < K;
+        const int64_t row = at.row;
+        const int j = at.j;
+        const half8 h = __builtin_bit_cast(half8, v);
+        // An infinity or a NaN has all exponent bits set: one more carries into
+        // the sign's place.
+        uint32_t carry = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            w[i] = f16_bits_to_f32(h[i]);
-            if ((h[i] & 0x7c00) == 0x7c00) inf = 1.0f;    // an infinity or a NaN
-            lo = fminf(lo, w[i]);
-            hi = fmaxf(hi, w[i]);
-        }
-        auto mx = [](float a, float b) { return fmaxf(a, b); };
-        auto mn = [](float a, float b) { return fminf(a, b); };
-        hi = group_reduce<LANES>(hi, mx);
-        lo = group_reduce<LANES>(lo, mn);
-        inf = group_reduce<LANES>(inf, mx);
+        for (int i = 0; i < 4; ++i) carry |= (v[i] & 0x7c007c00u) + 0x04000400u;
+        float inf = 0.0f;
+        if (__ballot((carry & 0x80008000u) != 0))          // rare, and then for the whole wave
+            inf = group_reduce<LANES>((carry & 0x80008000u) != 0 ? 1.0f : 0.0f,
+                                      [](float a, float b) { return fmaxf(a, b); });
+        const half2v h0 = {h[0], h[1]}, h1 = {h[2], h[3]}, h2 = {h[4], h[5]}, h3 = {h[6], h[7]};
+        const half2v top = __builtin_elementwise_max(__builtin_elementwise_max(h0, h1), __builtin_elementwise_max(h2, h3));
+        const half2v low = __builtin_elementwise_min(__builtin_elementwise_min(h0, h1), __builtin_elementwise_min(h2, h3));
+        const float hi = group_reduce<LANES>(fmaxf(fmaxf((float)top[0], (float)top[1]), 0.0f),
+                                             [](float a, float b) { return fmaxf(a, b); });
+        const float lo = group_reduce<LANES>(fminf(fminf((float)low[0], (float)low[1]), 0.0f),
+                                             [](float a, float b) { return fminf(a, b); });
         // (a zero scale is +0, whatever the signs of the zeros it came from)
-        const uint16_t sb = f32_to_f16_bits(fabsf(Z ? (hi - lo) / 15.0f : fmaxf(hi, -lo) / 7.0f));
+        const float span = ASYM ? hi - lo : fmaxf(hi, -lo);
+        const uint16_t sb = f32_to_f16_bits(fabsf(w4_quotient(span, ASYM ? 15.0f : 7.0f, ASYM ? 1.0f / 15.0f : 1.0f / 7.0f)));
         const float s = f16_bits_to_f32(sb);
         const bool flat = s == 0.0f || inf != 0.0f;       // all codes are z
-        const float r = 1.0f / s;
-        float z = 8.0f;
-        if (Z) z = flat ? 0.0f : fminf(rintf(-lo / s), 15.0f);
-        uint32_t word = 0;
+        const float r0 = __builtin_amdgcn_rcpf(flat ? 1.0f : s), r = fmaf(fmaf(-s, r0, 1.0f), r0, r0);
+        const float z = !ASYM ? 8.0f : flat ? 0.0f : fminf(rintf(w4_quotient(-lo, s, r)), 15.0f);
+        float c[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float t0 = w[i] * r;
-            const float t = fmaf(fmaf(-t0, s, w[i]), r, t0);
-            const float q = flat ? z : fminf(fmaxf(rintf(t) + z, 0.0f), 15.0f);
-            word |= (uint32_t)(int)q << (4 * i);
-        }
-        if (some) __builtin_nontemporal_store(word, Q + row * (K / 8) + j);
+        for (int i = 0; i < 8; ++i)                       // the bounds are whole: clamping first is the same
+            c[i] = rintf(fminf(fmaxf(w4_quotient((float)h[i], s, r), -z), 15.0f - z));
+        // c0 + 16 c1 + .. + 16^5 c5, exact below 2^24
+        const float six = fmaf(fmaf(fmaf(fmaf(fmaf(c[5], 16.0f, c[4]), 16.0f, c[3]), 16.0f, c[2]), 16.0f, c[1]), 16.0f, c[0]);
+        const float two = fmaf(c[7], 16.0f, c[6]);
+        const uint32_t codes = flat ? 0u : (uint32_t)(int)six + ((uint32_t)(int)two << 24);
+        if (some) __builtin_nontemporal_store(codes + (uint32_t)(int)z * 0x11111111u, Q + row * (K / 8) + j);
         if (live && j % LANES == 0) {
-            const int64_t at = row * G + j / LANES;
-            S[at] = inf != 0.0f ? (uint16_t)0x7e00 : sb;
-            if (Z) Z[at] = (uint8_t)(int)z;
+            const int64_t g = row * G + j / LANES;
+            S[g] = inf != 0.0f ? (uint16_t)0x7e00 : sb;
+            if (ASYM) Z[g] = (uint8_t)(int)z;
         }
+        v = following;
     }
 }
 
-// One word of codes per thread.  (q - z) * s has at most 15 significant bits,
-// so the fp32 product is exact and the store rounds once.
+// The eight weights (q - z) * s of a word as fp16, in order.  A byte holds an
+// even k's code in its low half and the next one's in its high half; with the
+// exponent of 1024 put over them they are 1024 + q and 1024 + 16 q, and one
+// fused multiply-add brings both to q - z, exactly; the product with s rounds.
+// off: w4_offsets(z).
+__device__ __forceinline__ half8 w4_weights(uint32_t w, half2v off, half2v s)
+{
+    const half2v f = {(_Float16)1.0f, (_Float16)0.0625f};
+    half2v p[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        const uint32_t u = __builtin_amdgcn_perm(0u, w, 0x0c000c00u + 0x00010001u * (uint32_t)b);
+        p[b] = __builtin_elementwise_fma(__builtin_bit_cast(half2v, (u & 0x00f0000fu) | 0x64006400u), f, off) * s;
+    }
+    return half8{p[0][0], p[0][1], p[1][0], p[1][1], p[2][0], p[2][1], p[3][0], p[3][1]};
+}
+
+// -1024 - z and -64 - z: steps of 1 and of 1/16 from the bits of -1024 and -64.
+__device__ __forceinline__ half2v w4_offsets(uint32_t z)
+{
+    return __builtin_bit_cast(half2v, 0xd400e400u + (z & 0xffu) * 0x00100001u);
+}
+
+__device__ __forceinline__ half2v w4_twice(uint32_t bits)
+{
+    return __builtin_bit_cast(half2v, (bits & 0xffffu) * 0x00010001u);
+}
+
+// One word of codes per thread.
 template <int GROUP, bool VEC>
 __global__ __launch_bounds__(256) void w4_dequantize_kernel(const uint32_t* __restrict__ Q,
                                                             const uint16_t* __restrict__ S,
                                                             const uint8_t* __restrict__ Z,
-                                                            uint16_t* __restrict__ W, int K, int G,
-                                                            int64_t words)
+                                                            uint16_t* __restrict__ W, int K, int G, W4Walk walk)
 {
-    const int per_row = K / 8;
-    const int64_t stride = (int64_t)gridDim.x * 256;
-    for (int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x; idx < words; idx += stride) {
-        const int64_t row = idx / per_row;
-        const int j = (int)(idx - row * per_row);
-        const uint32_t q = __builtin_nontemporal_load(Q + idx);
-        const int64_t at = row * G + j / (GROUP / 8);
-        const float s = f16_bits_to_f32(S[at]), z = Z ? (float)Z[at] : 8.0f;
-        uint16_t h[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = f32_to_f16_bits(((float)((q >> (4 * i)) & 15u) - z) * s);
+    struct Word {
+        uint32_t q, s, z;
+    };
+    auto load = [&](const W4Place& p) __attribute__((always_inline)) {
+        Word w = {0u, 0u, 8u};
+        if (p.live(walk) && p.j * 8 < K) {
+            w.q = __builtin_nontemporal_load(Q + p.row * (K / 8) + p.j);
+            const int64_t g = p.row * G + p.j / (GROUP / 8);
+            w.s = S[g];
+            if (Z) w.z = Z[g];
+        }
+        return w;
+    };
+    W4Place at(walk), ahead(walk);
+    Word w0 = load(at);
+    ahead.next(walk);
+    Word w1 = load(ahead);
+    for (; at.more(walk); at.next(walk)) {                // two more words in flight
+        ahead.next(walk);
+        const Word w2 = load(ahead), w = w0;
+        w0 = w1;
+        w1 = w2;
+        if (!at.live(walk) || at.j * 8 >= K) continue;
+        const half8 h = w4_weights(w.q, w4_offsets(w.z), w4_twice(w.s));
+        uint16_t* p = W + at.row * K + (int64_t)at.j * 8;
+        // (taken apart as words: a bit cast of one element of h was seen to yield
+        // the first one for all eight)
+        const u32x4 v = __builtin_bit_cast(u32x4, h);
         if constexpr (VEC) {
-            u32x4 v;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = h[2 * i] | ((uint32_t)h[2 * i + 1] << 16);
-            __builtin_nontemporal_store(v, (u32x4*)W + idx);
+            __builtin_nontemporal_store(v, (u32x4*)p);
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) W[idx * 8 + i] = h[i];
+            for (int i = 0; i < 8; ++i) p[i] = (uint16_t)(v[i / 2] >> (16 * (i % 2)));
         }
     }
 }
@@ -879,23 +974,6 @@ struct W4TileCfg {
     static_assert(LDS_BYTES <= 160 * 1024, "one CU's LDS");
 };
 
-// The eight weights (q - z) * s of a word as fp16, in order.  A byte holds an
-// even k's code in its low half and the next one's in its high half; with the
-// exponent of 1024 put over them they are 1024 + q and 1024 + 16 q, and one
-// fused multiply-add brings both to q - z, exactly; the product with s rounds.
-// off: -1024 - z and -64 - z.
-__device__ __forceinline__ half8 w4_weights(uint32_t w, half2v off, half2v s)
-{
-    const half2v f = {(_Float16)1.0f, (_Float16)0.0625f};
-    half2v p[4];
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        const uint32_t u = __builtin_amdgcn_perm(0u, w, 0x0c000c00u + 0x00010001u * (uint32_t)b);
-        p[b] = __builtin_elementwise_fma(__builtin_bit_cast(half2v, (u & 0x00f0000fu) | 0x64006400u), f, off) * s;
-    }
-    return half8{p[0][0], p[0][1], p[1][0], p[1][1], p[2][0], p[2][1], p[3][0], p[3][1]};
-}
-
 // WINDOW: K % 256 == 0, S 16-byte and Z 8-byte aligned.  A row of Q, S or Z is
 // a line of its own, so what a lane loads from them costs a line whatever its
 // width: codes are then loaded two steps at a time and scales and zero points
@@ -1019,9 +1097,8 @@ __global__ __launch_bounds__(Cfg::NT) void w4_tile_kernel(W4Args a)
                 sb = sw[0][f][g / 2 % SW] >> (16 * (g % 2));
                 z = zw[0][f][0] >> (8 * g);
             }
-            sc[f] = __builtin_bit_cast(half2v, (sb & 0xffffu) * 0x00010001u);
-            // -1024 - z and -64 - z: steps of 1 and of 1/16 from the bits of -1024 and -64
-            off[f] = __builtin_bit_cast(half2v, 0xd400e400u + (a.Z ? z & 0xffu : 8u) * 0x00100001u);
+            sc[f] = w4_twice(sb);
+            off[f] = w4_offsets(a.Z ? z : 8u);
         }
     };
 
