@@ -40,40 +40,43 @@ W4Walk w4_walk(int64_t N, int K, int group, int& grid)
     return w;
 }
 
-template <int GROUP, bool ASYM>
+template <int GROUP, bool ASYM, bool VEC>
 hipError_t quantize(const void* W, void* Q, void* S, void* Z, int64_t N, int K, hipStream_t stream)
 {
     int grid;
     const W4Walk w = w4_walk(N, K, GROUP, grid);
-    const int G = ceil_div(K, GROUP);
-    if (w4_aligned(W, 16))
-        hipLaunchKernelGGL((w4_quantize_kernel<GROUP, ASYM, true>), dim3(grid), dim3(256), 0, stream,
-                           (const uint16_t*)W, (uint32_t*)Q, (uint16_t*)S, (uint8_t*)Z, K, G, w);
-    else
-        hipLaunchKernelGGL((w4_quantize_kernel<GROUP, ASYM, false>), dim3(grid), dim3(256), 0, stream,
-                           (const uint16_t*)W, (uint32_t*)Q, (uint16_t*)S, (uint8_t*)Z, K, G, w);
+    auto kern = w.rows_at_once > 1 ? w4_quantize_kernel<GROUP, ASYM, VEC, true> : w4_quantize_kernel<GROUP, ASYM, VEC, false>;
+    hipLaunchKernelGGL(kern, dim3(grid), dim3(256), 0, stream, (const uint16_t*)W, (uint32_t*)Q, (uint16_t*)S,
+                       (uint8_t*)Z, K, ceil_div(K, GROUP), w);
     return hipGetLastError();
 }
 
 template <int GROUP>
 hipError_t quantize(const void* W, void* Q, void* S, void* Z, int64_t N, int K, hipStream_t stream)
 {
-    return Z ? quantize<GROUP, true>(W, Q, S, Z, N, K, stream) : quantize<GROUP, false>(W, Q, S, Z, N, K, stream);
+    if (w4_aligned(W, 16))
+        return Z ? quantize<GROUP, true, true>(W, Q, S, Z, N, K, stream)
+                 : quantize<GROUP, false, true>(W, Q, S, Z, N, K, stream);
+    return Z ? quantize<GROUP, true, false>(W, Q, S, Z, N, K, stream)
+             : quantize<GROUP, false, false>(W, Q, S, Z, N, K, stream);
+}
+
+template <int GROUP, bool VEC>
+hipError_t dequantize(const void* Q, const void* S, const void* Z, void* W, int64_t N, int K, hipStream_t stream)
+{
+    int grid;
+    const W4Walk w = w4_walk(N, K, GROUP, grid);
+    auto kern = w.rows_at_once > 1 ? w4_dequantize_kernel<GROUP, VEC, true> : w4_dequantize_kernel<GROUP, VEC, false>;
+    hipLaunchKernelGGL(kern, dim3(grid), dim3(256), 0, stream, (const uint32_t*)Q, (const uint16_t*)S,
+                       (const uint8_t*)Z, (uint16_t*)W, K, ceil_div(K, GROUP), w);
+    return hipGetLastError();
 }
 
 template <int GROUP>
 hipError_t dequantize(const void* Q, const void* S, const void* Z, void* W, int64_t N, int K, hipStream_t stream)
 {
-    int grid;
-    const W4Walk w = w4_walk(N, K, GROUP, grid);
-    const int G = ceil_div(K, GROUP);
-    if (w4_aligned(W, 16))
-        hipLaunchKernelGGL((w4_dequantize_kernel<GROUP, true>), dim3(grid), dim3(256), 0, stream,
-                           (const uint32_t*)Q, (const uint16_t*)S, (const uint8_t*)Z, (uint16_t*)W, K, G, w);
-    else
-        hipLaunchKernelGGL((w4_dequantize_kernel<GROUP, false>), dim3(grid), dim3(256), 0, stream,
-                           (const uint32_t*)Q, (const uint16_t*)S, (const uint8_t*)Z, (uint16_t*)W, K, G, w);
-    return hipGetLastError();
+    return w4_aligned(W, 16) ? dequantize<GROUP, true>(Q, S, Z, W, N, K, stream)
+                             : dequantize<GROUP, false>(Q, S, Z, W, N, K, stream);
 }
 
 __global__ void w4_zero_kernel(uint16_t* __restrict__ p, int64_t n)

@@ -36,42 +36,58 @@ struct W4Walk {
     int64_t rows;
 };
 
+// SHORT: several rows at once.  Otherwise the row is the same for the whole
+// workgroup, and its addresses are scalars.
+template <bool SHORT>
 struct W4Place {
-    int64_t row;          // of this thread
-    int j, c, sub;        // word within the row; piece; row within the iteration
+    int64_t row0;         // first row of the iteration
+    int sub, j, c;        // this thread's row in it; word within the row; piece
     __device__ __forceinline__ W4Place(const W4Walk& w)
     {
-        sub = w.rows_at_once > 1 ? (int)threadIdx.x / w.per_row : 0;
+        sub = SHORT ? (int)threadIdx.x / w.per_row : 0;
         j = (int)threadIdx.x - sub * w.per_row;
         c = 0;
-        row = (int64_t)blockIdx.x * w.rows_at_once + sub;
+        row0 = (int64_t)blockIdx.x * (SHORT ? w.rows_at_once : 1);
     }
-    __device__ __forceinline__ bool more(const W4Walk& w) const { return row - sub < w.rows; }   // uniform
+    __device__ __forceinline__ int64_t row() const { return SHORT ? row0 + sub : row0; }
+    __device__ __forceinline__ bool more(const W4Walk& w) const { return row0 < w.rows; }   // uniform
     __device__ __forceinline__ bool live(const W4Walk& w) const
     {
-        return sub < w.rows_at_once && row < w.rows && j < w.per_row;
+        if constexpr (SHORT) return sub < w.rows_at_once && row0 + sub < w.rows;
+        else return row0 < w.rows && j < w.per_row;
     }
     __device__ __forceinline__ void next(const W4Walk& w)
     {
-        if (++c < w.chunks) {
+        if constexpr (SHORT) {
+            row0 += (int64_t)gridDim.x * w.rows_at_once;
+        } else if (++c < w.chunks) {
             j += 256;
         } else {
             j -= (w.chunks - 1) * 256;
             c = 0;
-            row += (int64_t)gridDim.x * w.rows_at_once;
+            row0 += gridDim.x;
         }
     }
 };
 
-// The same value in the LANES neighbouring lanes (4, 8 or 16) that share a group:
-// f over all of them, by lane permutes within a DPP row.
-template <int LANES, class F>
-__device__ __forceinline__ float group_reduce(float v, F f)
+// Maximum of both 16-bit halves over the LANES neighbouring lanes (4, 8 or 16)
+// that share a group, in all of them, by lane permutes within a DPP row.
+typedef uint16_t ushort2v __attribute__((ext_vector_type(2)));
+template <int CTRL>
+__device__ __forceinline__ uint32_t w4_max_step(uint32_t v)
 {
-    v = f(v, dpp_f32<0xB1>(v));                            // quad_perm [1,0,3,2]
-    v = f(v, dpp_f32<0x4E>(v));                            // quad_perm [2,3,0,1]
-    if constexpr (LANES >= 8) v = f(v, dpp_f32<0x141>(v)); // row_half_mirror
-    if constexpr (LANES >= 16) v = f(v, dpp_f32<0x140>(v));// row_mirror
+    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xF, 0xF, true);
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(ushort2v, v),
+                                                                  __builtin_bit_cast(ushort2v, o)));
+}
+
+template <int LANES>
+__device__ __forceinline__ uint32_t group_max(uint32_t v)
+{
+    v = w4_max_step<0xB1>(v);                             // quad_perm [1,0,3,2]
+    v = w4_max_step<0x4E>(v);                             // quad_perm [2,3,0,1]
+    if constexpr (LANES >= 8) v = w4_max_step<0x141>(v);  // row_half_mirror
+    if constexpr (LANES >= 16) v = w4_max_step<0x140>(v); // row_mirror
     return v;
 }
 
@@ -96,17 +112,18 @@ __device__ __forceinline__ float w4_quotient(float a, float b, float r)
 // Bound by HBM and the vector ALU alike (2 bytes read and half a byte written
 // for about 10 instructions), so the codes are put together as exact fp32
 // integers, six to a sum, and the zero point is added to all eight at once.
-template <int GROUP, bool ASYM, bool VEC>
+template <int GROUP, bool ASYM, bool VEC, bool SHORT>
 __global__ __launch_bounds__(256) void w4_quantize_kernel(const uint16_t* __restrict__ W,
                                                           uint32_t* __restrict__ Q,
                                                           uint16_t* __restrict__ S, uint8_t* __restrict__ Z,
                                                           int K, int G, W4Walk walk)
 {
     constexpr int LANES = GROUP / 8;
-    auto load = [&](const W4Place& p) __attribute__((always_inline)) {
+    typedef W4Place<SHORT> Place;
+    auto load = [&](const Place& p) __attribute__((always_inline)) {
         u32x4 v = {0u, 0u, 0u, 0u};
         if (p.live(walk) && p.j * 8 < K) {
-            const uint16_t* src = W + p.row * K + (int64_t)p.j * 8;
+            const uint16_t* src = W + p.row() * K + p.j * 8;
             if constexpr (VEC) {
                 v = __builtin_nontemporal_load((const u32x4*)src);
             } else {
@@ -116,13 +133,13 @@ __global__ __launch_bounds__(256) void w4_quantize_kernel(const uint16_t* __rest
         }
         return v;
     };
-    W4Place at(walk), ahead(walk);
+    Place at(walk), ahead(walk);
     u32x4 v = load(at);
     for (; at.more(walk); at = ahead) {                   // the next piece is in flight while one is worked on
         ahead.next(walk);
         const u32x4 following = load(ahead);
         const bool live = at.live(walk), some = live && at.j * 8 < K;
-        const int64_t row = at.row;
+        const int64_t row = at.row();
         const int j = at.j;
         const half8 h = __builtin_bit_cast(half8, v);
         // An infinity or a NaN has all exponent bits set: one more carries into
@@ -130,28 +147,32 @@ __global__ __launch_bounds__(256) void w4_quantize_kernel(const uint16_t* __rest
         uint32_t carry = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) carry |= (v[i] & 0x7c007c00u) + 0x04000400u;
-        float inf = 0.0f;
-        if (__ballot((carry & 0x80008000u) != 0))          // rare, and then for the whole wave
-            inf = group_reduce<LANES>((carry & 0x80008000u) != 0 ? 1.0f : 0.0f,
-                                      [](float a, float b) { return fmaxf(a, b); });
+        bool bad = (carry & 0x80008000u) != 0;
+        if (__ballot(bad)) bad = group_max<LANES>(bad ? 1u : 0u) != 0;   // rare, and then for the whole wave
+        // max(0, w) and max(0, -w) side by side: as 16-bit patterns both are
+        // non-negative numbers, which order like whole ones
         const half2v h0 = {h[0], h[1]}, h1 = {h[2], h[3]}, h2 = {h[4], h[5]}, h3 = {h[6], h[7]};
         const half2v top = __builtin_elementwise_max(__builtin_elementwise_max(h0, h1), __builtin_elementwise_max(h2, h3));
         const half2v low = __builtin_elementwise_min(__builtin_elementwise_min(h0, h1), __builtin_elementwise_min(h2, h3));
-        const float hi = group_reduce<LANES>(fmaxf(fmaxf((float)top[0], (float)top[1]), 0.0f),
-                                             [](float a, float b) { return fmaxf(a, b); });
-        const float lo = group_reduce<LANES>(fminf(fminf((float)low[0], (float)low[1]), 0.0f),
-                                             [](float a, float b) { return fminf(a, b); });
+        const uint32_t t = __builtin_bit_cast(uint32_t, top), n = __builtin_bit_cast(uint32_t, low) ^ 0x80008000u;
+        const half2v zero = {(_Float16)0.0f, (_Float16)0.0f};
+        const half2v side = __builtin_elementwise_max(
+            __builtin_elementwise_max(__builtin_bit_cast(half2v, __builtin_amdgcn_perm(n, t, 0x05040100u)),
+                                      __builtin_bit_cast(half2v, __builtin_amdgcn_perm(n, t, 0x07060302u))), zero);
+        const uint32_t both = group_max<LANES>(__builtin_bit_cast(uint32_t, side) & 0x7fff7fffu);
+        const float hi = f16_bits_to_f32((uint16_t)both), lo = -f16_bits_to_f32((uint16_t)(both >> 16));
         // (a zero scale is +0, whatever the signs of the zeros it came from)
-        const float span = ASYM ? hi - lo : fmaxf(hi, -lo);
-        const uint16_t sb = f32_to_f16_bits(fabsf(w4_quotient(span, ASYM ? 15.0f : 7.0f, ASYM ? 1.0f / 15.0f : 1.0f / 7.0f)));
+        const float span = ASYM ? hi - lo : __builtin_fmaxf(hi, -lo);
+        const uint16_t sb = f32_to_f16_bits(w4_quotient(span, ASYM ? 15.0f : 7.0f, ASYM ? 1.0f / 15.0f : 1.0f / 7.0f));
         const float s = f16_bits_to_f32(sb);
-        const bool flat = s == 0.0f || inf != 0.0f;       // all codes are z
+        const bool flat = s == 0.0f || bad;               // all codes are z
         const float r0 = __builtin_amdgcn_rcpf(flat ? 1.0f : s), r = fmaf(fmaf(-s, r0, 1.0f), r0, r0);
         const float z = !ASYM ? 8.0f : flat ? 0.0f : fminf(rintf(w4_quotient(-lo, s, r)), 15.0f);
+        const float least = -z, most = 15.0f - z;
         float c[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)                       // the bounds are whole: clamping first is the same
-            c[i] = rintf(fminf(fmaxf(w4_quotient((float)h[i], s, r), -z), 15.0f - z));
+            c[i] = rintf(__builtin_amdgcn_fmed3f(w4_quotient((float)h[i], s, r), least, most));
         // c0 + 16 c1 + .. + 16^5 c5, exact below 2^24
         const float six = fmaf(fmaf(fmaf(fmaf(fmaf(c[5], 16.0f, c[4]), 16.0f, c[3]), 16.0f, c[2]), 16.0f, c[1]), 16.0f, c[0]);
         const float two = fmaf(c[7], 16.0f, c[6]);
@@ -159,7 +180,7 @@ __global__ __launch_bounds__(256) void w4_quantize_kernel(const uint16_t* __rest
         if (some) __builtin_nontemporal_store(codes + (uint32_t)(int)z * 0x11111111u, Q + row * (K / 8) + j);
         if (live && j % LANES == 0) {
             const int64_t g = row * G + j / LANES;
-            S[g] = inf != 0.0f ? (uint16_t)0x7e00 : sb;
+            S[g] = bad ? (uint16_t)0x7e00 : sb;
             if (ASYM) Z[g] = (uint8_t)(int)z;
         }
         v = following;
@@ -195,26 +216,27 @@ __device__ __forceinline__ half2v w4_twice(uint32_t bits)
 }
 
 // One word of codes per thread.
-template <int GROUP, bool VEC>
+template <int GROUP, bool VEC, bool SHORT>
 __global__ __launch_bounds__(256) void w4_dequantize_kernel(const uint32_t* __restrict__ Q,
                                                             const uint16_t* __restrict__ S,
                                                             const uint8_t* __restrict__ Z,
                                                             uint16_t* __restrict__ W, int K, int G, W4Walk walk)
 {
+    typedef W4Place<SHORT> Place;
     struct Word {
         uint32_t q, s, z;
     };
-    auto load = [&](const W4Place& p) __attribute__((always_inline)) {
+    auto load = [&](const Place& p) __attribute__((always_inline)) {
         Word w = {0u, 0u, 8u};
         if (p.live(walk) && p.j * 8 < K) {
-            w.q = __builtin_nontemporal_load(Q + p.row * (K / 8) + p.j);
-            const int64_t g = p.row * G + p.j / (GROUP / 8);
-            w.s = S[g];
-            if (Z) w.z = Z[g];
+            w.q = __builtin_nontemporal_load(Q + p.row() * (K / 8) + p.j);
+            const uint32_t g = (uint32_t)p.j / (GROUP / 8);
+            w.s = *(S + p.row() * G + g);
+            if (Z) w.z = *(Z + p.row() * G + g);
         }
         return w;
     };
-    W4Place at(walk), ahead(walk);
+    Place at(walk), ahead(walk);
     Word w0 = load(at);
     ahead.next(walk);
     Word w1 = load(ahead);
@@ -225,7 +247,7 @@ __global__ __launch_bounds__(256) void w4_dequantize_kernel(const uint32_t* __re
         w1 = w2;
         if (!at.live(walk) || at.j * 8 >= K) continue;
         const half8 h = w4_weights(w.q, w4_offsets(w.z), w4_twice(w.s));
-        uint16_t* p = W + at.row * K + (int64_t)at.j * 8;
+        uint16_t* p = W + at.row() * K + at.j * 8;
         // (taken apart as words: a bit cast of one element of h was seen to yield
         // the first one for all eight)
         const u32x4 v = __builtin_bit_cast(u32x4, h);
