@@ -85,24 +85,6 @@ __global__ void w4_zero_kernel(uint16_t* __restrict__ p, int64_t n)
     for (int64_t t = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; t < n; t += stride) p[t] = 0;
 }
 
-template <int GROUP, int MB, int NB, bool QVEC, bool AVEC, bool GROUPED>
-int launch_stream(const W4Args& a, hipStream_t stream)
-{
-    constexpr int WAVES = 8, LDS = WAVES * MB * NB * 256 * 4;
-    auto kern = w4_stream_kernel<GROUP, MB, NB, WAVES, QVEC, AVEC, GROUPED>;
-    static std::atomic<uint64_t> lds_opt_in{0};
-    if (LDS > 64 * 1024) {
-        const hipError_t e = opt_in_lds((const void*)kern, LDS, lds_opt_in, stream);
-        if (e != hipSuccess) return GF_ERR_HIP;
-    }
-    int64_t blocks = ceil_div(a.M, 16 * MB);
-    if (GROUPED) blocks = a.g.T / (16 * MB) + (a.g.E < a.g.T ? a.g.E : a.g.T);
-    const int64_t grid = blocks * ceil_div(a.N, 16 * NB);
-    if (grid > kW4MaxGrid) return GF_ERR_INVALID_ARG;
-    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(WAVES * 64), LDS, stream, a);
-    return w4_status(hipGetLastError());
-}
-
 template <class Cfg, int GROUP, bool WINDOW, bool GROUPED>
 int launch_tile_of(const W4Args& a, hipStream_t stream)
 {
@@ -121,7 +103,7 @@ int launch_tile_of(const W4Args& a, hipStream_t stream)
 template <class Cfg, int GROUP, bool GROUPED>
 int launch_tile(const W4Args& a, hipStream_t stream)
 {
-    if (a.K % 256 == 0 && w4_aligned(a.S, 16) && w4_aligned(a.Z, 8))
+    if (a.K % 256 == 0)
         return launch_tile_of<Cfg, GROUP, true, GROUPED>(a, stream);
     return launch_tile_of<Cfg, GROUP, false, GROUPED>(a, stream);
 }
@@ -130,17 +112,12 @@ template <class Cfg, bool GROUPED>
 int launch_rows(const W4Args& a, hipStream_t stream)
 {
     auto kern = w4_rows_kernel<Cfg, GROUPED>;
-    static std::atomic<uint64_t> lds_opt_in{0};
-    const int lds = Cfg::RED_BYTES + (Cfg::XLDS ? a.M * (a.K + Cfg::XPAD) * 2 : 0);
-    if (lds > 64 * 1024) {
-        const hipError_t e = opt_in_lds((const void*)kern, 160 * 1024, lds_opt_in, stream);
-        if (e != hipSuccess) return GF_ERR_HIP;
-    }
+    static_assert(Cfg::LDS_BYTES <= 64 * 1024, "no opt-in for large LDS");
     int64_t blocks = ceil_div(a.M, 16 * Cfg::MB);
     if (GROUPED) blocks = a.g.T / (16 * Cfg::MB) + (a.g.E < a.g.T ? a.g.E : a.g.T);
     const int64_t grid = blocks * ceil_div(a.N, 16 * Cfg::NB);
     if (grid > kW4MaxGrid) return GF_ERR_INVALID_ARG;
-    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(Cfg::WAVES * 64), lds, stream, a);
+    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(Cfg::WAVES * 64), Cfg::LDS_BYTES, stream, a);
     return w4_status(hipGetLastError());
 }
 
@@ -163,24 +140,16 @@ int launch_band(const W4Args& a, int ring, int parts, hipStream_t stream)
     return w4_status(hipGetLastError());
 }
 
-template <int GROUP, int MB, int NB, bool GROUPED>
-int stream_by_alignment(const W4Args& a, hipStream_t stream)
-{
-    const bool avec = w4_aligned(a.A, 16), qvec = avec && w4_aligned(a.Q, 16) && a.K % 32 == 0;
-    if (qvec) return launch_stream<GROUP, MB, NB, true, true, GROUPED>(a, stream);
-    if (avec) return launch_stream<GROUP, MB, NB, false, true, GROUPED>(a, stream);
-    return launch_stream<GROUP, MB, NB, false, false, GROUPED>(a, stream);
-}
-
 // The band form's launch.  Two workgroups to a CU, with as much in flight as
-// their LDS leaves, where there are row groups for them; else one with all of it.
+// their LDS leaves, where there are row groups for them and the registers allow
+// it (not with A in registers); else one with all of it.
 template <class Cfg, bool GROUPED>
 int band(const W4Args& a, hipStream_t stream)
 {
     const int fixed = 2 * Cfg::WAVES * (GROUPED ? 16 * Cfg::MB : a.M) * 64 + (Cfg::XLDS ? a.M * a.K * 2 : 0);
     const int per_task = Cfg::WAVES * Cfg::TASK_BYTES;
     const int64_t groups = (int64_t)ceil_div(a.N, 16) * (GROUPED ? a.g.E : 1);
-    const int per_cu = groups > 256 && fixed + per_task <= 80 * 1024 ? 2 : 1;
+    const int per_cu = Cfg::XLDS && groups > 256 && fixed + per_task <= 80 * 1024 ? 2 : 1;
     int ring = (160 * 1024 / per_cu - fixed) / per_task;
     const int blocks = ceil_div(a.K, Cfg::BK * Cfg::WAVES);        // of a wave, in one row group
     const int64_t tasks = ceil_div((int)(groups < (1 << 30) ? groups : 1 << 30), 256 * per_cu) * (int64_t)blocks;
@@ -196,25 +165,25 @@ template <int GROUP, bool GROUPED>
 int product(const W4Args& a, hipStream_t stream)
 {
     const int64_t rows = GROUPED ? (a.g.T + a.g.E - 1) / a.g.E : a.M;
-    const bool aq = w4_aligned(a.A, 16) && w4_aligned(a.Q, 16), wide = aq && w4_aligned(a.S, 16) && w4_aligned(a.Z, 8);
-    if (rows > 64 && aq && a.K % 32 == 0 && a.K >= 64) {
+    const bool wide = w4_aligned(a.A, 16) && w4_aligned(a.Q, 16) && w4_aligned(a.S, 16) && w4_aligned(a.Z, 8);
+    if (rows > 64 && w4_aligned(a.A, 16) && a.K >= 64) {
         const int64_t blocks = GROUPED ? a.g.T / 256 + a.g.E : ceil_div(a.M, 256);
         if (blocks * ceil_div(a.N, 256) >= 192) return launch_tile<W4TileCfg<4, 2, 2, 4, 4>, GROUP, GROUPED>(a, stream);
         return launch_tile<W4TileCfg<2, 1, 1, 4, 4>, GROUP, GROUPED>(a, stream);
     }
     if (wide && a.K % 512 == 0 && a.K > 0 && a.N >= 16) {
         if constexpr (!GROUPED)
-            if (a.M * a.K <= 32768 && a.M <= 16) return band<W4BandCfg<GROUP, 1, 0>, false>(a, stream);
+            if (a.M <= 16 && a.M * a.K <= 32768) return band<W4BandCfg<GROUP, 1, 0>, false>(a, stream);
         if (rows <= 16 && a.K <= 4096) return band<W4BandCfg<GROUP, 1, 1>, GROUPED>(a, stream);
         if (rows <= 16 && a.K <= 8192) return band<W4BandCfg<GROUP, 1, 2>, GROUPED>(a, stream);
         if (rows <= 32 && a.K <= 4096) return band<W4BandCfg<GROUP, 2, 1>, GROUPED>(a, stream);
     }
-    if (wide && a.K % 256 == 0 && a.K > 0) {
-        if (rows <= 16) return launch_rows<W4RowsCfg<GROUP, 1, 1, 8, 2, false>, GROUPED>(a, stream);
-        return launch_rows<W4RowsCfg<GROUP, 2, 2, 8, 2, false>, GROUPED>(a, stream);
-    }
-    if (rows <= 16) return stream_by_alignment<GROUP, 1, 2, GROUPED>(a, stream);
-    return stream_by_alignment<GROUP, 2, 2, GROUPED>(a, stream);
+    constexpr int CB = GROUP == 32 ? 2 : 4;
+    if (rows <= 16)
+        return a.N >= 8192 ? launch_rows<W4RowsCfg<GROUP, 1, 2, 8, CB>, GROUPED>(a, stream)
+                           : launch_rows<W4RowsCfg<GROUP, 1, 1, 8, CB>, GROUPED>(a, stream);
+    if (rows > 32 && a.N >= 8192) return launch_rows<W4RowsCfg<GROUP, 2, 4, 4, 2>, GROUPED>(a, stream);
+    return launch_rows<W4RowsCfg<GROUP, 2, 2, 8, CB>, GROUPED>(a, stream);
 }
 
 template <bool GROUPED>

@@ -299,211 +299,68 @@ __device__ __forceinline__ half2v w4_minus(uint32_t z)
     return __builtin_bit_cast(half2v, z * 0x00010001u | 0x80008000u);
 }
 
-constexpr float kW4Unit = 16777216.0f;   // 2^24: one code step, as a subnormal, is its reciprocal
-
-// Row-streaming product for few rows of A.  A workgroup owns 16 * NB rows of
-// Q and up to 16 * MB rows of A; its waves split K into chunks of 128, each
-// wave multiplying 16 x 16 x 32 MFMA steps, and their partial sums are added
-// in wave order through LDS (a fixed order: results repeat bit for bit).
-// A lane's 16-byte load of Q holds 32 consecutive k of one row.  An MFMA step
-// sums over the four lanes of a row, and has to stay within one group: with
-// groups of 128 the whole chunk is one group and step i takes word i of each
-// lane; with shorter groups the four words of four lanes are exchanged first
-// (two rounds of lane swaps), so that step i holds k = 32 i .. 32 i + 31.
-// Out of range: rows of Q and A are clamped (the results are not stored), k
-// past K multiplies a zeroed A.
-template <int GROUP, int MB, int NB, int WAVES, bool QVEC, bool AVEC, bool GROUPED>
-__global__ __launch_bounds__(WAVES * 64) void w4_stream_kernel(W4Args a)
+// Word i of the lane with c4 = j to word j of the lane with c4 = i, among the four
+// lanes c4 * 16 + r of each r.
+__device__ __forceinline__ u32x4 w4_exchange(u32x4 q)
 {
-#if defined(__HIP_DEVICE_COMPILE__)
-    constexpr int CK = 128;
-    constexpr bool SWAP = QVEC && GROUP < 128;
-    constexpr bool BY_LANE = QVEC && GROUP == 128;      // step i: word i of each lane
-    extern __shared__ __attribute__((aligned(16))) char w4_smem[];
-    GF_LDS float* red = (GF_LDS float*)w4_smem;
-
-    const int lane = threadIdx.x % kWave;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int r16 = lane % 16, c4 = lane / 16;
-    const int tiles_n = ceil_div(a.N, 16 * NB);
-    int tm, tn, M = a.M;
-    if constexpr (GROUPED) {
-        int e, lo, hi, item;
-        if (!a.g.template find<16 * MB>(blockIdx.x, tiles_n, e, lo, hi, item)) return;
-        M = hi - lo;
-        a.A += (size_t)lo * a.K;
-        a.C += (size_t)lo * a.N;
-        a.Q += (size_t)e * a.N * (a.K / 8);
-        a.S += (size_t)e * a.N * a.G;
-        if (a.Z) a.Z += (size_t)e * a.N * a.G;
-        tm = item % ceil_div(M, 16 * MB);
-        tn = item / ceil_div(M, 16 * MB);
-    } else {
-        tm = blockIdx.x / tiles_n;
-        tn = blockIdx.x % tiles_n;
-    }
-    const int m0 = tm * 16 * MB, n0 = tn * 16 * NB;
-    const int K = a.K, nch = ceil_div(K, CK);
-
-    const uint32_t* qrow[NB];
-    int srow[NB];
-    const uint16_t* arow[MB];
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        const int n = min(n0 + 16 * b + r16, a.N - 1);
-        qrow[b] = a.Q + (size_t)n * (K / 8);
-        srow[b] = n * a.G;
-    }
-#pragma unroll
-    for (int b = 0; b < MB; ++b) arow[b] = a.A + (size_t)min(m0 + 16 * b + r16, M - 1) * K;
-
-    struct Chunk {
-        u32x4 q[NB], x[MB][4];
-    };
-    auto load = [&](int ch, Chunk& c) __attribute__((always_inline)) {
-        const int k0 = ch * CK;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            if constexpr (QVEC) {
-                const int k = min(k0 + 32 * c4, K - 32);
-                c.q[b] = __builtin_nontemporal_load((const u32x4*)(qrow[b] + k / 8));
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) c.q[b][i] = qrow[b][min(k0 + 32 * i + 8 * c4, K - 8) / 8];
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int k = k0 + (BY_LANE ? 32 * c4 + 8 * i : 32 * i + 8 * c4);
-#pragma unroll
-            for (int b = 0; b < MB; ++b) {
-                u32x4 v = {0u, 0u, 0u, 0u};
-                if (k < K) {
-                    if constexpr (AVEC) {
-                        v = *(const u32x4*)(arow[b] + k);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            v[e] = arow[b][k + 2 * e] | ((uint32_t)arow[b][k + 2 * e + 1] << 16);
-                    }
-                }
-                c.x[b][i] = v;
-            }
-        }
-    };
-
-    floatx4 acc[MB][NB] = {};
-    constexpr int SPG = GROUP / 32;                     // MFMA steps per group
-    auto compute = [&](int ch, Chunk& c) __attribute__((always_inline)) {
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            u32x4 q = c.q[nb];
-            if constexpr (SWAP) {
-                u32x2 p = __builtin_amdgcn_permlane32_swap(q[0], q[2], false, false);
-                u32x2 r = __builtin_amdgcn_permlane32_swap(q[1], q[3], false, false);
-                u32x2 s = __builtin_amdgcn_permlane16_swap(p[0], r[0], false, false);
-                u32x2 t = __builtin_amdgcn_permlane16_swap(p[1], r[1], false, false);
-                q = u32x4{s[0], s[1], t[0], t[1]};
-            }
-#pragma unroll
-            for (int g0 = 0; g0 < 4 / SPG; ++g0) {
-                const int g = ch * (CK / GROUP) + g0;
-                const bool in = g < a.G;
-                const int at = srow[nb] + (in ? g : a.G - 1);
-                // past the last group: a scale of 0, not another group's (which may be infinite)
-                const float s = in ? f16_bits_to_f32(a.S[at]) * kW4Unit : 0.0f;
-                const half2v nz = w4_minus(a.Z ? a.Z[at] : 8u);
-                floatx4 part[MB] = {};
-#pragma unroll
-                for (int i = g0 * SPG; i < (g0 + 1) * SPG; ++i) {
-                    const half8 w = w4_unpack(q[i], nz);
-#pragma unroll
-                    for (int b = 0; b < MB; ++b)
-                        part[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, c.x[b][i]), w,
-                                                                             part[b], 0, 0, 0);
-                }
-#pragma unroll
-                for (int b = 0; b < MB; ++b)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[b][nb][i] = fmaf(part[b][i], s, acc[b][nb][i]);
-            }
-        }
-    };
-
-    if (wave < nch) {
-        Chunk c0, c1;
-        load(wave, c0);
-        int ch = wave;
-        for (; ch + WAVES < nch; ch += 2 * WAVES) {
-            load(ch + WAVES, c1);
-            compute(ch, c0);
-            if (ch + 2 * WAVES < nch) load(ch + 2 * WAVES, c0);
-            compute(ch + WAVES, c1);
-        }
-        if (ch < nch) compute(ch, c0);
-    }
-
-    // ---- the waves' sums, in wave order ----
-    constexpr int PER_WAVE = MB * NB * 256;             // floats
-#pragma unroll
-    for (int b = 0; b < MB; ++b)
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                red[wave * PER_WAVE + ((b * NB + nb) * 4 + i) * 64 + lane] = acc[b][nb][i];
-    __syncthreads();
-    for (int t = threadIdx.x; t < PER_WAVE; t += WAVES * 64) {
-        const int n = t % (16 * NB), m = t / (16 * NB);            // within the tile
-        const int at = (((m / 16) * NB + n / 16) * 4 + m % 4) * 64 + (m % 16) / 4 * 16 + n % 16;
-        float s = 0.0f;
-#pragma unroll
-        for (int w = 0; w < WAVES; ++w) s += red[w * PER_WAVE + at];
-        if (m0 + m < M && n0 + n < a.N) a.C[(size_t)(m0 + m) * a.N + n0 + n] = f32_to_f16_bits(s);
-    }
-#endif
+    const u32x2 p = __builtin_amdgcn_permlane32_swap(q[0], q[2], false, false);
+    const u32x2 r = __builtin_amdgcn_permlane32_swap(q[1], q[3], false, false);
+    const u32x2 s = __builtin_amdgcn_permlane16_swap(p[0], r[0], false, false);
+    const u32x2 t = __builtin_amdgcn_permlane16_swap(p[1], r[1], false, false);
+    return u32x4{s[0], s[1], t[0], t[1]};
 }
 
-// The same product where rows of Q, S and Z can be read in wide pieces: K % 256
-// == 0, A and Q 16-byte, S 16-byte and Z 8-byte aligned.
-// What bounds it is not only the bytes: each row that a load touches is a cache
-// line of its own, and a line costs its cycle whether 2 or 64 bytes of it are
-// used.  So the waves take K in blocks of CB chunks of 128 (block b goes to wave
-// b % WAVES), and load a block's scales and zero points with one instruction
-// each; the next block is in flight while one is multiplied.  XLDS: A (few rows,
-// read by every wave through LDS) is copied there once, rows padded by 16 bytes;
-// otherwise each wave loads its own chunks of A one chunk ahead.
-template <int GROUP_, int MB_, int NB_, int WAVES_, int CB_, bool XLDS_>
-struct W4RowsCfg {
-    static constexpr int GROUP = GROUP_, MB = MB_, NB = NB_, WAVES = WAVES_, CB = CB_;
-    static constexpr bool XLDS = XLDS_;
-    static constexpr int BK = 128 * CB;                  // k per block
-    static constexpr int SW = BK / GROUP / 2;            // registers of a block's scales
-    static constexpr int ZW = (BK / GROUP + 3) / 4;      // and zero points
-    static constexpr int RED_BYTES = WAVES * MB * NB * 256 * 4;
-    static constexpr int XPAD = 8;                       // fp16 between rows of A in LDS
-};
+constexpr float kW4Unit = 16777216.0f;   // 2^24: one code step, as a subnormal, is its reciprocal
+
+// Loads of wider words than their addresses are aligned to (the hardware takes
+// any alignment; the compiler has to be told).
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef u32x2 u32x2_any __attribute__((aligned(1)));
+typedef uint32_t u32_any __attribute__((aligned(1)));
+typedef uint16_t u16_any __attribute__((aligned(1)));
 
 // N consecutive 32-bit words (N = 1, 2, 4 or 8), or a 16-bit one for N = 0.
 template <int N>
 __device__ __forceinline__ void load_words(const void* p, uint32_t* v)
 {
     if constexpr (N == 0) {
-        v[0] = *(const uint16_t*)p;
+        v[0] = *(const u16_any*)p;
     } else if constexpr (N == 1) {
-        v[0] = *(const uint32_t*)p;
+        v[0] = *(const u32_any*)p;
     } else if constexpr (N == 2) {
-        const u32x2 t = *(const u32x2*)p;
+        const u32x2 t = *(const u32x2_any*)p;
         v[0] = t[0]; v[1] = t[1];
     } else {
 #pragma unroll
-        for (int i = 0; i < N / 4; ++i) {
-            const u32x4 t = ((const u32x4*)p)[i];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[4 * i + e] = t[e];
-        }
+        for (int i = 0; i < N / 2; ++i) load_words<2>((const u32x2_any*)p + i, v + 2 * i);
     }
 }
+
+// The general product for few rows of A: any K (a multiple of 8), N and
+// alignment.  A workgroup owns 16 * NB rows of Q and up to 16 * MB rows of A; its
+// waves split K, each multiplying 16 x 16 x 32 MFMA steps, and their partial sums
+// are added in wave order through LDS (a fixed order: results repeat bit for bit).
+// What bounds it is not only the bytes: each row that a load touches is a cache
+// line of its own, and a line costs its cycle whether 2 or 64 bytes of it are
+// used.  So the waves take K in blocks of CB chunks of 128 (block b goes to wave
+// b % WAVES), and load a block's scales and zero points with few instructions;
+// the next block is in flight while one is multiplied, and the next chunk of A.
+// A lane's 16-byte load of Q holds 32 consecutive k of one row.  An MFMA step
+// sums over the four lanes of a row, and has to stay within one group: with
+// groups of 128 the whole chunk is one group and step i takes word i of each
+// lane; with shorter groups the four words of four lanes are exchanged first
+// (two rounds of lane swaps), so that step i holds k = 32 i .. 32 i + 31.
+// What is left of K behind the last block goes chunk by chunk, word by word.
+// Out of range: rows of Q and A are clamped (the results are not stored), k
+// past K multiplies a zeroed A.
+template <int GROUP_, int MB_, int NB_, int WAVES_, int CB_>
+struct W4RowsCfg {
+    static constexpr int GROUP = GROUP_, MB = MB_, NB = NB_, WAVES = WAVES_, CB = CB_;
+    static constexpr int BK = 128 * CB;                  // k per block
+    static constexpr int SW = BK / GROUP / 2;            // registers of a block's scales
+    static constexpr int ZW = (BK / GROUP + 3) / 4;      // and zero points
+    static constexpr int LDS_BYTES = WAVES * MB * NB * 256 * 4;
+};
 
 template <class Cfg, bool GROUPED>
 __global__ __launch_bounds__(Cfg::WAVES * 64) void w4_rows_kernel(W4Args a)
@@ -513,7 +370,6 @@ __global__ __launch_bounds__(Cfg::WAVES * 64) void w4_rows_kernel(W4Args a)
     constexpr int GPB = Cfg::BK / GROUP;                 // groups per block
     extern __shared__ __attribute__((aligned(16))) char w4_smem[];
     GF_LDS float* red = (GF_LDS float*)w4_smem;
-    GF_LDS char* xs = (GF_LDS char*)w4_smem + Cfg::RED_BYTES;
 
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -536,7 +392,7 @@ __global__ __launch_bounds__(Cfg::WAVES * 64) void w4_rows_kernel(W4Args a)
         tn = blockIdx.x % tiles_n;
     }
     const int m0 = tm * 16 * MB, n0 = tn * 16 * NB;
-    const int K = a.K, nblk = K / Cfg::BK;
+    const int K = a.K, nblk = K / Cfg::BK, rest = ceil_div(K - nblk * Cfg::BK, 128);
 
     const uint32_t* qrow[NB];
     int srow[NB];
@@ -544,7 +400,7 @@ __global__ __launch_bounds__(Cfg::WAVES * 64) void w4_rows_kernel(W4Args a)
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
         const int n = min(n0 + 16 * b + r16, a.N - 1);
-        qrow[b] = a.Q + (size_t)n * (K / 8) + c4 * 4;
+        qrow[b] = a.Q + (size_t)n * (K / 8);
         srow[b] = n * a.G;
     }
     struct Block {
@@ -555,8 +411,7 @@ __global__ __launch_bounds__(Cfg::WAVES * 64) void w4_rows_kernel(W4Args a)
 #pragma unroll
         for (int c = 0; c < CB; ++c)
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
-                v.q[c][b] = __builtin_nontemporal_load((const u32x4*)(qrow[b] + (blk * CB + c) * 16));
+            for (int b = 0; b < NB; ++b) v.q[c][b] = *(const u32x4_any*)(qrow[b] + (blk * CB + c) * 16 + c4 * 4);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             load_words<Cfg::SW>(a.S + srow[b] + blk * GPB, v.s[b]);
@@ -570,95 +425,104 @@ __global__ __launch_bounds__(Cfg::WAVES * 64) void w4_rows_kernel(W4Args a)
     constexpr int kstep = GROUP == 128 ? 8 : 32;
     const uint16_t* arow[MB];
 #pragma unroll
-    for (int b = 0; b < MB; ++b) arow[b] = a.A + (size_t)min(m0 + 16 * b + r16, M - 1) * K + koff;
-    const GF_LDS char* xrow = xs + min(r16, M - 1) * (K + Cfg::XPAD) * 2 + koff * 2;
+    for (int b = 0; b < MB; ++b) arow[b] = a.A + (size_t)min(m0 + 16 * b + r16, M - 1) * K;
     half8 x[MB][4];
     auto load_x = [&](int ch, half8 (&v)[MB][4]) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int b = 0; b < MB; ++b) {
-                if constexpr (Cfg::XLDS) v[b][i] = *(const GF_LDS half8*)(xrow + (ch * 128 + kstep * i) * 2);
-                else v[b][i] = *(const half8*)(arow[b] + ch * 128 + kstep * i);
-            }
+            for (int b = 0; b < MB; ++b)
+                v[b][i] = __builtin_bit_cast(half8, (u32x4)*(const u32x4_any*)(arow[b] + koff + ch * 128 + kstep * i));
     };
 
     floatx4 acc[MB][NB] = {};
     constexpr int SPG = GROUP / 32, GPC = 128 / GROUP;   // MFMA steps per group, groups per chunk
+    // One group of one column block: steps g0 * SPG .. of a chunk.
+    auto group = [&](int nb, int g0, const u32x4& q, float s, half2v nz) __attribute__((always_inline)) {
+        floatx4 part[MB] = {};
+#pragma unroll
+        for (int i = g0 * SPG; i < (g0 + 1) * SPG; ++i) {
+            const half8 w = w4_unpack(q[i], nz);
+#pragma unroll
+            for (int b = 0; b < MB; ++b) part[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[b][i], w, part[b], 0, 0, 0);
+        }
+#pragma unroll
+        for (int b = 0; b < MB; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[b][nb][i] = fmaf(part[b][i], s, acc[b][nb][i]);
+    };
     auto multiply = [&](const Block& v, auto c_c) __attribute__((always_inline)) {
         constexpr int c = decltype(c_c)::value;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
             u32x4 q = v.q[c][nb];
-            if constexpr (GROUP < 128) {
-                const u32x2 p = __builtin_amdgcn_permlane32_swap(q[0], q[2], false, false);
-                const u32x2 r = __builtin_amdgcn_permlane32_swap(q[1], q[3], false, false);
-                const u32x2 s = __builtin_amdgcn_permlane16_swap(p[0], r[0], false, false);
-                const u32x2 t = __builtin_amdgcn_permlane16_swap(p[1], r[1], false, false);
-                q = u32x4{s[0], s[1], t[0], t[1]};
-            }
+            if constexpr (GROUP < 128) q = w4_exchange(q);
 #pragma unroll
             for (int g0 = 0; g0 < GPC; ++g0) {
                 const int g = c * GPC + g0;              // within the block
                 const uint16_t sb = (uint16_t)(v.s[nb][g / 2] >> (16 * (g % 2)));
-                const float s = f16_bits_to_f32(sb) * kW4Unit;
                 const half2v nz = w4_minus(a.Z ? (v.z[nb][g / 4] >> (8 * (g % 4))) & 0xffu : 8u);
-                floatx4 part[MB] = {};
-#pragma unroll
-                for (int i = g0 * SPG; i < (g0 + 1) * SPG; ++i) {
-                    const half8 w = w4_unpack(q[i], nz);
-#pragma unroll
-                    for (int b = 0; b < MB; ++b)
-                        part[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[b][i], w, part[b], 0, 0, 0);
-                }
-#pragma unroll
-                for (int b = 0; b < MB; ++b)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[b][nb][i] = fmaf(part[b][i], s, acc[b][nb][i]);
+                group(nb, g0, q, f16_bits_to_f32(sb) * kW4Unit, nz);
             }
+            if constexpr (MB > 1) __builtin_amdgcn_sched_barrier(0);   // unpacked operands of one block at a time
         }
     };
 
     // Blocks are loaded for a clamped number past the wave's last one, so that
     // no load stands under a branch.
-    Block v0, v1;
-    const int last = nblk - 1;
-    load(min(wave, last), v0);
-    if constexpr (Cfg::XLDS) {
-        const int per = K / 8, n = M * per;
-        for (int t = threadIdx.x; t < n; t += WAVES * 64) {
-            const int m = t / per, j = t - m * per;
-            *(GF_LDS u32x4*)(xs + m * (K + Cfg::XPAD) * 2 + j * 16) = *(const u32x4*)(a.A + (size_t)m * K + j * 8);
-        }
-        __syncthreads();
-    } else {
-        load_x(min(wave, last) * CB, x);
-    }
-    auto block = [&](int blk, const Block& v) __attribute__((always_inline)) {
+    auto block = [&](int blk, const Block& v, int last) __attribute__((always_inline)) {
         static_for<CB>([&](auto c_c) __attribute__((always_inline)) {
             constexpr int c = decltype(c_c)::value;
-            if constexpr (Cfg::XLDS) {
-                load_x(blk * CB + c, x);
-                multiply(v, c_c);
-            } else {
-                half8 next[MB][4];
-                load_x(c + 1 < CB ? blk * CB + c + 1 : min(blk + WAVES, last) * CB, next);
-                multiply(v, c_c);
+            half8 next[MB][4];
+            load_x(c + 1 < CB ? blk * CB + c + 1 : min(blk + WAVES, last) * CB, next);
+            multiply(v, c_c);
 #pragma unroll
-                for (int b = 0; b < MB; ++b)
+            for (int b = 0; b < MB; ++b)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) x[b][i] = next[b][i];
-            }
+                for (int i = 0; i < 4; ++i) x[b][i] = next[b][i];
         });
     };
-    int blk = wave;
-    for (; blk + WAVES <= last; blk += 2 * WAVES) {
-        load(blk + WAVES, v1);
-        block(blk, v0);
-        load(min(blk + 2 * WAVES, last), v0);
-        block(blk + WAVES, v1);
+    if (wave < nblk) {
+        const int last = nblk - 1;
+        Block v0, v1;
+        load(wave, v0);
+        load_x(wave * CB, x);
+        int blk = wave;
+        for (; blk + WAVES <= last; blk += 2 * WAVES) {
+            load(blk + WAVES, v1);
+            block(blk, v0, last);
+            load(min(blk + 2 * WAVES, last), v0);
+            block(blk + WAVES, v1, last);
+        }
+        if (blk <= last) block(blk, v0, last);
     }
-    if (blk <= last) block(blk, v0);
+    // ---- the chunks behind the last block ----
+    for (int i = 0; i < rest; ++i) {
+        if ((nblk + i) % WAVES != wave) continue;
+        const int ch = nblk * CB + i, k0 = ch * 128 + 8 * c4;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const int k = k0 + 32 * s;
+#pragma unroll
+            for (int b = 0; b < MB; ++b) {
+                u32x4 v = *(const u32x4_any*)(arow[b] + min(k, K - 8));
+                x[b][s] = __builtin_bit_cast(half8, k < K ? v : u32x4{0u, 0u, 0u, 0u});
+            }
+        }
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            u32x4 q;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) q[s] = qrow[nb][min(k0 + 32 * s, K - 8) / 8];
+#pragma unroll
+            for (int g0 = 0; g0 < GPC; ++g0) {
+                const int g = ch * GPC + g0, at = srow[nb] + min(g, a.G - 1);
+                // past the last group: a scale of 0, not another's (which may be infinite)
+                const float s = g < a.G ? f16_bits_to_f32(a.S[at]) * kW4Unit : 0.0f;
+                group(nb, g0, q, s, w4_minus(a.Z ? a.Z[at] : 8u));
+            }
+        }
+    }
 
     // ---- the waves' sums, in wave order ----
     constexpr int PER_WAVE = MB * NB * 256;             // floats
@@ -877,13 +741,7 @@ __global__ __launch_bounds__(Cfg::WAVES * 64) void w4_band_kernel(W4Args a, int 
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {             // chunks of 128 k
                     u32x4 q = *(const GF_LDS u32x4*)(buf + qat[c]);
-                    if constexpr (GROUP < 128) {
-                        const u32x2 p = __builtin_amdgcn_permlane32_swap(q[0], q[2], false, false);
-                        const u32x2 r = __builtin_amdgcn_permlane32_swap(q[1], q[3], false, false);
-                        const u32x2 s = __builtin_amdgcn_permlane16_swap(p[0], r[0], false, false);
-                        const u32x2 t = __builtin_amdgcn_permlane16_swap(p[1], r[1], false, false);
-                        q = u32x4{s[0], s[1], t[0], t[1]};
-                    }
+                    if constexpr (GROUP < 128) q = w4_exchange(q);
                     constexpr int SPG = GROUP / 32, GPC = 128 / GROUP;
 #pragma unroll
                     for (int g0 = 0; g0 < GPC; ++g0) {
@@ -978,10 +836,10 @@ __global__ __launch_bounds__(Cfg::WAVES * 64) void w4_band_kernel(W4Args a, int 
 //    loads of STAGES - 2 steps are then pending: a count of those alone, since
 //    the compiler may merge or reorder the loads into registers, for which it
 //    waits itself.  Loads are issued for every step, also past the last, and
-//    always of 64 k inside K (so K >= 64): where K ends in half a step, the last
-//    step takes the last 64 k and its first half, done before, as zeros on both
-//    sides.  No load stands under a branch or goes through the flat path: the
-//    compiler would then wait for all of them wherever it needs one.
+//    from inside the rows: where K ends within a step, what lies past it is
+//    cleared once the last step has landed.  No load stands under a branch or
+//    goes through the flat path: the compiler would then wait for all of them
+//    wherever it needs one.
 template <int FM_, int FN_, int WM_, int WN_, int STAGES_>
 struct W4TileCfg {
     static constexpr int FM = FM_, FN = FN_, WM = WM_, WN = WN_, STAGES = STAGES_;
@@ -996,8 +854,8 @@ struct W4TileCfg {
     static_assert(LDS_BYTES <= 160 * 1024, "one CU's LDS");
 };
 
-// WINDOW: K % 256 == 0, S 16-byte and Z 8-byte aligned.  A row of Q, S or Z is
-// a line of its own, so what a lane loads from them costs a line whatever its
+// K >= 64, A 16-byte aligned.  WINDOW: K % 256 == 0.  A row of Q, S or Z is a
+// line of its own, so what a lane loads from them costs a line whatever its
 // width: codes are then loaded two steps at a time and scales and zero points
 // four (a window).  Otherwise step by step.
 template <class Cfg, int GROUP, bool WINDOW, bool GROUPED>
@@ -1038,15 +896,24 @@ __global__ __launch_bounds__(Cfg::NT) void w4_tile_kernel(W4Args a)
         const int slot = r * Cfg::NT + tid, row = slot / 8, c = (slot % 8) ^ (row / 2 % 8);
         voff[r] = ((uint32_t)min(m0 + row, M - 1) * (uint32_t)K + 8u * c) * 2u;
     }
+    // In the last step, chunks past K: the last one inside instead (zeros later).
+    const int last_chunks = (K - (nk - 1) * BK) / 8;
+    uint32_t back[Cfg::LPS];
+#pragma unroll
+    for (int r = 0; r < Cfg::LPS; ++r) {
+        const int slot = r * Cfg::NT + tid, c = (slot % 8) ^ (slot / 16 % 8);
+        back[r] = WINDOW ? 0u : 16u * (uint32_t)max(c - (last_chunks - 1), 0);
+    }
     const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
         (void*)a.A, 0, (int)((uint32_t)M * (uint32_t)K * 2u), 0x00020000);
     auto issue_a = [&](int t, int stage_no) __attribute__((always_inline)) {
         GF_LDS char* stage = smem + stage_no * Cfg::STAGE_BYTES;
-        const uint32_t koff = (uint32_t)__builtin_amdgcn_readfirstlane(min(t * BK, K - BK)) * 2u;
+        const int ts = __builtin_amdgcn_readfirstlane(min(t, nk - 1));
 #pragma unroll
         for (int r = 0; r < Cfg::LPS; ++r)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                ra, (GF_LDS void*)(stage + (r * Cfg::NT + wave * kWave) * 16), 16, voff[r], koff, 0, 0);
+                ra, (GF_LDS void*)(stage + (r * Cfg::NT + wave * kWave) * 16), 16,
+                WINDOW || ts < nk - 1 ? voff[r] : voff[r] - back[r], (uint32_t)ts * (BK * 2), 0, 0);
     };
 
     // ---- codes, scale and zero point of the lane's 32 k in each column block ----
@@ -1068,9 +935,9 @@ __global__ __launch_bounds__(Cfg::NT) void w4_tile_kernel(W4Args a)
     uint32_t sw[WINDOW ? 1 : D][FN][SW], zw[WINDOW ? 1 : D][FN][ZW];
     auto load_codes = [&](int t, auto i_c) __attribute__((always_inline)) {
         constexpr int i = decltype(i_c)::value;
-        const int kc = min(t * BK, K - BK) + 32 * h;
+        const int kc = min(min(t, nk - 1) * BK + 32 * h, K - 32);
 #pragma unroll
-        for (int f = 0; f < FN; ++f) codes[i][f] = *(const u32x4*)(qrow[f] + kc / 8);
+        for (int f = 0; f < FN; ++f) codes[i][f] = *(const u32x4_any*)(qrow[f] + kc / 8);
     };
     auto load_scales = [&](int t, auto i_c) __attribute__((always_inline)) {
         constexpr int i = WINDOW ? 0 : decltype(i_c)::value;
@@ -1078,29 +945,20 @@ __global__ __launch_bounds__(Cfg::NT) void w4_tile_kernel(W4Args a)
         for (int f = 0; f < FN; ++f) {
             if constexpr (WINDOW) {
                 const int at = srow[f] + min(t * BK, K - 4 * BK) / GROUP;
-                if constexpr (GROUP == 128) {
-                    sw[i][f][0] = *(const uint32_t*)(a.S + at);
-                    zw[i][f][0] = *(const uint16_t*)(zsrc + at);
-                } else if constexpr (GROUP == 64) {
-                    const u32x2 v = *(const u32x2*)(a.S + at);
-                    sw[i][f][0] = v[0]; sw[i][f][1] = v[1];
-                    zw[i][f][0] = *(const uint32_t*)(zsrc + at);
-                } else {
-                    const u32x4 v = *(const u32x4*)(a.S + at);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sw[i][f][e] = v[e];
-                    const u32x2 z = *(const u32x2*)(zsrc + at);
-                    zw[i][f][0] = z[0]; zw[i][f][1] = z[1];
-                }
+                load_words<SW>(a.S + at, sw[i][f]);
+                load_words<GROUP == 128 ? 0 : ZW>(zsrc + at, zw[i][f]);
             } else {
-                const int at = srow[f] + (min(t * BK, K - BK) + 32 * h) / GROUP;
+                const int at = srow[f] + min(min(t, nk - 1) * BK + 32 * h, K - 8) / GROUP;
                 sw[i][f][0] = a.S[at];
                 zw[i][f][0] = zsrc[at];
             }
         }
     };
-    // In the last step, whether this lane's 32 k are not those of the step before.
-    const bool last_new = WINDOW || h == 1 || K % BK == 0;
+    // In the last step: whether any of this lane's 32 k lie inside K, and how many
+    // words its codes, loaded from inside the row, are ahead of their place.
+    const int last_k = (nk - 1) * BK + 32 * h;
+    const bool last_some = WINDOW || last_k < K;
+    const int last_ahead = max(last_k - (K - 32), 0) / 8;
     half2v off[FN], sc[FN];
     // Scale and offset of step t, which is step i of the D unrolled.
     auto scale = [&](int t, auto i_c) __attribute__((always_inline)) {
@@ -1109,7 +967,7 @@ __global__ __launch_bounds__(Cfg::NT) void w4_tile_kernel(W4Args a)
         for (int f = 0; f < FN; ++f) {
             uint32_t sb, z;
             if constexpr (!WINDOW) {
-                sb = t < nk - 1 || last_new ? sw[i][f][0] : 0u;
+                sb = t < nk - 1 || last_some ? sw[i][f][0] : 0u;
                 z = zw[i][f][0];
             } else if constexpr (GROUP == 32) {
                 sb = sw[0][f][i % SW] >> (16 * h);
@@ -1177,11 +1035,19 @@ __global__ __launch_bounds__(Cfg::NT) void w4_tile_kernel(W4Args a)
                 wait_vmcnt<Cfg::LPS * (S - 2)>();
                 lds_barrier();                            // step t + 1 has landed; buffer st is free
                 if constexpr (!WINDOW) {
-                    if (K % BK != 0 && t == nk - 2) {     // the last step's first half: zeros
-                        for (int z = tid; z < Cfg::BM * 4; z += Cfg::NT) {
-                            const int row = z / 4, c = (z % 4) ^ (row / 2 % 8);
-                            *(GF_LDS u32x4*)(smem + st1 * Cfg::STAGE_BYTES + row * (BK * 2) + c * 16) =
-                                u32x4{0u, 0u, 0u, 0u};
+                    if (K % BK != 0 && t == nk - 2) {     // the last step's k past K: zeros on both sides
+                        for (int z = tid; z < Cfg::BM * 8; z += Cfg::NT) {
+                            const int row = z / 8, c = z % 8;
+                            if (c >= last_chunks)
+                                *(GF_LDS u32x4*)(smem + st1 * Cfg::STAGE_BYTES + row * (BK * 2) +
+                                                 ((c ^ (row / 2 % 8)) * 16)) = u32x4{0u, 0u, 0u, 0u};
+                        }
+#pragma unroll
+                        for (int f = 0; f < FN; ++f) {
+                            u32x4 q = codes[i1][f];
+                            if (last_ahead & 1) q = u32x4{q[1], q[2], q[3], 0u};
+                            if (last_ahead & 2) q = u32x4{q[2], q[3], 0u, 0u};
+                            codes[i1][f] = q;             // (a lane wholly past K has a scale of 0)
                         }
                         lds_barrier();
                     }

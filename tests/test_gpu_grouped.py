@@ -132,7 +132,9 @@ def test_grouped_tn(f32, route, N, K):
 @pytest.mark.parametrize("zeros", [True, False])
 @pytest.mark.parametrize("route,N,K", [("one", 40, 72), ("token", 136, 264), ("few", 200, 512), ("few", 33, 136),
                                        ("mid", 136, 256), ("many", 40, 96), ("sixty-five", 16, 32),
-                                       ("big", 264, 160), ("big", 3000, 96), ("none", 16, 32)])
+                                       ("big", 264, 160), ("big", 3000, 96), ("none", 16, 32), ("few", 200, 1024),
+                                       ("few", 33, 4608), ("many", 40, 512), ("token", 100, 8192),
+                                       ("mid", 70, 264), ("big", 264, 168), ("sixty-four", 40, 1024)])
 def test_w4_grouped(route, N, K, group, zeros):
     sizes, off, T = _route(route)
     E, G = len(sizes), plain.groups_of(K, group)

@@ -147,7 +147,9 @@ def _extra(A, absum):
 
 SHAPES = [(1, 1, 8), (1, 16, 32), (1, 100, 4096), (2, 33, 136), (3, 64, 1000), (15, 15, 256), (16, 48, 128),
           (17, 31, 640), (33, 130, 2056), (64, 64, 2048), (65, 200, 1024), (130, 77, 512), (200, 300, 416),
-          (66, 40, 32), (300, 520, 160), (1700, 7000, 96)]
+          (66, 40, 32), (300, 520, 160), (1700, 7000, 96), (1, 50, 5128), (20, 8200, 264), (50, 8200, 520),
+          (65, 70, 64), (90, 40, 72), (100, 150, 104), (130, 140, 1112), (1700, 7000, 120), (1, 16, 1536),
+          (1, 8200, 1024), (16, 9000, 512), (9, 33, 8192), (12, 2000, 4608), (32, 130, 4096), (5, 17, 512)]
 
 
 @pytest.mark.parametrize("group", [32, 64, 128])
@@ -181,7 +183,7 @@ def test_gemm_w4_off_the_16_byte_grid(M, shift_a, shift_q):
 
 @pytest.mark.parametrize("M", [1, 4, 30, 70, 300])
 @pytest.mark.parametrize("group", [32, 128])
-@pytest.mark.parametrize("K", [8 * 37, 32 * 9])           # both with a short last group
+@pytest.mark.parametrize("K", [8 * 37, 32 * 9, 512])      # the first two with a short last group
 def test_gemm_w4_infinities_and_nan(M, group, K):
     """An infinite or NaN entry of A or S shows in its row or column as the
     formula has it, and nowhere else; the group behind the last is not read."""
