@@ -27,13 +27,14 @@
 //  * Workgroup order: optional XCD-aware remap plus grouped (panel) order.
 //  * Epilogues: fp16 C through a per-wave LDS transpose and 128-bit stores;
 //    fp32 atomic add (split-K); fp32 plain stores into a slice workspace
-//    (deterministic two-pass split-K).
+//    (deterministic two-pass split-K); fp32 C through LDS and 128-bit stores
+//    (grouped weight gradients).
 #pragma once
 #include "common.hpp"
 
 namespace gf {
 
-enum Epi { EPI_F16 = 0, EPI_F32_ATOMIC = 1, EPI_F32_STORE = 2 };
+enum Epi { EPI_F16 = 0, EPI_F32_ATOMIC = 1, EPI_F32_STORE = 2, EPI_F32_ROWS = 3 };
 
 struct GemmArgs {
     const uint16_t* A;
@@ -972,6 +973,44 @@ __global__ __launch_bounds__(Cfg::NT) void gemm_nt_kernel(Args a)
                     if (grow < a.M && gcol < a.N)
                         unsafeAtomicAdd(C + (size_t)grow * a.N + gcol, acc[fm][fn][i]);
                 }
+    } else if constexpr (EPI == EPI_F32_ROWS) {
+        // One row of MFMA blocks at a time through LDS, so that a store
+        // instruction writes whole rows of the sub-tile, 16 bytes a lane.
+        constexpr int LDW = Cfg::WTN + 4;        // floats per LDS row
+        static_assert(Cfg::NWAVES * MT * LDW * 4 <= Cfg::LDS_BYTES, "the epilogue's LDS");
+        float* C = (float*)a.C;
+        lds_barrier();                           // operand buffers are free now
+        GF_LDS float* reg = (GF_LDS float*)(smem + wave * (MT * LDW * 4));
+        constexpr int CPR = Cfg::WTN / 4, ITERS = MT * CPR / kWave;
+        const bool vec_ok = ALIGNED && a.N % 4 == 0;
+#pragma unroll
+        for (int fm = 0; fm < Cfg::FM; ++fm) {
+#pragma unroll
+            for (int fn = 0; fn < Cfg::FN; ++fn)
+#pragma unroll
+                for (int i = 0; i < MF::NACC; ++i)
+                    reg[MF::row(i, lane) * LDW + fn * MT + lane % MT] = acc[fm][fn][i];
+            asm volatile("" ::: "memory");
+            wait_lgkmcnt0();
+#pragma unroll
+            for (int it = 0; it < ITERS; ++it) {
+                const int q = it * kWave + lane;
+                const int r = q / CPR, cc = q % CPR;
+                const floatx4 v = *(const GF_LDS floatx4*)(reg + r * LDW + cc * 4);
+                const int grow = wrow0 + fm * MT + r, gcol = wcol0 + cc * 4;
+                if (grow >= a.M) continue;
+                float* dst = C + (size_t)grow * a.N + gcol;
+                if (vec_ok && gcol + 4 <= a.N) {
+                    __builtin_nontemporal_store(v, (floatx4*)dst);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (gcol + e < a.N) dst[e] = v[e];
+                }
+            }
+            asm volatile("" ::: "memory");
+            wait_lgkmcnt0();
+        }
     } else {
         float* W = (float*)a.C + (size_t)slice * a.M * a.N;
 #pragma unroll

@@ -35,6 +35,53 @@ int run_rows(GroupRowArgs a, bool al, hipStream_t stream)
     return e == hipSuccess ? GF_OK : GF_ERR_HIP;
 }
 
+template <class Cfg>
+int run_band(const GroupRowArgs& a, hipStream_t stream)
+{
+    // Two workgroups to a CU (two tasks in flight a wave), about 256 of them in
+    // all but at least 16 a group (most groups of a decode batch have rows, and
+    // uneven ones leave a tail).
+    const int64_t want = 256 / a.g.E, blocks = ceil_div(a.N, 16);
+    int64_t parts = want < 16 ? 16 : (want > 64 ? 64 : want);
+    if (parts > blocks) parts = blocks;
+    if (parts * a.g.E > kGroupMaxGrid) return GF_ERR_INVALID_ARG;
+    const hipError_t e = launch_group_band<Cfg>(a, 2, (int)parts, stream);
+    return e == hipSuccess ? GF_OK : GF_ERR_HIP;
+}
+
+// The launch for T rows over E groups, of which only the mean is known.  Timed
+// side by side with B rotated through HBM (us):
+//  * a handful of rows a group, K-contiguous B: the streaming form, 36 against
+//    57 for every tile at T = 48, E = 16, 4096 x 2048; 41 against 59 at T = 16,
+//    E = 8, 4096 x 4096; 11 against 20 at T = 18, E = 17, 488 x 2672.  At a mean
+//    of 19 the 64 x 64 tile is ahead of it (34 against 39);
+//  * then 64 x 64 up to a mean of 64 (64 against 68 at T = 500, E = 16), 128 x 128
+//    with three stages beyond (45 against 56 at T = 1111, E = 8, 2048 x 4096);
+//  * 256 x 256 where the groups fill several of them and they fill the CUs (296
+//    against 327 at T = 8191, E = 8, 4096 x 4096; 97 against 111 for K x N B at
+//    T = 4096);
+//  * K x N B (transposing reads, which the one-wave-per-SIMD tiles have): 128 x
+//    128 for everything smaller (45 against 57 at T = 48, E = 16).
+template <int LB>
+int rows_dispatch(const GroupRowArgs& a, bool al, hipStream_t stream)
+{
+    const int64_t mean = (int64_t)a.g.T / a.g.E;
+    if constexpr (LB == 0) {
+        if (al && mean <= 12 && a.N >= 16 && a.K > 0) {
+            if (mean > 4 && a.K <= 4096)
+                return a.K <= 2048 ? run_band<GroupBandCfg<2, 2>>(a, stream) : run_band<GroupBandCfg<2, 4>>(a, stream);
+            if (a.K <= 2048) return run_band<GroupBandCfg<1, 2>>(a, stream);
+            if (a.K <= 4096) return run_band<GroupBandCfg<1, 4>>(a, stream);
+            if (a.K <= 8192) return run_band<GroupBandCfg<1, 8>>(a, stream);
+        }
+    }
+    if (mean >= 192 && ((int64_t)a.g.T / 256) * ceil_div(a.N, 256) >= 128)
+        return run_rows<GemmCfg<256, 256, 64, 2, 256, 2, 0, LB>>(a, al, stream);
+    if constexpr (LB == 0)
+        if (mean < 64) return run_rows<GemmCfg<64, 64, 64, 3, 256, 0, 0, 0>>(a, al, stream);
+    return run_rows<GemmCfg<128, 128, 64, 3, 256, 2, 0, LB>>(a, al, stream);
+}
+
 // LB: 0 for B[e] N x K, 1 for K x N.
 template <int LB>
 int rows_impl(const void* A, const void* B, void* C, const int* offsets, int T, int E, int N, int K,
@@ -54,11 +101,7 @@ int rows_impl(const void* A, const void* B, void* C, const int* offsets, int T, 
     a.c_bytes = 2;
     const bool al = g_aligned(A, 16) && g_aligned(B, 16) && g_aligned(C, 16) && K % 8 == 0 &&
                     (LB == 0 || N % 8 == 0);
-    const int64_t mean = (int64_t)T / E;
-    if (mean >= 192 && ((int64_t)T / 256) * ceil_div(N, 256) >= 128)
-        return run_rows<GemmCfg<256, 256, 64, 2, 256, 2, 0, LB>>(a, al, stream);
-    if (mean >= 64) return run_rows<GemmCfg<128, 128, 64, 2, 256, 2, 0, LB>>(a, al, stream);
-    return run_rows<GemmCfg<64, 128, 64, 2, 256, 2, 0, LB>>(a, al, stream);
+    return rows_dispatch<LB>(a, al, stream);
 }
 
 template <class Cfg>
@@ -68,8 +111,8 @@ int run_depth(GroupDepthArgs a, bool al, bool f32, hipStream_t stream)
     if (grid > kGroupMaxGrid) return GF_ERR_INVALID_ARG;
     hipError_t e;
     if (f32)
-        e = al ? launch_grouped<Cfg, EPI_F32_STORE, true>(a, grid, stream)
-               : launch_grouped<Cfg, EPI_F32_STORE, false>(a, grid, stream);
+        e = al ? launch_grouped<Cfg, EPI_F32_ROWS, true>(a, grid, stream)
+               : launch_grouped<Cfg, EPI_F32_ROWS, false>(a, grid, stream);
     else
         e = al ? launch_grouped<Cfg, EPI_F16, true>(a, grid, stream)
                : launch_grouped<Cfg, EPI_F16, false>(a, grid, stream);

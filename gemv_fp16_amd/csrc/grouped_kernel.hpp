@@ -154,4 +154,160 @@ hipError_t launch_grouped(Args a, int64_t grid, hipStream_t stream)
     return hipGetLastError();
 }
 
+// ---------------------------------------------------------------------------
+// few rows a group: stream the weights
+// ---------------------------------------------------------------------------
+//
+// C[r] = A[r] . B[e]^T where a group has a handful of rows: bound by B's bytes.
+// Workgroup p of `parts` of group e walks the 16-row blocks of B[e] grid-stride
+// (the last one is the last 16 rows, some a second time), once for every
+// 16 * MB rows of A.  Its 8 waves split K in tasks of 128 k; a task's 16 rows of
+// 256 bytes go to LDS by direct loads of whole cache lines, `ring` tasks in
+// flight a wave, and are read from there as MFMA operands (chunk c of row n at
+// slot c ^ n: the 16 rows read together lie in different banks).  Each wave keeps
+// its part of A in registers (XB tasks' worth), so nothing else is loaded in the
+// loop and no wave waits for another's loads.  Each row block ends in one
+// barrier; the waves' sums are added in wave order, in slots that alternate.
+// k past K: A's registers hold zeros, B's chunks are read from 16 zero bytes.
+// K % 8 == 0, N >= 16, A and B 16-byte aligned.
+// 16 groups of 4096 x 2048, 48 rows over 14 of them: 36 us, 6.5 TB/s of the 6.6
+// that a plain read reaches (tiles: 57 us; what they measured is in grouped.hip).
+template <int MB_, int XB_>
+struct GroupBandCfg {
+    static constexpr int MB = MB_, XB = XB_, WAVES = 8, BK = 128, LOADS = 4, TASK_BYTES = 4096, MAX_RING = 4;
+    static constexpr int RED_BYTES = 2 * WAVES * 16 * MB * 16 * 4;
+    static constexpr int lds_bytes(int ring) { return WAVES * ring * TASK_BYTES + RED_BYTES; }
+};
+
+template <class Cfg>
+__global__ __launch_bounds__(Cfg::WAVES * 64) void group_band_kernel(GroupRowArgs a, int ring, int parts)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    constexpr int MB = Cfg::MB, XB = Cfg::XB, WAVES = Cfg::WAVES, L = Cfg::LOADS, MR = 16 * MB;
+    extern __shared__ __attribute__((aligned(1024))) char smem_raw[];
+    const int lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int r16 = lane % 16, c4 = lane / 16;
+    const int N = a.N, K = a.K;
+    const int e = blockIdx.x / parts, part = blockIdx.x - e * parts;
+    int lo, hi;
+    a.g.rows(e, lo, hi);
+    const int rows = __builtin_amdgcn_readfirstlane(hi - lo);
+    if (rows == 0) return;
+    const uint16_t* A = a.A + (size_t)lo * K;
+    const uint16_t* B = a.B + (size_t)e * N * K;
+    uint16_t* C = (uint16_t*)a.C + (size_t)lo * N;
+
+    GF_LDS char* tasks = (GF_LDS char*)smem_raw + wave * ring * Cfg::TASK_BYTES;
+    GF_LDS float* red = (GF_LDS float*)((GF_LDS char*)smem_raw + WAVES * ring * Cfg::TASK_BYTES);
+    const int nblk = ceil_div(K, Cfg::BK);
+    const int b0 = wave * nblk / WAVES, nb = (wave + 1) * nblk / WAVES - b0;   // this wave's tasks per row block
+    const int blocks = ceil_div(N, 16);
+    const int ng = (blocks - part + parts - 1) / parts;
+    const int ntasks = ng * nb;
+
+    uint32_t boff[4], bat[4];                             // direct loads' sources; operands' places
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 4 * i + c4;
+        boff[i] = (uint32_t)r * (uint32_t)K + (uint32_t)(r16 ^ r) * 8u;
+        bat[i] = (uint32_t)(r16 * 256 + (((4 * i + c4) ^ r16) * 16));
+    }
+    for (int m0 = 0; m0 < rows; m0 += MR) {
+        const int M = min(rows - m0, MR);
+        int ig = part, ib = 0, islot = 0, issued = 0;     // the next task to issue
+        auto issue = [&]() __attribute__((always_inline)) {
+            GF_LDS char* buf = tasks + islot * Cfg::TASK_BYTES;
+            const int k0 = (b0 + ib) * Cfg::BK;
+            const uint16_t* src = B + (size_t)min(ig * 16, N - 16) * K + k0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const void* p = src + boff[i];
+                if (k0 + Cfg::BK > K && k0 + (r16 ^ (4 * i + c4)) * 8 >= K) p = (const void*)g_zero16;
+                __builtin_amdgcn_global_load_lds(p, (GF_LDS void*)(buf + i * 1024), 16, 0, 2);
+            }
+            ++issued;
+            if (++ib == nb) { ib = 0; ig += parts; }
+            if (++islot == ring) islot = 0;
+        };
+        auto wait_tasks = [&](int left) __attribute__((always_inline)) {   // younger tasks that may be pending
+            left = __builtin_amdgcn_readfirstlane(left);
+            if (left >= 3) wait_vmcnt<3 * L>();
+            else if (left == 2) wait_vmcnt<2 * L>();
+            else if (left == 1) wait_vmcnt<L>();
+            else wait_vmcnt<0>();
+        };
+        const int first = min(ring, ntasks);
+        for (int i = 0; i < first; ++i) issue();
+        half8 x[XB * 4][MB];
+#pragma unroll
+        for (int b = 0; b < XB; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int m = 0; m < MB; ++m) {
+                    const int k = (b0 + b) * Cfg::BK + 32 * i + 8 * c4;
+                    const half8 v = *(const half8*)(A + (size_t)(m0 + min(16 * m + r16, M - 1)) * K + min(k, K - 8));
+                    x[b * 4 + i][m] = k < K ? v : half8{};
+                }
+
+        int done = 0, slot = 0;
+        for (int gi = 0; gi < ng; ++gi) {
+            floatx4 acc[MB] = {};
+            static_for<XB>([&](auto b_c) __attribute__((always_inline)) {
+                constexpr int b = decltype(b_c)::value;
+                if (b < nb) {
+                    wait_tasks(issued - done - 1);
+                    asm volatile("" ::: "memory");
+                    const GF_LDS char* buf = tasks + slot * Cfg::TASK_BYTES;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const half8 w = *(const GF_LDS half8*)(buf + bat[i]);
+#pragma unroll
+                        for (int m = 0; m < MB; ++m)
+                            acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[b * 4 + i][m], w, acc[m], 0, 0, 0);
+                    }
+                    asm volatile("" ::: "memory");
+                    wait_lgkmcnt0();                      // the buffer is read: it may be filled again
+                    if (issued < ntasks) issue();
+                    ++done;
+                    if (++slot == ring) slot = 0;
+                }
+            });
+            GF_LDS float* mine = red + (gi & 1) * WAVES * MR * 16;
+#pragma unroll
+            for (int m = 0; m < MB; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = 16 * m + 4 * c4 + i;
+                    if (row < M) mine[(wave * MR + row) * 16 + r16] = acc[m][i];
+                }
+            lds_barrier();
+            const int n0 = min((part + gi * parts) * 16, N - 16);
+            for (int t = threadIdx.x; t < M * 16; t += WAVES * kWave) {
+                float s = 0.0f;
+#pragma unroll
+                for (int w = 0; w < WAVES; ++w) s += mine[w * MR * 16 + t];
+                C[(size_t)(m0 + t / 16) * N + n0 + t % 16] = f32_to_f16_bits(s);
+            }
+        }
+        wait_vmcnt<0>();
+        lds_barrier();                                    // the next pass reuses the sums' slots
+    }
+#endif
+}
+
+template <class Cfg>
+hipError_t launch_group_band(const GroupRowArgs& a, int ring, int parts, hipStream_t stream)
+{
+    auto kern = group_band_kernel<Cfg>;
+    static std::atomic<uint64_t> lds_opt_in{0};
+    const int lds = Cfg::lds_bytes(ring);
+    static_assert(Cfg::lds_bytes(Cfg::MAX_RING) <= 160 * 1024, "one CU's LDS");
+    const hipError_t e = opt_in_lds((const void*)kern, Cfg::lds_bytes(Cfg::MAX_RING), lds_opt_in, stream);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kern, dim3((unsigned)(a.g.E * parts)), dim3(Cfg::WAVES * kWave), lds, stream, a, ring, parts);
+    return hipGetLastError();
+}
+
 }  // namespace gf

@@ -52,7 +52,8 @@ ROUTES = {
 }
 CASES = [("one", 40, 72), ("token", 136, 264), ("few", 200, 520), ("few", 33, 77), ("mid", 264, 136),
          ("mid", 129, 65), ("many", 72, 104), ("sixty-four", 48, 64), ("sixty-five", 16, 24), ("big", 4104, 72),
-         ("none", 64, 64), ("few", 64, 0), ("few", 8, 8), ("few", 1, 3)]
+         ("none", 64, 64), ("few", 64, 0), ("few", 8, 8), ("few", 1, 3), ("few", 16, 2048), ("few", 1000, 3000),
+         ("token", 72, 8000), ("many", 40, 4096), ("sixty-four", 24, 8192), ("one", 17, 8), ("few", 100, 9000)]
 
 
 def _route(name):
