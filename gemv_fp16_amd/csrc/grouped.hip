@@ -23,16 +23,47 @@ int validate_groups(const void* offsets, int T, int E, int N, int K)
 
 bool bad_ptr(const void* p, uintptr_t a) { return !p || !g_aligned(p, a); }
 
-template <class Cfg>
-int run_rows(GroupRowArgs a, bool al, hipStream_t stream)
+// Tiles at most: whole ones, and a partial one for every group that can have a row.
+template <class Cfg, class Args>
+int64_t most_tiles(const Args& a)
 {
-    // Tiles at most: whole ones, and a partial one for every group that can have a row.
-    const int64_t blocks = (int64_t)a.g.T / Cfg::BM + (a.g.E < a.g.T ? a.g.E : a.g.T);
-    const int64_t grid = blocks * ceil_div(a.N, Cfg::BN);
+    return ((int64_t)a.g.T / Cfg::BM + (a.g.E < a.g.T ? a.g.E : a.g.T)) * ceil_div(a.N, Cfg::BN);
+}
+
+template <class Cfg, class Args>
+int run_rows(const Args& a, int64_t grid, bool al, hipStream_t stream)
+{
     if (grid > kGroupMaxGrid) return GF_ERR_INVALID_ARG;
     const hipError_t e = al ? launch_grouped<Cfg, EPI_F16, true>(a, grid, stream)
                             : launch_grouped<Cfg, EPI_F16, false>(a, grid, stream);
     return e == hipSuccess ? GF_OK : GF_ERR_HIP;
+}
+
+template <class Cfg>
+int run_rows(const GroupRowArgs& a, bool al, hipStream_t stream)
+{
+    return run_rows<Cfg>(a, most_tiles<Cfg>(a), al, stream);
+}
+
+// 256 x 256 tiles run in rounds of 256, one to a CU; a last round that is at most
+// half full costs as much as a full one (8191 rows over 8 groups by 4096: 2.3
+// rounds).  So the tiles that fill whole rounds run as one launch and the rest as
+// a second one of 128 x 128 tiles, which spread over the chip.  How many there are
+// is known on the device only: both launches hold the most there can be, and the
+// second one's workgroups end at once where the last round is fuller.  The same
+// products in the same order, so the results do not depend on the split.
+template <int LB>
+int run_rounds(const GroupRowArgs& a, bool al, hipStream_t stream)
+{
+    typedef GemmCfg<256, 256, 64, 2, 256, 2, 0, LB> Big;
+    typedef GemmCfg<128, 128, 64, 4, 256, 2, 0, LB> Small;
+    GroupRowShare<1> a1;
+    GroupRowShare<2> a2;
+    static_cast<GemmArgs&>(a1) = a;
+    static_cast<GemmArgs&>(a2) = a;
+    a1.g = a2.g = a.g;
+    const int rc = run_rows<Big>(a1, most_tiles<Big>(a), al, stream);
+    return rc ? rc : run_rows<Small>(a2, 4 * 128, al, stream);
 }
 
 template <class Cfg>
@@ -61,7 +92,11 @@ int run_band(const GroupRowArgs& a, hipStream_t stream)
 //    against 327 at T = 8191, E = 8, 4096 x 4096; 97 against 111 for K x N B at
 //    T = 4096);
 //  * K x N B (transposing reads, which the one-wave-per-SIMD tiles have): 128 x
-//    128 for everything smaller (45 against 57 at T = 48, E = 16).
+//    128 for everything smaller (45 against 57 at T = 48, E = 16);
+//  * below K = 1024, tiles that leave room for two workgroups on a CU, so that one
+//    stores while the other multiplies: 128 x 128 with two stages (43 against 56
+//    at T = 7600, E = 41, K x N of 320 x 2784), 64 x 128 for few rows (31 against
+//    40 at T = 306, E = 10, 816 x 6568).
 template <int LB>
 int rows_dispatch(const GroupRowArgs& a, bool al, hipStream_t stream)
 {
@@ -76,10 +111,13 @@ int rows_dispatch(const GroupRowArgs& a, bool al, hipStream_t stream)
         }
     }
     if (mean >= 192 && ((int64_t)a.g.T / 256) * ceil_div(a.N, 256) >= 128)
-        return run_rows<GemmCfg<256, 256, 64, 2, 256, 2, 0, LB>>(a, al, stream);
+        return run_rounds<LB>(a, al, stream);
     if constexpr (LB == 0)
         if (mean < 64) return run_rows<GemmCfg<64, 64, 64, 3, 256, 0, 0, 0>>(a, al, stream);
-    return run_rows<GemmCfg<128, 128, 64, 3, 256, 2, 0, LB>>(a, al, stream);
+    if (a.K >= 1024) return run_rows<GemmCfg<128, 128, 64, 3, 256, 2, 0, LB>>(a, al, stream);
+    if constexpr (LB == 1)
+        if (mean < 64) return run_rows<GemmCfg<64, 128, 64, 2, 256, 2, 0, LB>>(a, al, stream);
+    return run_rows<GemmCfg<128, 128, 64, 2, 256, 2, 0, LB>>(a, al, stream);
 }
 
 // LB: 0 for B[e] N x K, 1 for K x N.
@@ -98,7 +136,6 @@ int rows_impl(const void* A, const void* B, void* C, const int* offsets, int T, 
     a.C = C;
     a.M = 0; a.N = N; a.K = K;
     a.g.offsets = offsets; a.g.E = E; a.g.T = T;
-    a.c_bytes = 2;
     const bool al = g_aligned(A, 16) && g_aligned(B, 16) && g_aligned(C, 16) && K % 8 == 0 &&
                     (LB == 0 || N % 8 == 0);
     return rows_dispatch<LB>(a, al, stream);
@@ -155,7 +192,10 @@ int gemm_f16_grouped_tn(const void* A, const void* B, void* C, const int* offset
     a.g.offsets = offsets; a.g.E = E; a.g.T = T;
     a.c_bytes = c_f32 ? 4 : 2;
     const bool al = g_aligned(A, 16) && g_aligned(B, 16) && g_aligned(C, 16) && M % 8 == 0 && N % 8 == 0;
-    if ((int64_t)E * ceil_div(M, 256) * ceil_div(N, 256) >= 256)
+    // Shallow groups are all start and store, which two workgroups on a CU overlap:
+    // 128 x 128 tiles 31 us against 34 at 1000 rows over 16 groups of 1024 x 2048,
+    // 166 against 187 at 600 over 2 of 8192 x 8192; 113 against 109 at 4096 over 8.
+    if ((int64_t)E * ceil_div(M, 256) * ceil_div(N, 256) >= 256 && T / E >= 384)
         return run_depth<GemmCfg<256, 256, 64, 2, 256, 2, 1, 1>>(a, al, c_f32 != 0, (hipStream_t)stream);
     return run_depth<GemmCfg<128, 128, 64, 2, 256, 2, 1, 1>>(a, al, c_f32 != 0, (hipStream_t)stream);
 }

@@ -36,7 +36,10 @@ struct Groups {
     // has ceil(n / BM) * per_block items; the items are dealt to the XCDs in
     // contiguous runs.  Every lane of the wave must call it; the results are
     // wave-uniform.  Returns false past the last item.
-    template <int BM>
+    // SHARE 0: all items.  1: those that fill whole rounds of 256 (all of them
+    // where the last round is more than half full).  2: the rest, w / 4 (the
+    // caller cuts each in four).
+    template <int BM, int SHARE = 0>
     __device__ __forceinline__ bool find(int w, int per_block, int& e, int& lo, int& hi, int& item) const
     {
         const int lane = threadIdx.x % kWave;
@@ -53,8 +56,16 @@ struct Groups {
             }
             total += __builtin_amdgcn_readlane(scan, kWave - 1);
         }
-        if (w >= total) return false;
-        const int L = xcd_remap(w, total);
+        const int whole = total % 256 <= 128 ? total - total % 256 : total;
+        int L;
+        if constexpr (SHARE == 2) {
+            L = whole + w / 4;
+            if (L >= total) return false;
+        } else {
+            const int share = SHARE == 1 ? whole : total;
+            if (w >= share) return false;
+            L = xcd_remap(w, share);
+        }
         int before = 0;
         for (int base = 0;; base += kWave) {
             if (E > kWave) {                       // else the first loop's one pass is still in registers
@@ -87,25 +98,34 @@ struct Groups {
 constexpr int kGroupPanel = 8;   // tile-rows per raster panel within a group
 
 // By rows.  M and C's rows are the group's; A, B, C point at its parts.
-struct GroupRowArgs : GemmArgs {
+// SHARE 1 and 2: the launch in two parts of grouped.hip's run_rounds (1 with the
+// whole tiles, 2 with tiles of half their side).
+template <int SHARE>
+struct GroupRowShare : GemmArgs {
     Groups g;
-    int c_bytes;          // of one element of C
     static constexpr bool PER_GROUP = true;
 
     template <int BM, int BN>
     __device__ __forceinline__ bool locate(int& tm, int& tn)
     {
-        const int tiles_n = ceil_div(N, BN);
+        constexpr int F = SHARE == 2 ? 2 : 1;             // tiles are F * BM x F * BN
+        const int tiles_n = ceil_div(N, F * BN);
         int e, lo, hi, item;
-        if (!g.find<BM>(blockIdx.x, tiles_n, e, lo, hi, item)) return false;
+        if (!g.find<F * BM, SHARE>(blockIdx.x, tiles_n, e, lo, hi, item)) return false;
         M = hi - lo;
         A += (size_t)lo * K;
         B += (size_t)e * N * K;
-        C = (char*)C + (size_t)lo * N * c_bytes;
-        grouped_tile(item, ceil_div(M, BM), tiles_n, kGroupPanel, tm, tn);
+        C = (uint16_t*)C + (size_t)lo * N;
+        grouped_tile(item, ceil_div(M, F * BM), tiles_n, kGroupPanel, tm, tn);
+        if constexpr (SHARE == 2) {
+            tm = 2 * tm + (blockIdx.x % 4) / 2;
+            tn = 2 * tn + blockIdx.x % 2;
+            return tm * BM < M && tn * BN < N;
+        }
         return true;
     }
 };
+typedef GroupRowShare<0> GroupRowArgs;
 
 // By depth.  C is E x M x N; K becomes the group's number of rows.
 struct GroupDepthArgs : GemmArgs {
