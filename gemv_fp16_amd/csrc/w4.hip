@@ -140,49 +140,87 @@ int launch_band(const W4Args& a, int ring, int parts, hipStream_t stream)
     return w4_status(hipGetLastError());
 }
 
-// The band form's launch.  Two workgroups to a CU, with as much in flight as
-// their LDS leaves, where there are row groups for them and the registers allow
-// it (not with A in registers); else one with all of it.
+// The band form's launch.  One weight: two workgroups to a CU, with as much in
+// flight as their LDS leaves, where there are row groups for them and the
+// registers allow it (not with A in registers); else one with all of it.  Grouped:
+// about 256 workgroups in all but at least 8 a group, two tasks in flight a wave
+// (25 us against 32 with twice as many and four, at 24 rows over 16 groups of
+// 4096 x 4096; 18 against 30 at 16 over 8 of 2048 x 8192).
 template <class Cfg, bool GROUPED>
 int band(const W4Args& a, hipStream_t stream)
 {
-    const int fixed = 2 * Cfg::WAVES * (GROUPED ? 16 * Cfg::MB : a.M) * 64 + (Cfg::XLDS ? a.M * a.K * 2 : 0);
-    const int per_task = Cfg::WAVES * Cfg::TASK_BYTES;
-    const int64_t groups = (int64_t)ceil_div(a.N, 16) * (GROUPED ? a.g.E : 1);
-    const int per_cu = Cfg::XLDS && groups > 256 && fixed + per_task <= 80 * 1024 ? 2 : 1;
-    int ring = (160 * 1024 / per_cu - fixed) / per_task;
-    const int blocks = ceil_div(a.K, Cfg::BK * Cfg::WAVES);        // of a wave, in one row group
-    const int64_t tasks = ceil_div((int)(groups < (1 << 30) ? groups : 1 << 30), 256 * per_cu) * (int64_t)blocks;
-    if (ring > Cfg::MAX_RING) ring = Cfg::MAX_RING;
-    if (ring > tasks) ring = (int)tasks;
-    const int parts = GROUPED ? max(1, 256 * per_cu * 2 / a.g.E) : 256 * per_cu;
-    return launch_band<Cfg, GROUPED>(a, ring, parts, stream);
+    if constexpr (GROUPED) {
+        const int want = 256 / a.g.E;
+        return launch_band<Cfg, true>(a, 2, want < 8 ? 8 : (want > 64 ? 64 : want), stream);
+    } else {
+        const int fixed = 2 * Cfg::WAVES * a.M * 64 + (Cfg::XLDS ? a.M * a.K * 2 : 0);
+        const int per_task = Cfg::WAVES * Cfg::TASK_BYTES;
+        const int groups = ceil_div(a.N, 16);
+        const int per_cu = Cfg::XLDS && groups > 256 && fixed + per_task <= 80 * 1024 ? 2 : 1;
+        int ring = (160 * 1024 / per_cu - fixed) / per_task;
+        const int tasks = ceil_div(groups, 256 * per_cu) * ceil_div(a.K, Cfg::BK * Cfg::WAVES);   // of a wave
+        if (ring > Cfg::MAX_RING) ring = Cfg::MAX_RING;
+        if (ring > tasks) ring = tasks;
+        return launch_band<Cfg, false>(a, ring, 256 * per_cu, stream);
+    }
+}
+
+// The tile form's launch, timed side by side over sizes (us):
+//  * one weight: 256 x 256 where they fill the CUs (129 against 138 for 128 x 256
+//    at 2048 x 8192 x 4096), else 128 x 256 with 8 waves from 400 tiles of 128 x
+//    128 (70 against 74 and 101 at 1024 x 8192 x 4096), 128 x 128 from 160 (40
+//    against 42 at 700 x 4096 x 4096), 64 x 128 from 64 of its own (32 against 38
+//    at 300 x 4096 x 4096), else 32 x 128 (14 against 17 at 130 x 1469 x 1344);
+//  * grouped, by the mean rows of a group: 32 x 128 up to 48 (24 against 26, and
+//    50 in the rows form, at 600 rows over 16 groups of 2048 x 2048), 64 x 128 up
+//    to 80, else 128 x 128 (42 against 47 at 1111 over 8 of 2048 x 4096; 256 x 256
+//    wastes the groups' ends: 343 against 314 at 8000 over 8 of 4096 x 4096).
+template <int GROUP, bool GROUPED>
+int tile(const W4Args& a, int64_t rows, hipStream_t stream)
+{
+    typedef W4TileCfg<1, 1, 1, 4, 5> T32;
+    typedef W4TileCfg<2, 1, 1, 4, 4> T64;
+    typedef W4TileCfg<4, 1, 1, 4, 4> T128;
+    if constexpr (GROUPED) {
+        if (rows <= 48) return launch_tile<T32, GROUP, true>(a, stream);
+        if (rows <= 80) return launch_tile<T64, GROUP, true>(a, stream);
+        return launch_tile<T128, GROUP, true>(a, stream);
+    } else {
+        auto tiles = [&](int bm, int bn) { return (int64_t)ceil_div(a.M, bm) * ceil_div(a.N, bn); };
+        if (tiles(256, 256) >= 192) return launch_tile<W4TileCfg<4, 2, 2, 4, 4>, GROUP, false>(a, stream);
+        if (tiles(128, 128) >= 400) return launch_tile<W4TileCfg<4, 1, 1, 8, 4>, GROUP, false>(a, stream);
+        if (tiles(128, 128) >= 160) return launch_tile<T128, GROUP, false>(a, stream);
+        if (tiles(64, 128) >= 64) return launch_tile<T64, GROUP, false>(a, stream);
+        return launch_tile<T32, GROUP, false>(a, stream);
+    }
 }
 
 // Which form, by the rows of A (of a group, on average) and by what the operands'
-// sizes and alignment allow.
+// sizes and alignment allow.  The tile form rounds weights to fp16, which one
+// weight's users see from 65 rows on; between 17 and 64 rows the streaming forms
+// are also the faster ones there (16 us against 31 at 24 x 11008 x 4096, 13
+// against 31 at 64 x 4096 x 4096).  Groups of that size stream badly (every group
+// has its own uneven rest), and take the tiles from a mean of 17 rows.
 template <int GROUP, bool GROUPED>
 int product(const W4Args& a, hipStream_t stream)
 {
     const int64_t rows = GROUPED ? (a.g.T + a.g.E - 1) / a.g.E : a.M;
+    if (rows > (GROUPED ? 16 : 64) && w4_aligned(a.A, 16) && a.K >= 64) return tile<GROUP, GROUPED>(a, rows, stream);
     const bool wide = w4_aligned(a.A, 16) && w4_aligned(a.Q, 16) && w4_aligned(a.S, 16) && w4_aligned(a.Z, 8);
-    if (rows > 64 && w4_aligned(a.A, 16) && a.K >= 64) {
-        const int64_t blocks = GROUPED ? a.g.T / 256 + a.g.E : ceil_div(a.M, 256);
-        if (blocks * ceil_div(a.N, 256) >= 192) return launch_tile<W4TileCfg<4, 2, 2, 4, 4>, GROUP, GROUPED>(a, stream);
-        return launch_tile<W4TileCfg<2, 1, 1, 4, 4>, GROUP, GROUPED>(a, stream);
-    }
     if (wide && a.K % 512 == 0 && a.K > 0 && a.N >= 16) {
         if constexpr (!GROUPED)
             if (a.M <= 16 && a.M * a.K <= 32768) return band<W4BandCfg<GROUP, 1, 0>, false>(a, stream);
         if (rows <= 16 && a.K <= 4096) return band<W4BandCfg<GROUP, 1, 1>, GROUPED>(a, stream);
         if (rows <= 16 && a.K <= 8192) return band<W4BandCfg<GROUP, 1, 2>, GROUPED>(a, stream);
-        if (rows <= 32 && a.K <= 4096) return band<W4BandCfg<GROUP, 2, 1>, GROUPED>(a, stream);
+        if constexpr (!GROUPED)
+            if (rows <= 32 && a.K <= 4096) return band<W4BandCfg<GROUP, 2, 1>, false>(a, stream);
     }
     constexpr int CB = GROUP == 32 ? 2 : 4;
     if (rows <= 16)
         return a.N >= 8192 ? launch_rows<W4RowsCfg<GROUP, 1, 2, 8, CB>, GROUPED>(a, stream)
                            : launch_rows<W4RowsCfg<GROUP, 1, 1, 8, CB>, GROUPED>(a, stream);
-    if (rows > 32 && a.N >= 8192) return launch_rows<W4RowsCfg<GROUP, 2, 4, 4, 2>, GROUPED>(a, stream);
+    if constexpr (!GROUPED)
+        if (rows > 32 && a.N >= 8192) return launch_rows<W4RowsCfg<GROUP, 2, 4, 4, 2>, false>(a, stream);
     return launch_rows<W4RowsCfg<GROUP, 2, 2, 8, CB>, GROUPED>(a, stream);
 }
 

@@ -1108,7 +1108,6 @@ __global__ __launch_bounds__(Cfg::NT) void w4_tile_kernel(W4Args a)
     asm volatile("" ::: "memory");
     wait_lgkmcnt0();
     constexpr int CPR = WC / 8, ITERS = WR * CPR / kWave;
-    const bool vec = a.N % 8 == 0 && (reinterpret_cast<uintptr_t>(a.C) & 15) == 0;
 #pragma unroll
     for (int it = 0; it < ITERS; ++it) {
         const int q = it * kWave + lane, r = q / CPR, cc = q % CPR;
@@ -1116,8 +1115,8 @@ __global__ __launch_bounds__(Cfg::NT) void w4_tile_kernel(W4Args a)
         const int row = m0 + wm * WR + r, col = n0 + wn * WC + cc * 8;
         if (row >= M) continue;
         uint16_t* dst = a.C + (size_t)row * a.N + col;
-        if (vec && col + 8 <= a.N) {
-            __builtin_nontemporal_store(v, (u32x4*)dst);
+        if (col + 8 <= a.N) {                             // (whatever its alignment)
+            __builtin_nontemporal_store(v, (u32x4_any*)dst);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)

@@ -401,12 +401,16 @@ int gemm_f16_grouped_tn(const void* A, const void* B, void* C, const int* offset
  * weights (E x N x K).
  *
  * gemm_w4_f16_nt: C = A . W^T with A M x K and C M x N fp16; gemv_w4_f16 is its
- * single row, y = W . x.  Products a * (q - z) are summed in fp32 within a
- * group, the groups' sums scaled and added in fp32, and each result rounded
- * once to fp16: the weights themselves are not rounded.  Results repeat bit
- * for bit from run to run.
+ * single row, y = W . x.  Up to 64 rows of A, products a * (q - z) are summed in
+ * fp32 within a group, the groups' sums scaled and added in fp32, and each result
+ * rounded once to fp16: the weights themselves are not rounded.  From 65 rows on
+ * the matrix cores are the bound, and each weight is rounded once to fp16 first,
+ * as w4_dequantize_f16 rounds it; sums are in fp32 all the same.  (Where K < 64
+ * or A is not 16-byte aligned, the first way holds for any number of rows.)  Results repeat bit for bit
+ * from run to run.
  * gemm_w4_f16_grouped_nt: gemm_f16_grouped_nt with 4-bit weights, Q E x N x
- * K/8, S and Z E x N x G; offsets and rows as there.
+ * K/8, S and Z E x N x G; offsets and rows as there.  Its weights are rounded
+ * as above from a mean of 17 rows a group (T > 16 E) on.
  * Entries of Z above 15 are outside the contract (no fault).  The fast path
  * needs A and Q 16-byte aligned and K % 32 == 0.  M == 0 or N == 0 is a
  * no-op; K == 0 writes +0.  Each operand (a group's part of Q) must stand for

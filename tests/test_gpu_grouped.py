@@ -84,7 +84,7 @@ def _check_rows(C, A, B, off, T, depth, what, transpose, rounded=False):
         b = B[e].astype(np.float64)
         b = b.T if transpose else b
         absum = np.abs(a[r]) @ np.abs(b)
-        # 4-bit weights are rounded to fp16 first where the groups have more than 64 rows on average
+        # 4-bit weights are rounded to fp16 first where the groups have more than 16 rows on average
         extra = plain.rounded_weights(absum, np.abs(a[r]).sum(1, keepdims=True)) if rounded else 0.0
         plain.check(got[r], a[r] @ b, absum, depth, plain.F16, "%s group %d" % (what, e), extra)
     assert (bits[~seen] == SENTINEL).all(), what + ": rows of no group changed"
@@ -151,7 +151,7 @@ def test_w4_grouped(route, N, K, group, zeros):
     for shift in (0, 1):
         C = gf.gemm_w4_f16_grouped_nt(_shifted(dev(A), shift), Q3, S3, Z3, dev(off), _sentinel((T, N)), group)
         torch.cuda.synchronize()
-        _check_rows(C, A, W, off, T, K, "w4", True, T > 64 * E)
+        _check_rows(C, A, W, off, T, K, "w4", True, T > 16 * E)
 
 
 def test_grouped_same_as_one_product():
@@ -218,7 +218,7 @@ def test_expert_layer_run_together():
         plain.check(dw[e].cpu().numpy(), a.T @ b, np.abs(a).T @ np.abs(b), sizes[e], plain.F32, "dw")
     q = plain.unpack(Q.view(E * N, -1).cpu().numpy())
     W4 = plain.weights(q, S.view(E * N, -1).cpu().numpy(), Z.view(E * N, -1).cpu().numpy(), 64).reshape(E, N, K)
-    _check_rows(y4, X, W4, off, T, K, "y4", True, T > 64 * E)
+    _check_rows(y4, X, W4, off, T, K, "y4", True, T > 16 * E)
     _check_rows(yb, X, back.cpu().numpy(), off, T, K, "yb", True)
 
 
