@@ -51,12 +51,15 @@ int run_rows(const GroupRowArgs& a, bool al, hipStream_t stream)
 // a second one of 128 x 128 tiles, which spread over the chip.  How many there are
 // is known on the device only: both launches hold the most there can be, and the
 // second one's workgroups end at once where the last round is fuller.  The same
-// products in the same order, so the results do not depend on the split.
+// products in the same order, so the results do not depend on the split.  Where
+// there cannot be more than one round, one launch (98 us against 102 at 4096 rows
+// over 8 groups of 2048 x 4096).
 template <int LB>
 int run_rounds(const GroupRowArgs& a, bool al, hipStream_t stream)
 {
     typedef GemmCfg<256, 256, 64, 2, 256, 2, 0, LB> Big;
     typedef GemmCfg<128, 128, 64, 4, 256, 2, 0, LB> Small;
+    if (most_tiles<Big>(a) <= 256) return run_rows<Big>(a, al, stream);
     GroupRowShare<1> a1;
     GroupRowShare<2> a2;
     static_cast<GemmArgs&>(a1) = a;
