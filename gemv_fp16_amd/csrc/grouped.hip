@@ -91,15 +91,17 @@ int run_band(const GroupRowArgs& a, hipStream_t stream)
 //    of 19 the 64 x 64 tile is ahead of it (34 against 39);
 //  * then 64 x 64 up to a mean of 64 (64 against 68 at T = 500, E = 16), 128 x 128
 //    with three stages beyond (45 against 56 at T = 1111, E = 8, 2048 x 4096);
-//  * 256 x 256 where the groups fill several of them and they fill the CUs (296
-//    against 327 at T = 8191, E = 8, 4096 x 4096; 97 against 111 for K x N B at
-//    T = 4096);
-//  * K x N B (transposing reads, which the one-wave-per-SIMD tiles have): 128 x
-//    128 for everything smaller (45 against 57 at T = 48, E = 16);
-//  * below K = 1024, tiles that leave room for two workgroups on a CU, so that one
-//    stores while the other multiplies: 128 x 128 with two stages (43 against 56
-//    at T = 7600, E = 41, K x N of 320 x 2784), 64 x 128 for few rows (31 against
-//    40 at T = 306, E = 10, 816 x 6568).
+//  * 256 x 256 where the groups fill several of them, they fill the CUs and K is
+//    long enough to fill their pipeline (278 against 330 at T = 8191, E = 8, 4096 x
+//    4096; 98 against 121 for K x N B at T = 4096, 2048 x 4096; but 50 against 46
+//    at T = 5000, E = 16, 4096 x 512);
+//  * K x N B (transposing reads, which the one-wave-per-SIMD tiles have): 64 x 128
+//    below a mean of 16 (42 against 50 and 58 at T = 48, E = 16, 4096 x 2048), 128 x
+//    128 beyond (33 against 37 at T = 500, E = 16, 2048 x 2048);
+//  * up to K = 1024, tiles that leave room for two workgroups on a CU, so that one
+//    stores while the other multiplies: 128 x 128 with two stages (71 against 84 at
+//    T = 5000, E = 16, 4096 x 1024; 43 against 56 at T = 7600, E = 41, K x N of 320
+//    x 2784), 64 x 128 for few rows (31 against 40 at T = 306, E = 10, 816 x 6568).
 template <int LB>
 int rows_dispatch(const GroupRowArgs& a, bool al, hipStream_t stream)
 {
@@ -113,13 +115,14 @@ int rows_dispatch(const GroupRowArgs& a, bool al, hipStream_t stream)
             if (a.K <= 8192) return run_band<GroupBandCfg<1, 8>>(a, stream);
         }
     }
-    if (mean >= 192 && ((int64_t)a.g.T / 256) * ceil_div(a.N, 256) >= 128)
+    if (mean >= 192 && a.K > 1024 && ((int64_t)a.g.T / 256) * ceil_div(a.N, 256) >= 128)
         return run_rounds<LB>(a, al, stream);
     if constexpr (LB == 0)
         if (mean < 64) return run_rows<GemmCfg<64, 64, 64, 3, 256, 0, 0, 0>>(a, al, stream);
-    if (a.K >= 1024) return run_rows<GemmCfg<128, 128, 64, 3, 256, 2, 0, LB>>(a, al, stream);
     if constexpr (LB == 1)
-        if (mean < 64) return run_rows<GemmCfg<64, 128, 64, 2, 256, 2, 0, LB>>(a, al, stream);
+        if (mean < (a.K > 1024 ? 16 : 64))
+            return run_rows<GemmCfg<64, 128, 64, 2, 256, 2, 0, LB>>(a, al, stream);
+    if (a.K > 1024) return run_rows<GemmCfg<128, 128, 64, 3, 256, 2, 0, LB>>(a, al, stream);
     return run_rows<GemmCfg<128, 128, 64, 2, 256, 2, 0, LB>>(a, al, stream);
 }
 
@@ -195,12 +198,14 @@ int gemm_f16_grouped_tn(const void* A, const void* B, void* C, const int* offset
     a.g.offsets = offsets; a.g.E = E; a.g.T = T;
     a.c_bytes = c_f32 ? 4 : 2;
     const bool al = g_aligned(A, 16) && g_aligned(B, 16) && g_aligned(C, 16) && M % 8 == 0 && N % 8 == 0;
-    // Shallow groups are all start and store, which two workgroups on a CU overlap:
-    // 128 x 128 tiles 31 us against 34 at 1000 rows over 16 groups of 1024 x 2048,
-    // 166 against 187 at 600 over 2 of 8192 x 8192; 113 against 109 at 4096 over 8.
+    // Shallow groups are all start and store, which three workgroups on a CU overlap
+    // (48 KB of LDS each): 128 x 128 tiles in steps of 32 rows, 56 us against 62 at
+    // 2999 rows over 32 groups of 1024 x 2048 (61 in steps of 64, two to a CU), 154
+    // against 192 at 600 over 2 of 8192 x 8192.  Deep ones are matrix work: 307
+    // against 233 at 8192 over 2 of 4096 x 4096; even at 4096 over 8 (110).
     if ((int64_t)E * ceil_div(M, 256) * ceil_div(N, 256) >= 256 && T / E >= 384)
         return run_depth<GemmCfg<256, 256, 64, 2, 256, 2, 1, 1>>(a, al, c_f32 != 0, (hipStream_t)stream);
-    return run_depth<GemmCfg<128, 128, 64, 2, 256, 2, 1, 1>>(a, al, c_f32 != 0, (hipStream_t)stream);
+    return run_depth<GemmCfg<128, 128, 32, 3, 256, 2, 1, 1>>(a, al, c_f32 != 0, (hipStream_t)stream);
 }
 
 }  // extern "C"
