@@ -78,8 +78,9 @@ int run_band(const GroupRowArgs& a, hipStream_t stream)
     const int64_t want = 256 / a.g.E, blocks = ceil_div(a.N, 16);
     int64_t parts = want < 16 ? 16 : (want > 64 ? 64 : want);
     if (parts > blocks) parts = blocks;
-    if (parts * a.g.E > kGroupMaxGrid) return GF_ERR_INVALID_ARG;
-    const hipError_t e = launch_group_band<Cfg>(a, 2, (int)parts, stream);
+    const int64_t grid = (a.g.T / (16 * Cfg::MB) + (a.g.E < a.g.T ? a.g.E : a.g.T)) * parts;
+    if (grid > kGroupMaxGrid) return GF_ERR_INVALID_ARG;
+    const hipError_t e = launch_group_band<Cfg>(a, 2, (int)parts, grid, stream);
     return e == hipSuccess ? GF_OK : GF_ERR_HIP;
 }
 
@@ -87,7 +88,7 @@ int run_band(const GroupRowArgs& a, hipStream_t stream)
 // side by side with B rotated through HBM (us):
 //  * a handful of rows a group, K-contiguous B: the streaming form, 36 against
 //    57 for every tile at T = 48, E = 16, 4096 x 2048; 41 against 59 at T = 16,
-//    E = 8, 4096 x 4096; 11 against 20 at T = 18, E = 17, 488 x 2672.  At a mean
+//    E = 8, 4096 x 4096; 16 against 20 at T = 18, E = 17, 488 x 2672.  At a mean
 //    of 19 the 64 x 64 tile is ahead of it (34 against 39);
 //  * then 64 x 64 up to a mean of 64 (64 against 68 at T = 500, E = 16), 128 x 128
 //    with three stages beyond (45 against 56 at T = 1111, E = 8, 2048 x 4096);

@@ -179,9 +179,10 @@ hipError_t launch_grouped(Args a, int64_t grid, hipStream_t stream)
 // ---------------------------------------------------------------------------
 //
 // C[r] = A[r] . B[e]^T where a group has a handful of rows: bound by B's bytes.
-// Workgroup p of `parts` of group e walks the 16-row blocks of B[e] grid-stride
-// (the last one is the last 16 rows, some a second time), once for every
-// 16 * MB rows of A.  Its 8 waves split K in tasks of 128 k; a task's 16 rows of
+// For each 16 * MB rows of A of a group, `parts` workgroups walk the 16-row blocks
+// of B[e] grid-stride (the last one is the last 16 rows, some a second time): a
+// group with many rows has many workgroups, next to each other so that they share
+// B in their L2.  A workgroup's 8 waves split K in tasks of 128 k; a task's 16 rows of
 // 256 bytes go to LDS by direct loads of whole cache lines, `ring` tasks in
 // flight a wave, and are read from there as MFMA operands (chunk c of row n at
 // slot c ^ n: the 16 rows read together lie in different banks).  Each wave keeps
@@ -209,14 +210,13 @@ __global__ __launch_bounds__(Cfg::WAVES * 64) void group_band_kernel(GroupRowArg
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int r16 = lane % 16, c4 = lane / 16;
     const int N = a.N, K = a.K;
-    const int e = blockIdx.x / parts, part = blockIdx.x - e * parts;
-    int lo, hi;
-    a.g.rows(e, lo, hi);
-    const int rows = __builtin_amdgcn_readfirstlane(hi - lo);
-    if (rows == 0) return;
-    const uint16_t* A = a.A + (size_t)lo * K;
+    int e, lo, hi, item;
+    if (!a.g.template find<MR>(blockIdx.x, parts, e, lo, hi, item)) return;
+    const int passes = ceil_div(hi - lo, MR), part = item / passes;
+    const int begin = lo + item % passes * MR, M = min(hi - begin, MR);
+    const uint16_t* A = a.A + (size_t)begin * K;
     const uint16_t* B = a.B + (size_t)e * N * K;
-    uint16_t* C = (uint16_t*)a.C + (size_t)lo * N;
+    uint16_t* C = (uint16_t*)a.C + (size_t)begin * N;
 
     GF_LDS char* tasks = (GF_LDS char*)smem_raw + wave * ring * Cfg::TASK_BYTES;
     GF_LDS float* red = (GF_LDS float*)((GF_LDS char*)smem_raw + WAVES * ring * Cfg::TASK_BYTES);
@@ -233,92 +233,88 @@ __global__ __launch_bounds__(Cfg::WAVES * 64) void group_band_kernel(GroupRowArg
         boff[i] = (uint32_t)r * (uint32_t)K + (uint32_t)(r16 ^ r) * 8u;
         bat[i] = (uint32_t)(r16 * 256 + (((4 * i + c4) ^ r16) * 16));
     }
-    for (int m0 = 0; m0 < rows; m0 += MR) {
-        const int M = min(rows - m0, MR);
-        int ig = part, ib = 0, islot = 0, issued = 0;     // the next task to issue
-        auto issue = [&]() __attribute__((always_inline)) {
-            GF_LDS char* buf = tasks + islot * Cfg::TASK_BYTES;
-            const int k0 = (b0 + ib) * Cfg::BK;
-            const uint16_t* src = B + (size_t)min(ig * 16, N - 16) * K + k0;
+    int ig = part, ib = 0, islot = 0, issued = 0;     // the next task to issue
+    auto issue = [&]() __attribute__((always_inline)) {
+        GF_LDS char* buf = tasks + islot * Cfg::TASK_BYTES;
+        const int k0 = (b0 + ib) * Cfg::BK;
+        const uint16_t* src = B + (size_t)min(ig * 16, N - 16) * K + k0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const void* p = src + boff[i];
-                if (k0 + Cfg::BK > K && k0 + (r16 ^ (4 * i + c4)) * 8 >= K) p = (const void*)g_zero16;
-                __builtin_amdgcn_global_load_lds(p, (GF_LDS void*)(buf + i * 1024), 16, 0, 2);
+        for (int i = 0; i < 4; ++i) {
+            const void* p = src + boff[i];
+            if (k0 + Cfg::BK > K && k0 + (r16 ^ (4 * i + c4)) * 8 >= K) p = (const void*)g_zero16;
+            __builtin_amdgcn_global_load_lds(p, (GF_LDS void*)(buf + i * 1024), 16, 0, 2);
+        }
+        ++issued;
+        if (++ib == nb) { ib = 0; ig += parts; }
+        if (++islot == ring) islot = 0;
+    };
+    auto wait_tasks = [&](int left) __attribute__((always_inline)) {   // younger tasks that may be pending
+        left = __builtin_amdgcn_readfirstlane(left);
+        if (left >= 3) wait_vmcnt<3 * L>();
+        else if (left == 2) wait_vmcnt<2 * L>();
+        else if (left == 1) wait_vmcnt<L>();
+        else wait_vmcnt<0>();
+    };
+    const int first = min(ring, ntasks);
+    for (int i = 0; i < first; ++i) issue();
+    half8 x[XB * 4][MB];
+#pragma unroll
+    for (int b = 0; b < XB; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int m = 0; m < MB; ++m) {
+                const int k = (b0 + b) * Cfg::BK + 32 * i + 8 * c4;
+                const half8 v = *(const half8*)(A + (size_t)min(16 * m + r16, M - 1) * K + min(k, K - 8));
+                x[b * 4 + i][m] = k < K ? v : half8{};
             }
-            ++issued;
-            if (++ib == nb) { ib = 0; ig += parts; }
-            if (++islot == ring) islot = 0;
-        };
-        auto wait_tasks = [&](int left) __attribute__((always_inline)) {   // younger tasks that may be pending
-            left = __builtin_amdgcn_readfirstlane(left);
-            if (left >= 3) wait_vmcnt<3 * L>();
-            else if (left == 2) wait_vmcnt<2 * L>();
-            else if (left == 1) wait_vmcnt<L>();
-            else wait_vmcnt<0>();
-        };
-        const int first = min(ring, ntasks);
-        for (int i = 0; i < first; ++i) issue();
-        half8 x[XB * 4][MB];
-#pragma unroll
-        for (int b = 0; b < XB; ++b)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int m = 0; m < MB; ++m) {
-                    const int k = (b0 + b) * Cfg::BK + 32 * i + 8 * c4;
-                    const half8 v = *(const half8*)(A + (size_t)(m0 + min(16 * m + r16, M - 1)) * K + min(k, K - 8));
-                    x[b * 4 + i][m] = k < K ? v : half8{};
-                }
 
-        int done = 0, slot = 0;
-        for (int gi = 0; gi < ng; ++gi) {
-            floatx4 acc[MB] = {};
-            static_for<XB>([&](auto b_c) __attribute__((always_inline)) {
-                constexpr int b = decltype(b_c)::value;
-                if (b < nb) {
-                    wait_tasks(issued - done - 1);
-                    asm volatile("" ::: "memory");
-                    const GF_LDS char* buf = tasks + slot * Cfg::TASK_BYTES;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const half8 w = *(const GF_LDS half8*)(buf + bat[i]);
-#pragma unroll
-                        for (int m = 0; m < MB; ++m)
-                            acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[b * 4 + i][m], w, acc[m], 0, 0, 0);
-                    }
-                    asm volatile("" ::: "memory");
-                    wait_lgkmcnt0();                      // the buffer is read: it may be filled again
-                    if (issued < ntasks) issue();
-                    ++done;
-                    if (++slot == ring) slot = 0;
-                }
-            });
-            GF_LDS float* mine = red + (gi & 1) * WAVES * MR * 16;
-#pragma unroll
-            for (int m = 0; m < MB; ++m)
+    int done = 0, slot = 0;
+    for (int gi = 0; gi < ng; ++gi) {
+        floatx4 acc[MB] = {};
+        static_for<XB>([&](auto b_c) __attribute__((always_inline)) {
+            constexpr int b = decltype(b_c)::value;
+            if (b < nb) {
+                wait_tasks(issued - done - 1);
+                asm volatile("" ::: "memory");
+                const GF_LDS char* buf = tasks + slot * Cfg::TASK_BYTES;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int row = 16 * m + 4 * c4 + i;
-                    if (row < M) mine[(wave * MR + row) * 16 + r16] = acc[m][i];
-                }
-            lds_barrier();
-            const int n0 = min((part + gi * parts) * 16, N - 16);
-            for (int t = threadIdx.x; t < M * 16; t += WAVES * kWave) {
-                float s = 0.0f;
+                    const half8 w = *(const GF_LDS half8*)(buf + bat[i]);
 #pragma unroll
-                for (int w = 0; w < WAVES; ++w) s += mine[w * MR * 16 + t];
-                C[(size_t)(m0 + t / 16) * N + n0 + t % 16] = f32_to_f16_bits(s);
+                    for (int m = 0; m < MB; ++m)
+                        acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[b * 4 + i][m], w, acc[m], 0, 0, 0);
+                }
+                asm volatile("" ::: "memory");
+                wait_lgkmcnt0();                      // the buffer is read: it may be filled again
+                if (issued < ntasks) issue();
+                ++done;
+                if (++slot == ring) slot = 0;
             }
+        });
+        GF_LDS float* mine = red + (gi & 1) * WAVES * MR * 16;
+#pragma unroll
+        for (int m = 0; m < MB; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = 16 * m + 4 * c4 + i;
+                if (row < M) mine[(wave * MR + row) * 16 + r16] = acc[m][i];
+            }
+        lds_barrier();
+        const int n0 = min((part + gi * parts) * 16, N - 16);
+        for (int t = threadIdx.x; t < M * 16; t += WAVES * kWave) {
+            float s = 0.0f;
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) s += mine[w * MR * 16 + t];
+            C[(size_t)(t / 16) * N + n0 + t % 16] = f32_to_f16_bits(s);
         }
-        wait_vmcnt<0>();
-        lds_barrier();                                    // the next pass reuses the sums' slots
     }
+    wait_vmcnt<0>();
 #endif
 }
 
 template <class Cfg>
-hipError_t launch_group_band(const GroupRowArgs& a, int ring, int parts, hipStream_t stream)
+hipError_t launch_group_band(const GroupRowArgs& a, int ring, int parts, int64_t grid, hipStream_t stream)
 {
     auto kern = group_band_kernel<Cfg>;
     static std::atomic<uint64_t> lds_opt_in{0};
@@ -326,7 +322,7 @@ hipError_t launch_group_band(const GroupRowArgs& a, int ring, int parts, hipStre
     static_assert(Cfg::lds_bytes(Cfg::MAX_RING) <= 160 * 1024, "one CU's LDS");
     const hipError_t e = opt_in_lds((const void*)kern, Cfg::lds_bytes(Cfg::MAX_RING), lds_opt_in, stream);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kern, dim3((unsigned)(a.g.E * parts)), dim3(Cfg::WAVES * kWave), lds, stream, a, ring, parts);
+    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(Cfg::WAVES * kWave), lds, stream, a, ring, parts);
     return hipGetLastError();
 }
 

@@ -121,7 +121,8 @@ int launch_rows(const W4Args& a, hipStream_t stream)
     return w4_status(hipGetLastError());
 }
 
-// parts: workgroups that share the row groups of one weight, at most one each.
+// parts: workgroups that share the row groups of one weight (and 16 MB rows of A),
+// at most one each.
 template <class Cfg, bool GROUPED>
 int launch_band(const W4Args& a, int ring, int parts, hipStream_t stream)
 {
@@ -134,7 +135,8 @@ int launch_band(const W4Args& a, int ring, int parts, hipStream_t stream)
     const int lds = Cfg::WAVES * ring * Cfg::TASK_BYTES + 2 * Cfg::WAVES * red_rows * 64 + (Cfg::XLDS ? a.M * a.K * 2 : 0);
     if (lds > kMaxLds || ring < 1 || ring > Cfg::MAX_RING) return GF_ERR_UNSUPPORTED;
     parts = parts < ceil_div(a.N, 16) ? parts : ceil_div(a.N, 16);
-    const int64_t grid = (int64_t)parts * (GROUPED ? a.g.E : 1);
+    int64_t grid = parts;
+    if (GROUPED) grid *= a.g.T / (16 * Cfg::MB) + (a.g.E < a.g.T ? a.g.E : a.g.T);
     if (grid > kW4MaxGrid) return GF_ERR_INVALID_ARG;
     hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(Cfg::WAVES * 64), lds, stream, a, ring, parts);
     return w4_status(hipGetLastError());

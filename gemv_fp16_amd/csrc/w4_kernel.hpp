@@ -562,8 +562,8 @@ __global__ __launch_bounds__(Cfg::WAVES * 64) void w4_rows_kernel(W4Args a)
 // Each row group ends in one barrier; the sums' slots alternate.
 // XB == 0: A is copied to LDS once (chunk c of row m at slot c ^ m % 8);
 // otherwise each wave keeps its part of up to 16 * MB rows of A in registers, XB
-// blocks' worth.  Grouped: workgroup p of `parts` of expert e walks that expert's
-// row groups, once for every 16 * MB of its rows of A.
+// blocks' worth.  Grouped: `parts` workgroups walk the row groups of one expert
+// for each 16 * MB of its rows of A, so that an expert with many rows has many.
 // What is left is the vector ALU's work, so it is kept short: a task's addresses
 // are one scalar offset, a scale multiplies straight from its half of a word
 // (acc is in units of 2^-24 until the end), and a word unpacks in 10
@@ -606,22 +606,21 @@ __global__ __launch_bounds__(Cfg::WAVES * 64) void w4_band_kernel(W4Args a, int 
     const int r16 = lane % 16, c4 = lane / 16;
     const int N = a.N, K = a.K, G = a.G;
 
-    int part = blockIdx.x, rows = a.M;                    // of A, in all
+    int part = blockIdx.x, M = a.M;
     if constexpr (GROUPED) {
-        const int e = part / parts;
-        part -= e * parts;
-        int lo, hi;
-        a.g.rows(e, lo, hi);
-        rows = __builtin_amdgcn_readfirstlane(hi - lo);
-        if (rows == 0) return;
-        a.A += (size_t)lo * K;
-        a.C += (size_t)lo * N;
+        int e, lo, hi, item;
+        if (!a.g.template find<16 * MB>(blockIdx.x, parts, e, lo, hi, item)) return;
+        const int passes = ceil_div(hi - lo, 16 * MB);
+        part = item / passes;
+        const int first = lo + item % passes * 16 * MB;
+        M = min(hi - first, 16 * MB);
+        a.A += (size_t)first * K;
+        a.C += (size_t)first * N;
         a.Q += (size_t)e * N * (K / 8);
         a.S += (size_t)e * N * G;
         if (a.Z) a.Z += (size_t)e * N * G;
     }
-    constexpr int MR = 16 * MB;                           // rows of A in one pass
-    const int red_rows = GROUPED ? MR : a.M;
+    const int red_rows = GROUPED ? 16 * MB : M;
     GF_LDS char* tasks = (GF_LDS char*)w4_smem + wave * ring * Cfg::TASK_BYTES;
     GF_LDS float* red = (GF_LDS float*)((GF_LDS char*)w4_smem + WAVES * ring * Cfg::TASK_BYTES);
     GF_LDS char* xs = (GF_LDS char*)(red + 2 * WAVES * red_rows * 16);
@@ -659,12 +658,12 @@ __global__ __launch_bounds__(Cfg::WAVES * 64) void w4_band_kernel(W4Args a, int 
     // 128, else k = 32 i .. 32 i + 31.
     constexpr int xstep = GROUP == 128 ? 1 : 4;
     const int xchunk = GROUP == 128 ? 4 * c4 : c4;
-    const int xm = min(r16, rows - 1);
+    const int xm = min(r16, M - 1);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         xat[i] = (uint32_t)(xm * K * 2 + ((xchunk + xstep * i) ^ (xm & 7)) * 16 + b0 * (Cfg::BK * 2));
     if constexpr (Cfg::XLDS) {
-        const int per = K / 8, n = rows * per;            // 16-byte chunks
+        const int per = K / 8, n = M * per;               // 16-byte chunks
         for (int t0 = wave * kWave; t0 < n; t0 += WAVES * kWave) {
             const int t = min(t0 + lane, n - 1), m = t / per, j = t - m * per;
             __builtin_amdgcn_global_load_lds((const void*)(a.A + (size_t)m * K + (j ^ (m & 7)) * 8),
@@ -672,137 +671,133 @@ __global__ __launch_bounds__(Cfg::WAVES * 64) void w4_band_kernel(W4Args a, int 
         }
     }
 
-    for (int m0 = 0; m0 < (GROUPED ? rows : 1); m0 += MR) {
-        const int M = GROUPED ? min(rows - m0, MR) : rows;
-        // ---- direct loads of a task ----
-        const int ntasks = ng * nb;
-        int ig = part, ib = 0, islot = 0, issued = 0;     // the next task to issue
-        auto issue = [&]() __attribute__((always_inline)) {
-            GF_LDS char* buf = tasks + islot * Cfg::TASK_BYTES;
-            const int n0 = min(ig * 16, N - 16);
-            const uint32_t so = (uint32_t)__builtin_amdgcn_readfirstlane(n0 * (K / 2) + (b0 + ib) * (Cfg::BK / 2));
+    // ---- direct loads of a task ----
+    const int ntasks = ng * nb;
+    int ig = part, ib = 0, islot = 0, issued = 0;     // the next task to issue
+    auto issue = [&]() __attribute__((always_inline)) {
+        GF_LDS char* buf = tasks + islot * Cfg::TASK_BYTES;
+        const int n0 = min(ig * 16, N - 16);
+        const uint32_t so = (uint32_t)__builtin_amdgcn_readfirstlane(n0 * (K / 2) + (b0 + ib) * (Cfg::BK / 2));
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rq, (GF_LDS void*)(buf + i * 1024), 16, qoff[i], so, 0, 2);
-            const size_t at = (size_t)n0 * G + (b0 + ib) * GPB;
+        for (int i = 0; i < 4; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rq, (GF_LDS void*)(buf + i * 1024), 16, qoff[i], so, 0, 2);
+        const size_t at = (size_t)n0 * G + (b0 + ib) * GPB;
 #pragma unroll
-            for (int i = 0; i < Cfg::SLOADS + Cfg::ZLOADS; ++i)
-                __builtin_amdgcn_global_load_lds((const void*)(szp[i] + (at << szshift[i])),
-                                                 (GF_LDS void*)(buf + 4096 + i * 256), 4, 0, 0);
-            ++issued;
-            if (++ib == nb) { ib = 0; ig += parts; }
-            if (++islot == ring) islot = 0;
-        };
-        // At most `left` younger tasks' loads stay pending.
-        auto wait_tasks = [&](int left) __attribute__((always_inline)) {
-            left = __builtin_amdgcn_readfirstlane(left);
-            if (left >= 3) wait_vmcnt<3 * L>();
-            else if (left == 2) wait_vmcnt<2 * L>();
-            else if (left == 1) wait_vmcnt<L>();
-            else wait_vmcnt<0>();
-        };
-        const int first = min(ring, ntasks);
-        for (int i = 0; i < first; ++i) issue();
-        half8 xreg[Cfg::XLDS ? 1 : Cfg::XB * 16][MB];
-        if constexpr (!Cfg::XLDS) {
+        for (int i = 0; i < Cfg::SLOADS + Cfg::ZLOADS; ++i)
+            __builtin_amdgcn_global_load_lds((const void*)(szp[i] + (at << szshift[i])),
+                                             (GF_LDS void*)(buf + 4096 + i * 256), 4, 0, 0);
+        ++issued;
+        if (++ib == nb) { ib = 0; ig += parts; }
+        if (++islot == ring) islot = 0;
+    };
+    // At most `left` younger tasks' loads stay pending.
+    auto wait_tasks = [&](int left) __attribute__((always_inline)) {
+        left = __builtin_amdgcn_readfirstlane(left);
+        if (left >= 3) wait_vmcnt<3 * L>();
+        else if (left == 2) wait_vmcnt<2 * L>();
+        else if (left == 1) wait_vmcnt<L>();
+        else wait_vmcnt<0>();
+    };
+    const int first = min(ring, ntasks);
+    for (int i = 0; i < first; ++i) issue();
+    half8 xreg[Cfg::XLDS ? 1 : Cfg::XB * 16][MB];
+    if constexpr (!Cfg::XLDS) {
 #pragma unroll
-            for (int b = 0; b < Cfg::XB; ++b)
+        for (int b = 0; b < Cfg::XB; ++b)
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
+            for (int i = 0; i < 16; ++i)
 #pragma unroll
-                    for (int m = 0; m < MB; ++m) {
-                        const half8 v = *(const half8*)(
-                            a.A + (size_t)(m0 + min(16 * m + r16, M - 1)) * K +
-                            min(b0 + b, nblk - 1) * Cfg::BK + (i / 4) * 128 + (xchunk + xstep * (i % 4)) * 8);
-                        xreg[b * 16 + i][m] = __builtin_shufflevector(v, v, 0, 4, 1, 5, 2, 6, 3, 7);
-                    }
-        }
-        if constexpr (Cfg::XLDS) {                        // A has landed: only whole tasks are pending
-            if (first >= 4) wait_vmcnt<4 * L>();
-            else wait_tasks(first);
-            lds_barrier();
-        }
-
-        int done = 0, slot = 0;
-        for (int gi = 0; gi < ng; ++gi) {
-            floatx4 acc[MB] = {};
-            auto block = [&](int b, auto xb_c) __attribute__((always_inline)) {
-                constexpr int xb = decltype(xb_c)::value;
-                wait_tasks(issued - done - 1);
-                asm volatile("" ::: "memory");
-                const GF_LDS char* buf = tasks + slot * Cfg::TASK_BYTES;
-                const GF_LDS uint32_t* sz = (const GF_LDS uint32_t*)(buf + 4096) + r16;
-                uint32_t sw[Cfg::SWORDS], zw[Cfg::ZWORDS];
-#pragma unroll
-                for (int j = 0; j < Cfg::SWORDS; ++j) sw[j] = sz[16 * j];
-#pragma unroll
-                for (int j = 0; j < Cfg::ZWORDS; ++j)
-                    zw[j] = a.Z ? sz[16 * ((GROUP == 128 ? 2 : Cfg::SLOADS * 4) + j)] : 0x08080808u;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {             // chunks of 128 k
-                    u32x4 q = *(const GF_LDS u32x4*)(buf + qat[c]);
-                    if constexpr (GROUP < 128) q = w4_exchange(q);
-                    constexpr int SPG = GROUP / 32, GPC = 128 / GROUP;
-#pragma unroll
-                    for (int g0 = 0; g0 < GPC; ++g0) {
-                        const int g = c * GPC + g0;       // within the block
-                        const _Float16 s = __builtin_bit_cast(_Float16, (uint16_t)(sw[g / 2] >> (16 * (g % 2))));
-                        const half2v nz = -__builtin_bit_cast(half2v, __builtin_amdgcn_perm(
-                            0u, zw[g / 4], 0x0c000c00u + 0x00010001u * (uint32_t)(g % 4)));
-                        floatx4 sum[MB] = {};
-#pragma unroll
-                        for (int i = g0 * SPG; i < (g0 + 1) * SPG; ++i) {
-                            if constexpr (Cfg::XLDS) {
-                                const half8 x = *(const GF_LDS half8*)(xs + xat[i] + b * (Cfg::BK * 2) + c * 256);
-                                sum[0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, w4_unpack(q[i], nz), sum[0], 0, 0, 0);
-                            } else {
-                                const half8 w = w4_unpack_pairs(q[i], nz);
-#pragma unroll
-                                for (int m = 0; m < MB; ++m)
-                                    sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xreg[xb * 16 + 4 * c + i][m], w,
-                                                                                    sum[m], 0, 0, 0);
-                            }
-                        }
-#pragma unroll
-                        for (int m = 0; m < MB; ++m)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) acc[m][i] = fmaf(sum[m][i], (float)s, acc[m][i]);
-                    }
+                for (int m = 0; m < MB; ++m) {
+                    const half8 v = *(const half8*)(
+                        a.A + (size_t)min(16 * m + r16, M - 1) * K +
+                        min(b0 + b, nblk - 1) * Cfg::BK + (i / 4) * 128 + (xchunk + xstep * (i % 4)) * 8);
+                    xreg[b * 16 + i][m] = __builtin_shufflevector(v, v, 0, 4, 1, 5, 2, 6, 3, 7);
                 }
-                asm volatile("" ::: "memory");
-                wait_lgkmcnt0();                          // the buffer is read: it may be filled again
-                if (issued < ntasks) issue();
-                ++done;
-                if (++slot == ring) slot = 0;
-            };
-            if constexpr (Cfg::XLDS) {
-                for (int b = 0; b < nb; ++b) block(b, std::integral_constant<int, 0>{});
-            } else {
-                static_for<Cfg::XB>([&](auto xb) __attribute__((always_inline)) {
-                    if (decltype(xb)::value < nb) block(decltype(xb)::value, xb);
-                });
-            }
-            // ---- the waves' sums, in wave order ----
-            GF_LDS float* mine = red + (gi & 1) * WAVES * red_rows * 16;
-#pragma unroll
-            for (int m = 0; m < MB; ++m)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int row = 16 * m + 4 * c4 + i;
-                    if (row < M) mine[(wave * red_rows + row) * 16 + r16] = acc[m][i];
-                }
-            lds_barrier();
-            const int n0 = min((part + gi * parts) * 16, N - 16);
-            for (int t = threadIdx.x; t < M * 16; t += WAVES * kWave) {
-                float s = 0.0f;
-#pragma unroll
-                for (int w = 0; w < WAVES; ++w) s += mine[w * red_rows * 16 + t];
-                a.C[(size_t)(m0 + t / 16) * N + n0 + t % 16] = f32_to_f16_bits(s * kW4Unit);
-            }
-        }
-        wait_vmcnt<0>();
-        if constexpr (GROUPED) lds_barrier();             // the next pass reuses the sums' slots
     }
+    if constexpr (Cfg::XLDS) {                        // A has landed: only whole tasks are pending
+        if (first >= 4) wait_vmcnt<4 * L>();
+        else wait_tasks(first);
+        lds_barrier();
+    }
+
+    int done = 0, slot = 0;
+    for (int gi = 0; gi < ng; ++gi) {
+        floatx4 acc[MB] = {};
+        auto block = [&](int b, auto xb_c) __attribute__((always_inline)) {
+            constexpr int xb = decltype(xb_c)::value;
+            wait_tasks(issued - done - 1);
+            asm volatile("" ::: "memory");
+            const GF_LDS char* buf = tasks + slot * Cfg::TASK_BYTES;
+            const GF_LDS uint32_t* sz = (const GF_LDS uint32_t*)(buf + 4096) + r16;
+            uint32_t sw[Cfg::SWORDS], zw[Cfg::ZWORDS];
+#pragma unroll
+            for (int j = 0; j < Cfg::SWORDS; ++j) sw[j] = sz[16 * j];
+#pragma unroll
+            for (int j = 0; j < Cfg::ZWORDS; ++j)
+                zw[j] = a.Z ? sz[16 * ((GROUP == 128 ? 2 : Cfg::SLOADS * 4) + j)] : 0x08080808u;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {             // chunks of 128 k
+                u32x4 q = *(const GF_LDS u32x4*)(buf + qat[c]);
+                if constexpr (GROUP < 128) q = w4_exchange(q);
+                constexpr int SPG = GROUP / 32, GPC = 128 / GROUP;
+#pragma unroll
+                for (int g0 = 0; g0 < GPC; ++g0) {
+                    const int g = c * GPC + g0;       // within the block
+                    const _Float16 s = __builtin_bit_cast(_Float16, (uint16_t)(sw[g / 2] >> (16 * (g % 2))));
+                    const half2v nz = -__builtin_bit_cast(half2v, __builtin_amdgcn_perm(
+                        0u, zw[g / 4], 0x0c000c00u + 0x00010001u * (uint32_t)(g % 4)));
+                    floatx4 sum[MB] = {};
+#pragma unroll
+                    for (int i = g0 * SPG; i < (g0 + 1) * SPG; ++i) {
+                        if constexpr (Cfg::XLDS) {
+                            const half8 x = *(const GF_LDS half8*)(xs + xat[i] + b * (Cfg::BK * 2) + c * 256);
+                            sum[0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, w4_unpack(q[i], nz), sum[0], 0, 0, 0);
+                        } else {
+                            const half8 w = w4_unpack_pairs(q[i], nz);
+#pragma unroll
+                            for (int m = 0; m < MB; ++m)
+                                sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xreg[xb * 16 + 4 * c + i][m], w,
+                                                                                sum[m], 0, 0, 0);
+                        }
+                    }
+#pragma unroll
+                    for (int m = 0; m < MB; ++m)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[m][i] = fmaf(sum[m][i], (float)s, acc[m][i]);
+                }
+            }
+            asm volatile("" ::: "memory");
+            wait_lgkmcnt0();                          // the buffer is read: it may be filled again
+            if (issued < ntasks) issue();
+            ++done;
+            if (++slot == ring) slot = 0;
+        };
+        if constexpr (Cfg::XLDS) {
+            for (int b = 0; b < nb; ++b) block(b, std::integral_constant<int, 0>{});
+        } else {
+            static_for<Cfg::XB>([&](auto xb) __attribute__((always_inline)) {
+                if (decltype(xb)::value < nb) block(decltype(xb)::value, xb);
+            });
+        }
+        // ---- the waves' sums, in wave order ----
+        GF_LDS float* mine = red + (gi & 1) * WAVES * red_rows * 16;
+#pragma unroll
+        for (int m = 0; m < MB; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = 16 * m + 4 * c4 + i;
+                if (row < M) mine[(wave * red_rows + row) * 16 + r16] = acc[m][i];
+            }
+        lds_barrier();
+        const int n0 = min((part + gi * parts) * 16, N - 16);
+        for (int t = threadIdx.x; t < M * 16; t += WAVES * kWave) {
+            float s = 0.0f;
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) s += mine[w * red_rows * 16 + t];
+            a.C[(size_t)(t / 16) * N + n0 + t % 16] = f32_to_f16_bits(s * kW4Unit);
+        }
+    }
+    wait_vmcnt<0>();
 #endif
 }
 
