@@ -131,12 +131,12 @@ int launch_band(const W4Args& a, int ring, int parts, hipStream_t stream)
     constexpr int kMaxLds = 160 * 1024;
     const hipError_t e = opt_in_lds((const void*)kern, kMaxLds, lds_opt_in, stream);
     if (e != hipSuccess) return GF_ERR_HIP;
-    const int red_rows = GROUPED ? 16 * Cfg::MB : a.M;
+    const int red_rows = !GROUPED && a.M < 16 * Cfg::MB ? a.M : 16 * Cfg::MB;
     const int lds = Cfg::WAVES * ring * Cfg::TASK_BYTES + 2 * Cfg::WAVES * red_rows * 64 + (Cfg::XLDS ? a.M * a.K * 2 : 0);
     if (lds > kMaxLds || ring < 1 || ring > Cfg::MAX_RING) return GF_ERR_UNSUPPORTED;
     parts = parts < ceil_div(a.N, 16) ? parts : ceil_div(a.N, 16);
-    int64_t grid = parts;
-    if (GROUPED) grid *= a.g.T / (16 * Cfg::MB) + (a.g.E < a.g.T ? a.g.E : a.g.T);
+    int64_t grid = Cfg::XLDS ? parts : (int64_t)ceil_div(parts, 8) * 8 * ceil_div(a.M, 16 * Cfg::MB);
+    if (GROUPED) grid = (int64_t)parts * (a.g.T / (16 * Cfg::MB) + (a.g.E < a.g.T ? a.g.E : a.g.T));
     if (grid > kW4MaxGrid) return GF_ERR_INVALID_ARG;
     hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(Cfg::WAVES * 64), lds, stream, a, ring, parts);
     return w4_status(hipGetLastError());
@@ -144,26 +144,30 @@ int launch_band(const W4Args& a, int ring, int parts, hipStream_t stream)
 
 // The band form's launch.  One weight: two workgroups to a CU, with as much in
 // flight as their LDS leaves, where there are row groups for them and the
-// registers allow it (not with A in registers); else one with all of it.  Grouped:
-// about 256 workgroups in all but at least 8 a group, two tasks in flight a wave
-// (25 us against 32 with twice as many and four, at 24 rows over 16 groups of
-// 4096 x 4096; 18 against 30 at 16 over 8 of 2048 x 8192).
+// registers allow it (not with A in registers); else one with all of it, shared
+// among the passes over 16 MB rows of A each.  Grouped: about 256 workgroups in
+// all but at least 8 to a pass, two tasks in flight a wave (24 us against 31 with
+// twice as many and four, at 24 rows over 16 groups of 4096 x 4096; 15 against 22
+// with twice as many at 16 over 8 of 2048 x 8192).
 template <class Cfg, bool GROUPED>
 int band(const W4Args& a, hipStream_t stream)
 {
     if constexpr (GROUPED) {
-        const int want = 256 / a.g.E;
+        const int64_t passes = (a.g.E < a.g.T ? a.g.E : a.g.T) + a.g.T / (16 * Cfg::MB);
+        const int want = (int)(256 / passes + 7) / 8 * 8;
         return launch_band<Cfg, true>(a, 2, want < 8 ? 8 : (want > 64 ? 64 : want), stream);
     } else {
-        const int fixed = 2 * Cfg::WAVES * a.M * 64 + (Cfg::XLDS ? a.M * a.K * 2 : 0);
+        const int passes = ceil_div(a.M, 16 * Cfg::MB), rows = passes > 1 ? 16 * Cfg::MB : a.M;
+        const int fixed = 2 * Cfg::WAVES * rows * 64 + (Cfg::XLDS ? a.M * a.K * 2 : 0);
         const int per_task = Cfg::WAVES * Cfg::TASK_BYTES;
         const int groups = ceil_div(a.N, 16);
         const int per_cu = Cfg::XLDS && groups > 256 && fixed + per_task <= 80 * 1024 ? 2 : 1;
         int ring = (160 * 1024 / per_cu - fixed) / per_task;
-        const int tasks = ceil_div(groups, 256 * per_cu) * ceil_div(a.K, Cfg::BK * Cfg::WAVES);   // of a wave
+        const int parts = passes > 1 ? 256 / passes / 8 * 8 : 256 * per_cu;   // (of each pass, dealt to 8 XCDs)
+        const int tasks = ceil_div(groups, parts) * ceil_div(a.K, Cfg::BK * Cfg::WAVES);   // of a wave
         if (ring > Cfg::MAX_RING) ring = Cfg::MAX_RING;
         if (ring > tasks) ring = tasks;
-        return launch_band<Cfg, false>(a, ring, 256 * per_cu, stream);
+        return launch_band<Cfg, false>(a, ring, parts, stream);
     }
 }
 
@@ -198,32 +202,51 @@ int tile(const W4Args& a, int64_t rows, hipStream_t stream)
 }
 
 // Which form, by the rows of A (of a group, on average) and by what the operands'
-// sizes and alignment allow.  The tile form rounds weights to fp16, which one
-// weight's users see from 65 rows on; between 17 and 64 rows the streaming forms
-// are also the faster ones there (16 us against 31 at 24 x 11008 x 4096, 13
-// against 31 at 64 x 4096 x 4096).  Groups of that size stream badly (every group
-// has its own uneven rest), and take the tiles from a mean of 17 rows.
+// sizes and alignment allow.  Timed side by side (us):
+//  * one weight, up to 64 rows: the band form, in passes of 16 rows of A, or of 32
+//    where 16 would make more than two sweeps of the chip (12 against 15 at 24 x
+//    11008 x 4096, but 7.3 against 8.4 at 24 x 4096 x 4096).  At 64 x 4096 x 4096 it
+//    takes 9.8, the general form 13, tiles 31.  Up to 32768 entries of A in one
+//    pass lie in LDS instead (4.8 against 5.7 at 9 x 2048 x 2048).  From 65 rows on,
+//    tiles.
+//  * grouped, the band form up to a mean of 16 rows, and of 32 where K is long (21
+//    against 33 at 200 rows over 8 groups of 2048 x 4096; 39 against 24 at 600 over
+//    16 of 2048 x 2048), in passes of 32 rows from a mean of 9 on (42 against 55 at
+//    150 over 16 of 4096 x 4096); then tiles.
+//  * what is left takes the general form, with 16 rows of A by 32 of Q (16 by 16
+//    for few rows of both; 32 by 64 for many rows of both where groups of 128
+//    leave the registers for it: 23 against 38 at 32 x 16384 x 5000, but 40 against
+//    44 the other way round, spilling, with groups of 64).
 template <int GROUP, bool GROUPED>
 int product(const W4Args& a, hipStream_t stream)
 {
     const int64_t rows = GROUPED ? (a.g.T + a.g.E - 1) / a.g.E : a.M;
-    if (rows > (GROUPED ? 16 : 64) && w4_aligned(a.A, 16) && a.K >= 64) return tile<GROUP, GROUPED>(a, rows, stream);
     const bool wide = w4_aligned(a.A, 16) && w4_aligned(a.Q, 16) && w4_aligned(a.S, 16) && w4_aligned(a.Z, 8);
     if (wide && a.K % 512 == 0 && a.K > 0 && a.N >= 16) {
-        if constexpr (!GROUPED)
+        if constexpr (GROUPED) {
+            if ((rows <= 16 || (rows <= 32 && a.K >= 4096)) && a.K <= 8192) {
+                if (a.K > 4096) return band<W4BandCfg<GROUP, 1, 2>, true>(a, stream);
+                if constexpr (GROUP > 32)
+                    if (rows > 8) return band<W4BandCfg<GROUP, 2, 1>, true>(a, stream);
+                return band<W4BandCfg<GROUP, 1, 1>, true>(a, stream);
+            }
+        } else {
             if (a.M <= 16 && a.M * a.K <= 32768) return band<W4BandCfg<GROUP, 1, 0>, false>(a, stream);
-        if (rows <= 16 && a.K <= 4096) return band<W4BandCfg<GROUP, 1, 1>, GROUPED>(a, stream);
-        if (rows <= 16 && a.K <= 8192) return band<W4BandCfg<GROUP, 1, 2>, GROUPED>(a, stream);
-        if constexpr (!GROUPED)
-            if (rows <= 32 && a.K <= 4096) return band<W4BandCfg<GROUP, 2, 1>, false>(a, stream);
+            if (a.M <= 64 && a.K <= 8192) {
+                if (a.K > 4096) return band<W4BandCfg<GROUP, 1, 2>, false>(a, stream);
+                if constexpr (GROUP > 32)                 // (spills with groups of 32)
+                    if (a.M > 16 && ceil_div(a.M, 16) * ceil_div(a.N, 16) > 512)
+                        return band<W4BandCfg<GROUP, 2, 1>, false>(a, stream);
+                return band<W4BandCfg<GROUP, 1, 1>, false>(a, stream);
+            }
+        }
     }
+    if (rows > (GROUPED ? 16 : 64) && w4_aligned(a.A, 16) && a.K >= 64) return tile<GROUP, GROUPED>(a, rows, stream);
     constexpr int CB = GROUP == 32 ? 2 : 4;
-    if (rows <= 16)
-        return a.N >= 8192 ? launch_rows<W4RowsCfg<GROUP, 1, 2, 8, CB>, GROUPED>(a, stream)
-                           : launch_rows<W4RowsCfg<GROUP, 1, 1, 8, CB>, GROUPED>(a, stream);
-    if constexpr (!GROUPED)
-        if (rows > 32 && a.N >= 8192) return launch_rows<W4RowsCfg<GROUP, 2, 4, 4, 2>, false>(a, stream);
-    return launch_rows<W4RowsCfg<GROUP, 2, 2, 8, CB>, GROUPED>(a, stream);
+    if constexpr (GROUP == 128)
+        if (rows > 16 && a.N >= 8192) return launch_rows<W4RowsCfg<GROUP, 2, 4, 4, 2>, GROUPED>(a, stream);
+    return rows > 16 || a.N >= 8192 ? launch_rows<W4RowsCfg<GROUP, 1, 2, 8, CB>, GROUPED>(a, stream)
+                                    : launch_rows<W4RowsCfg<GROUP, 1, 1, 8, CB>, GROUPED>(a, stream);
 }
 
 template <bool GROUPED>

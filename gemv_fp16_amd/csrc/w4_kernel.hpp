@@ -11,7 +11,8 @@
 // operation gives q - z (exact: small integers times 2^-24), and the products
 // a * (q - z) are summed in fp32 within a group.  Each group's sum is then scaled by
 // s * 2^24 in fp32, so that the only rounding to fewer bits is that of the
-// output: weights are never rounded to fp16.
+// output.  That is how few rows of A are multiplied; the tiles for many rows round
+// each weight to fp16 first (why, and what it buys, stands there).
 #pragma once
 #include "common.hpp"
 #include "gemv_kernel.hpp"
@@ -561,9 +562,11 @@ __global__ __launch_bounds__(Cfg::WAVES * 64) void w4_rows_kernel(W4Args a)
 // scales and zero points as 32-bit words, word j of row n at 16 j + n.
 // Each row group ends in one barrier; the sums' slots alternate.
 // XB == 0: A is copied to LDS once (chunk c of row m at slot c ^ m % 8);
-// otherwise each wave keeps its part of up to 16 * MB rows of A in registers, XB
-// blocks' worth.  Grouped: `parts` workgroups walk the row groups of one expert
-// for each 16 * MB of its rows of A, so that an expert with many rows has many.
+// otherwise each wave keeps its part of 16 * MB rows of A in registers, XB blocks'
+// worth, read through the tasks' buffers in whole lines as well (operands loaded
+// from A straight: 18.0 us against 12.8 at 32 x 11008 x 4096, 14.7 against 8.7 at
+// 16 x 4096 x 8192).  More rows are further passes, by workgroups of their own;
+// grouped, an expert with many rows has many.
 // What is left is the vector ALU's work, so it is kept short: a task's addresses
 // are one scalar offset, a scale multiplies straight from its half of a word
 // (acc is in units of 2^-24 until the end), and a word unpacks in 10
@@ -619,8 +622,17 @@ __global__ __launch_bounds__(Cfg::WAVES * 64) void w4_band_kernel(W4Args a, int 
         a.Q += (size_t)e * N * (K / 8);
         a.S += (size_t)e * N * G;
         if (a.Z) a.Z += (size_t)e * N * G;
+    } else if constexpr (!Cfg::XLDS) {
+        // passes over the same rows of Q on one XCD, at the same time
+        const int passes = ceil_div(M, 16 * MB), x = part / 8;
+        part = x / passes * 8 + part % 8;
+        if (part >= parts) return;
+        const int first = x % passes * 16 * MB;
+        M = min(M - first, 16 * MB);
+        a.A += (size_t)first * K;
+        a.C += (size_t)first * N;
     }
-    const int red_rows = GROUPED ? 16 * MB : M;
+    const int red_rows = GROUPED ? 16 * MB : min(a.M, 16 * MB);
     GF_LDS char* tasks = (GF_LDS char*)w4_smem + wave * ring * Cfg::TASK_BYTES;
     GF_LDS float* red = (GF_LDS float*)((GF_LDS char*)w4_smem + WAVES * ring * Cfg::TASK_BYTES);
     GF_LDS char* xs = (GF_LDS char*)(red + 2 * WAVES * red_rows * 16);
@@ -698,29 +710,72 @@ __global__ __launch_bounds__(Cfg::WAVES * 64) void w4_band_kernel(W4Args a, int 
         else if (left == 1) wait_vmcnt<L>();
         else wait_vmcnt<0>();
     };
-    const int first = min(ring, ntasks);
-    for (int i = 0; i < first; ++i) issue();
+    int done = 0, slot = 0;
     half8 xreg[Cfg::XLDS ? 1 : Cfg::XB * 16][MB];
-    if constexpr (!Cfg::XLDS) {
-#pragma unroll
-        for (int b = 0; b < Cfg::XB; ++b)
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-#pragma unroll
-                for (int m = 0; m < MB; ++m) {
-                    const half8 v = *(const half8*)(
-                        a.A + (size_t)min(16 * m + r16, M - 1) * K +
-                        min(b0 + b, nblk - 1) * Cfg::BK + (i / 4) * 128 + (xchunk + xstep * (i % 4)) * 8);
-                    xreg[b * 16 + i][m] = __builtin_shufflevector(v, v, 0, 4, 1, 5, 2, 6, 3, 7);
-                }
-    }
-    if constexpr (Cfg::XLDS) {                        // A has landed: only whole tasks are pending
-        if (first >= 4) wait_vmcnt<4 * L>();
+    if constexpr (Cfg::XLDS) {
+        const int first = min(ring, ntasks);
+        for (int i = 0; i < first; ++i) issue();
+        if (first >= 4) wait_vmcnt<4 * L>();              // A has landed: only whole tasks are pending
         else wait_tasks(first);
         lds_barrier();
+    } else if (nb > 0) {
+        // A passes through the tasks' buffers too, 16 rows by 128 k at a time, so
+        // that it is read in whole lines; the tasks follow it.
+        constexpr int P = Cfg::XB * 4 * MB;
+        const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
+            (void*)a.A, 0, (int)((uint32_t)M * (uint32_t)K * 2u), 0x00020000);
+        uint32_t xoff[MB][4];
+#pragma unroll
+        for (int m = 0; m < MB; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 4 * i + c4;
+                xoff[m][i] = (uint32_t)min(16 * m + r, M - 1) * (uint32_t)K * 2u + (uint32_t)(r16 ^ r) * 16u;
+            }
+        auto issue_x = [&](auto p_c) __attribute__((always_inline)) {
+            constexpr int b = decltype(p_c)::value / (4 * MB), c = decltype(p_c)::value / MB % 4,
+                          m = decltype(p_c)::value % MB;
+            GF_LDS char* buf = tasks + islot * Cfg::TASK_BYTES;
+            const uint32_t so = (uint32_t)__builtin_amdgcn_readfirstlane(
+                min(b0 + b, nblk - 1) * (Cfg::BK * 2) + c * 256);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (GF_LDS void*)(buf + i * 1024), 16, xoff[m][i], so, 0, 0);
+            if (++islot == ring) islot = 0;
+        };
+        static_for<Cfg::MAX_RING < P ? Cfg::MAX_RING : P>([&](auto p) __attribute__((always_inline)) {
+            if (decltype(p)::value < ring) issue_x(p);
+        });
+        static_for<P>([&](auto p_c) __attribute__((always_inline)) {
+            constexpr int p = decltype(p_c)::value, b = p / (4 * MB), c = p / MB % 4, m = p % MB;
+            // younger pieces and tasks, of 4 loads at least
+            const int left = __builtin_amdgcn_readfirstlane(min(p + ring, P) + issued - p - 1);
+            if (left >= 3) wait_vmcnt<12>();
+            else if (left == 2) wait_vmcnt<8>();
+            else if (left == 1) wait_vmcnt<4>();
+            else wait_vmcnt<0>();
+            asm volatile("" ::: "memory");
+            const GF_LDS char* buf = tasks + slot * Cfg::TASK_BYTES;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const half8 v = *(const GF_LDS half8*)(buf + r16 * 256 + (((xchunk + xstep * i) ^ r16) * 16));
+                xreg[b * 16 + c * 4 + i][m] = __builtin_shufflevector(v, v, 0, 4, 1, 5, 2, 6, 3, 7);
+            }
+            asm volatile("" ::: "memory");
+            wait_lgkmcnt0();
+            // the freed buffer: the piece after those in flight (rings of 1 to 4),
+            // or the next task
+            static_for<Cfg::MAX_RING>([&](auto r) __attribute__((always_inline)) {
+                constexpr int ahead = decltype(r)::value + 1;
+                if (ring == ahead) {
+                    if constexpr (p + ahead < P) issue_x(std::integral_constant<int, p + ahead>{});
+                    else if (issued < ntasks) issue();
+                }
+            });
+            if (++slot == ring) slot = 0;
+        });
     }
 
-    int done = 0, slot = 0;
     for (int gi = 0; gi < ng; ++gi) {
         floatx4 acc[MB] = {};
         auto block = [&](int b, auto xb_c) __attribute__((always_inline)) {

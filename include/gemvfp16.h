@@ -353,9 +353,11 @@ int gf_sp_default_config(int M, int N, int K, gf_sp_cfg* out);
  * in C, but no access outside the operands.
  * Every group's part of an operand, and each of A and C as a whole, must be
  * smaller than 2^31 elements; B as a whole may be larger.  fp32 accumulation,
- * one rounding at the end; a group's results do not depend on the other
- * groups' rows or sizes except through the tile the library picks from T / E
- * (the tile shapes add the same products in the same order).
+ * one rounding at the end.  A group's results do not depend on the other groups'
+ * rows or sizes except through the form the library picks from T / E: the tiles
+ * add the same products in the same order, the streaming form (up to 12 rows a
+ * group on average, nt only) adds eight parts of K.  Results repeat bit for bit
+ * from run to run.
  *
  * gemm_f16_grouped_nt: C[r] = A[r] . B[e]^T for the rows r of group e: A T x K,
  * B E x N x K, C T x N, all fp16.  The forward product of an expert layer.
@@ -368,8 +370,7 @@ int gf_sp_default_config(int M, int N, int K, gf_sp_cfg* out);
  * weights.  Every group's C is written: an empty group gives +0 everywhere.
  * K == 0 (or an empty group in the tn form) is the empty sum.  The fast path
  * needs 16-byte aligned A, B, C and each operand's contiguous extent a multiple
- * of 8 (N in the nt form excepted); anything else runs a masked path with the
- * same result.
+ * of 8 (N in the nt form excepted); anything else runs masked tiles.
  * GF_ERR_INVALID_ARG for negative sizes, NULL or misaligned pointers, operands
  * past the limits, or c_f32 other than 0 or 1.
  */
@@ -406,14 +407,16 @@ int gemm_f16_grouped_tn(const void* A, const void* B, void* C, const int* offset
  * rounded once to fp16: the weights themselves are not rounded.  From 65 rows on
  * the matrix cores are the bound, and each weight is rounded once to fp16 first,
  * as w4_dequantize_f16 rounds it; sums are in fp32 all the same.  (Where K < 64
- * or A is not 16-byte aligned, the first way holds for any number of rows.)  Results repeat bit for bit
- * from run to run.
+ * or A is not 16-byte aligned, the first way holds for any number of rows.)
+ * Results repeat bit for bit from run to run.
  * gemm_w4_f16_grouped_nt: gemm_f16_grouped_nt with 4-bit weights, Q E x N x
  * K/8, S and Z E x N x G; offsets and rows as there.  Its weights are rounded
- * as above from a mean of 17 rows a group (T > 16 E) on.
- * Entries of Z above 15 are outside the contract (no fault).  The fast path
- * needs A and Q 16-byte aligned and K % 32 == 0.  M == 0 or N == 0 is a
- * no-op; K == 0 writes +0.  Each operand (a group's part of Q) must stand for
+ * as above, or are not, from a mean of 17 rows a group (T > 16 E) on, as the form
+ * that is taken has it; up to there they are not.
+ * Entries of Z above 15 are outside the contract (no fault).  Up to 64 rows (32 a
+ * group) the fastest form needs K % 512 == 0, K <= 8192, A, Q and S 16-byte and Z
+ * 8-byte aligned; the tiles need A 16-byte aligned and run best with K % 256 == 0; a
+ * general form takes the rest.  M == 0 or N == 0 is a no-op; K == 0 writes +0.  Each operand (a group's part of Q) must stand for
  * fewer than 2^31 elements.  GF_ERR_INVALID_ARG for K % 8 != 0, another group
  * size, negative sizes, NULL or misaligned pointers, or sizes past the limit.
  */

@@ -159,6 +159,34 @@ def test_w4_grouped_tiles(sizes, K, group):
             _check(C[r], A[r], W.t().contiguous(), K, "group %d" % e, rounded=True)
 
 
+@pytest.mark.parametrize("M", [9, 17, 33, 48, 64])
+@pytest.mark.parametrize("N,K", [(17, 512), (1000, 2048), (9000, 4096), (3000, 8192), (300, 1536), (9000, 2008)])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_w4_passes_of_rows(M, N, K, group):
+    """Up to 64 rows: passes of 16 and 32 rows in the streaming form, and the general one."""
+    A, (Q, S, Z) = _half(20, M, K), _codes(21, (N,), K, group, zeros=group != 32)
+    _say("w4 passes", M, N, K, group)
+    C = gf.gemm_w4_f16_nt(A, Q, S, Z, group=group)
+    torch.cuda.synchronize()
+    _check(C, A, _weights(Q, S, Z, group).t().contiguous(), K, "passes")
+
+
+@pytest.mark.parametrize("sizes", [(10, 12, 0, 15), (40, 0, 33, 31), (1, 99, 0, 2)])
+@pytest.mark.parametrize("N,K", [(200, 4096), (700, 8192), (70, 512)])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_w4_grouped_passes_of_rows(sizes, N, K, group):
+    E, T, off = len(sizes), sum(sizes), plain.offsets_of(sizes)
+    A, (Q, S, Z) = _half(22, T, K), _codes(23, (E, N), K, group, zeros=group != 64)
+    _say("w4 grouped passes", sizes, N, K, group)
+    C = gf.gemm_w4_f16_grouped_nt(A, Q, S, Z, dev(off), group=group)
+    torch.cuda.synchronize()
+    for e in range(E):
+        r = slice(int(off[e]), int(off[e + 1]))
+        if sizes[e]:
+            W = _weights(Q[e], S[e], None if Z is None else Z[e], group)
+            _check(C[r], A[r], W.t().contiguous(), K, "group %d" % e, rounded=T > 16 * E)
+
+
 # ---- offsets past 32 bits -------------------------------------------------
 
 def _columns(N):
