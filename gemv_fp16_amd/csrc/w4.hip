@@ -163,7 +163,8 @@ int band(const W4Args& a, hipStream_t stream)
         const int groups = ceil_div(a.N, 16);
         const int per_cu = Cfg::XLDS && groups > 256 && fixed + per_task <= 80 * 1024 ? 2 : 1;
         int ring = (160 * 1024 / per_cu - fixed) / per_task;
-        const int parts = passes > 1 ? 256 / passes / 8 * 8 : 256 * per_cu;   // (of each pass, dealt to 8 XCDs)
+        // (of each pass, dealt to 8 XCDs)
+        const int parts = passes == 1 ? 256 * per_cu : passes <= 32 ? 256 / passes / 8 * 8 : 8;
         const int tasks = ceil_div(groups, parts) * ceil_div(a.K, Cfg::BK * Cfg::WAVES);   // of a wave
         if (ring > Cfg::MAX_RING) ring = Cfg::MAX_RING;
         if (ring > tasks) ring = tasks;
@@ -175,12 +176,14 @@ int band(const W4Args& a, hipStream_t stream)
 //  * one weight: 256 x 256 where they fill the CUs (129 against 138 for 128 x 256
 //    at 2048 x 8192 x 4096), else 128 x 256 with 8 waves from 400 tiles of 128 x
 //    128 (70 against 74 and 101 at 1024 x 8192 x 4096), 128 x 128 from 160 (40
-//    against 42 at 700 x 4096 x 4096), 64 x 128 from 64 of its own (32 against 38
-//    at 300 x 4096 x 4096), else 32 x 128 (14 against 17 at 130 x 1469 x 1344);
+//    against 42 at 700 x 4096 x 4096), 64 x 128 from 128 of its own (32 against 38
+//    at 300 x 4096 x 4096), else 32 x 128 (77 against 85 at 256 x 2000 x 7072);
 //  * grouped, by the mean rows of a group: 32 x 128 up to 48 (24 against 26, and
-//    50 in the rows form, at 600 rows over 16 groups of 2048 x 2048), 64 x 128 up
-//    to 80, else 128 x 128 (42 against 47 at 1111 over 8 of 2048 x 4096; 256 x 256
-//    wastes the groups' ends: 343 against 314 at 8000 over 8 of 4096 x 4096).
+//    50 in the general form, at 600 rows over 16 groups of 2048 x 2048), 64 x 128 up
+//    to 80, each also where the next larger ones are few (72 and 80 against 96 at
+//    1284 rows over 2 of 448 x 7072), else 128 x 128 (42 against 47 at
+//    1111 over 8 of 2048 x 4096; 256 x 256 wastes the groups' ends: 343 against 314
+//    at 8000 over 8 of 4096 x 4096).
 template <int GROUP, bool GROUPED>
 int tile(const W4Args& a, int64_t rows, hipStream_t stream)
 {
@@ -188,31 +191,37 @@ int tile(const W4Args& a, int64_t rows, hipStream_t stream)
     typedef W4TileCfg<2, 1, 1, 4, 4> T64;
     typedef W4TileCfg<4, 1, 1, 4, 4> T128;
     if constexpr (GROUPED) {
-        if (rows <= 48) return launch_tile<T32, GROUP, true>(a, stream);
-        if (rows <= 80) return launch_tile<T64, GROUP, true>(a, stream);
+        const int used = a.g.E < a.g.T ? a.g.E : a.g.T;
+        auto tiles = [&](int bm) { return ((int64_t)(a.g.T / bm) + used) * ceil_div(a.N, 128); };   // at most
+        if (rows <= 48 || tiles(64) < 128) return launch_tile<T32, GROUP, true>(a, stream);
+        if (rows <= 80 || tiles(128) < 128) return launch_tile<T64, GROUP, true>(a, stream);
         return launch_tile<T128, GROUP, true>(a, stream);
     } else {
         auto tiles = [&](int bm, int bn) { return (int64_t)ceil_div(a.M, bm) * ceil_div(a.N, bn); };
         if (tiles(256, 256) >= 192) return launch_tile<W4TileCfg<4, 2, 2, 4, 4>, GROUP, false>(a, stream);
         if (tiles(128, 128) >= 400) return launch_tile<W4TileCfg<4, 1, 1, 8, 4>, GROUP, false>(a, stream);
         if (tiles(128, 128) >= 160) return launch_tile<T128, GROUP, false>(a, stream);
-        if (tiles(64, 128) >= 64) return launch_tile<T64, GROUP, false>(a, stream);
+        if (tiles(64, 128) >= 128) return launch_tile<T64, GROUP, false>(a, stream);
         return launch_tile<T32, GROUP, false>(a, stream);
     }
 }
 
-// Which form, by the rows of A (of a group, on average) and by what the operands'
-// sizes and alignment allow.  Timed side by side (us):
+// Which form, by the rows of A (of a group, on average), the blocks of 16 x 16
+// entries of C, and by what the operands' sizes and alignment allow.  Timed side
+// by side (us):
 //  * one weight, up to 64 rows: the band form, in passes of 16 rows of A, or of 32
 //    where 16 would make more than two sweeps of the chip (12 against 15 at 24 x
 //    11008 x 4096, but 7.3 against 8.4 at 24 x 4096 x 4096).  At 64 x 4096 x 4096 it
 //    takes 9.8, the general form 13, tiles 31.  Up to 32768 entries of A in one
 //    pass lie in LDS instead (4.8 against 5.7 at 9 x 2048 x 2048).  From 65 rows on,
-//    tiles.
+//    tiles, but for products of few blocks and long K: tiles then leave most of the chip idle
+//    through all of K (26 against 6.1 at 100 x 500 x 4096, 30 against 9.8 at 100 x
+//    2000 x 4096, 57 against 23 at 512 x 512 x 8192; the general form 29 against 68 at
+//    512 x 512 x 7072).  Below K = 2048 they are even.
 //  * grouped, the band form up to a mean of 16 rows, and of 32 where K is long (21
 //    against 33 at 200 rows over 8 groups of 2048 x 4096; 39 against 24 at 600 over
 //    16 of 2048 x 2048), in passes of 32 rows from a mean of 9 on (42 against 55 at
-//    150 over 16 of 4096 x 4096); then tiles.
+//    150 over 16 of 4096 x 4096); then tiles, but for few blocks.
 //  * what is left takes the general form, with 16 rows of A by 32 of Q (16 by 16
 //    for few rows of both; 32 by 64 for many rows of both where groups of 128
 //    leave the registers for it: 23 against 38 at 32 x 16384 x 5000, but 40 against
@@ -221,10 +230,13 @@ template <int GROUP, bool GROUPED>
 int product(const W4Args& a, hipStream_t stream)
 {
     const int64_t rows = GROUPED ? (a.g.T + a.g.E - 1) / a.g.E : a.M;
+    const int64_t passes = GROUPED ? a.g.T / 16 + (a.g.E < a.g.T ? a.g.E : a.g.T) : ceil_div(a.M, 16);
+    const int64_t blocks = passes * ceil_div(a.N, 16);
     const bool wide = w4_aligned(a.A, 16) && w4_aligned(a.Q, 16) && w4_aligned(a.S, 16) && w4_aligned(a.Z, 8);
+    const bool few = blocks <= 2048 && passes <= 64 && a.K >= 2048;
     if (wide && a.K % 512 == 0 && a.K > 0 && a.N >= 16) {
         if constexpr (GROUPED) {
-            if ((rows <= 16 || (rows <= 32 && a.K >= 4096)) && a.K <= 8192) {
+            if ((rows <= 16 || (rows <= 32 && a.K >= 4096) || few) && a.K <= 8192) {
                 if (a.K > 4096) return band<W4BandCfg<GROUP, 1, 2>, true>(a, stream);
                 if constexpr (GROUP > 32)
                     if (rows > 8) return band<W4BandCfg<GROUP, 2, 1>, true>(a, stream);
@@ -232,16 +244,16 @@ int product(const W4Args& a, hipStream_t stream)
             }
         } else {
             if (a.M <= 16 && a.M * a.K <= 32768) return band<W4BandCfg<GROUP, 1, 0>, false>(a, stream);
-            if (a.M <= 64 && a.K <= 8192) {
+            if ((a.M <= 64 || few) && a.K <= 8192) {
                 if (a.K > 4096) return band<W4BandCfg<GROUP, 1, 2>, false>(a, stream);
                 if constexpr (GROUP > 32)                 // (spills with groups of 32)
-                    if (a.M > 16 && ceil_div(a.M, 16) * ceil_div(a.N, 16) > 512)
-                        return band<W4BandCfg<GROUP, 2, 1>, false>(a, stream);
+                    if (a.M > 16 && blocks > 512) return band<W4BandCfg<GROUP, 2, 1>, false>(a, stream);
                 return band<W4BandCfg<GROUP, 1, 1>, false>(a, stream);
             }
         }
     }
-    if (rows > (GROUPED ? 16 : 64) && w4_aligned(a.A, 16) && a.K >= 64) return tile<GROUP, GROUPED>(a, rows, stream);
+    if (rows > (GROUPED ? 16 : 64) && !(few && blocks <= 1536) && w4_aligned(a.A, 16) && a.K >= 64)
+        return tile<GROUP, GROUPED>(a, rows, stream);
     constexpr int CB = GROUP == 32 ? 2 : 4;
     if constexpr (GROUP == 128)
         if (rows > 16 && a.N >= 8192) return launch_rows<W4RowsCfg<GROUP, 2, 4, 4, 2>, GROUPED>(a, stream);

@@ -405,14 +405,13 @@ int gemm_f16_grouped_tn(const void* A, const void* B, void* C, const int* offset
  * single row, y = W . x.  Up to 64 rows of A, products a * (q - z) are summed in
  * fp32 within a group, the groups' sums scaled and added in fp32, and each result
  * rounded once to fp16: the weights themselves are not rounded.  From 65 rows on
- * the matrix cores are the bound, and each weight is rounded once to fp16 first,
- * as w4_dequantize_f16 rounds it; sums are in fp32 all the same.  (Where K < 64
- * or A is not 16-byte aligned, the first way holds for any number of rows.)
- * Results repeat bit for bit from run to run.
+ * the matrix cores are the bound, and each weight may be rounded once to fp16
+ * first, as w4_dequantize_f16 rounds it (one past the fp16 range to an infinity);
+ * sums are in fp32 all the same.  Which way is taken depends on the sizes and the
+ * operands' alignment alone, and results repeat bit for bit from run to run.
  * gemm_w4_f16_grouped_nt: gemm_f16_grouped_nt with 4-bit weights, Q E x N x
- * K/8, S and Z E x N x G; offsets and rows as there.  Its weights are rounded
- * as above, or are not, from a mean of 17 rows a group (T > 16 E) on, as the form
- * that is taken has it; up to there they are not.
+ * K/8, S and Z E x N x G; offsets and rows as there.  Its weights may be rounded
+ * so from a mean of 17 rows a group (T > 16 E) on.
  * Entries of Z above 15 are outside the contract (no fault).  Up to 64 rows (32 a
  * group) the fastest form needs K % 512 == 0, K <= 8192, A, Q and S 16-byte and Z
  * 8-byte aligned; the tiles need A 16-byte aligned and run best with K % 256 == 0; a

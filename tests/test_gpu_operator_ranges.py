@@ -131,8 +131,8 @@ def test_weight_gradients_shallow_and_deep(sizes, f32):
 
 # ---- launches of the 4-bit products ---------------------------------------
 
-# 256 x 256, 128 x 256, 128 x 128, 64 x 128, 32 x 128; K by windows of 256 and not
-@pytest.mark.parametrize("M,N", [(2900, 4100), (1500, 4357), (700, 4000), (100, 4104), (100, 500)])
+# 256 x 256, 128 x 256, 128 x 128, 64 x 128, 32 x 128; the general form; K by windows of 256 and not
+@pytest.mark.parametrize("M,N", [(2900, 4100), (1500, 4357), (700, 4000), (100, 8204), (100, 4104), (100, 500)])
 @pytest.mark.parametrize("K", [512, 328])
 @pytest.mark.parametrize("group", [32, 64, 128])
 def test_w4_tiles(M, N, K, group):
@@ -143,11 +143,13 @@ def test_w4_tiles(M, N, K, group):
     _check(C, A, _weights(Q, S, Z, group).t().contiguous(), K, "tiles", rounded=True)
 
 
-@pytest.mark.parametrize("sizes", [(40, 0, 33, 31), (150, 1, 99, 0), (400, 0, 130, 257)])     # 32, 64 and 128 rows
+# the general form, then 32, 64 and 128 rows
+@pytest.mark.parametrize("sizes,N", [((40, 0, 33, 31), 333), ((40, 0, 33, 31), 2309), ((150, 1, 99, 0), 2309),
+                                     ((400, 0, 130, 257), 2309)])
 @pytest.mark.parametrize("K", [512, 328])
 @pytest.mark.parametrize("group", [32, 64, 128])
-def test_w4_grouped_tiles(sizes, K, group):
-    E, T, N, off = len(sizes), sum(sizes), 333, plain.offsets_of(sizes)
+def test_w4_grouped_tiles(sizes, N, K, group):
+    E, T, off = len(sizes), sum(sizes), plain.offsets_of(sizes)
     A, (Q, S, Z) = _half(9, T, K), _codes(10, (E, N), K, group, zeros=group != 64)
     _say("w4 grouped tiles", sizes, K, group)
     C = gf.gemm_w4_f16_grouped_nt(A, Q, S, Z, dev(off), group=group)
@@ -159,11 +161,13 @@ def test_w4_grouped_tiles(sizes, K, group):
             _check(C[r], A[r], W.t().contiguous(), K, "group %d" % e, rounded=True)
 
 
-@pytest.mark.parametrize("M", [9, 17, 33, 48, 64])
-@pytest.mark.parametrize("N,K", [(17, 512), (1000, 2048), (9000, 4096), (3000, 8192), (300, 1536), (9000, 2008)])
+@pytest.mark.parametrize("M,N,K", [(m, n, k) for m in (9, 17, 33, 48, 64) for n, k in (
+    (17, 512), (1000, 2048), (9000, 4096), (3000, 8192), (300, 1536), (9000, 2008))] +
+    [(65, 4096, 2048), (512, 1000, 4096), (300, 500, 8192), (1024, 500, 2048), (700, 16, 4096), (1024, 17, 8192),
+     (300, 900, 2008), (1000, 200, 7072)])
 @pytest.mark.parametrize("group", [32, 64, 128])
 def test_w4_passes_of_rows(M, N, K, group):
-    """Up to 64 rows: passes of 16 and 32 rows in the streaming form, and the general one."""
+    """Up to 64 rows, or few blocks of C: passes of 16 and 32 rows in the streaming form, and the general one."""
     A, (Q, S, Z) = _half(20, M, K), _codes(21, (N,), K, group, zeros=group != 32)
     _say("w4 passes", M, N, K, group)
     C = gf.gemm_w4_f16_nt(A, Q, S, Z, group=group)
@@ -171,8 +175,8 @@ def test_w4_passes_of_rows(M, N, K, group):
     _check(C, A, _weights(Q, S, Z, group).t().contiguous(), K, "passes")
 
 
-@pytest.mark.parametrize("sizes", [(10, 12, 0, 15), (40, 0, 33, 31), (1, 99, 0, 2)])
-@pytest.mark.parametrize("N,K", [(200, 4096), (700, 8192), (70, 512)])
+@pytest.mark.parametrize("sizes", [(10, 12, 0, 15), (40, 0, 33, 31), (1, 99, 0, 2), (200, 0, 300, 77)])
+@pytest.mark.parametrize("N,K", [(200, 4096), (700, 8192), (70, 512), (300, 4008)])
 @pytest.mark.parametrize("group", [32, 64, 128])
 def test_w4_grouped_passes_of_rows(sizes, N, K, group):
     E, T, off = len(sizes), sum(sizes), plain.offsets_of(sizes)
