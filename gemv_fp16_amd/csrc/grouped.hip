@@ -14,7 +14,8 @@ bool g_aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>
 // (W as a whole may pass 2^31: it is addressed group by group).
 int validate_groups(const void* offsets, int T, int E, int N, int K)
 {
-    if (T < 0 || E < 0 || N < 0 || K < 0) return GF_ERR_INVALID_ARG;
+    if (T < 0 || E < 0 || N < 0 || K < 0 || E > kMaxGroups) return GF_ERR_INVALID_ARG;
+    if (T > kMaxExtent || N > kMaxExtent || K > kMaxExtent) return GF_ERR_INVALID_ARG;
     if ((int64_t)T * K > kGroupMaxElems || (int64_t)N * K > kGroupMaxElems || (int64_t)T * N > kGroupMaxElems)
         return GF_ERR_INVALID_ARG;
     if (E > 0 && (!offsets || !g_aligned(offsets, 4))) return GF_ERR_INVALID_ARG;

@@ -18,6 +18,9 @@
 
 namespace gf {
 
+constexpr int kMaxExtent = 1 << 30;    // of each size: the kernels round sizes up in 32 bits
+constexpr int kMaxGroups = 1 << 16;    // each workgroup looks through the groups
+
 // The groups, and what every kernel that walks them shares.
 struct Groups {
     const int* offsets;   // E + 1 entries
@@ -169,7 +172,7 @@ hipError_t launch_grouped(Args a, int64_t grid, hipStream_t stream)
     if (e != hipSuccess) return e;
     a.slices = 1;
     a.raster = 0;
-    a.kt_per_slice = 1 << 24;                     // one slice: more K tiles than any contraction has
+    a.kt_per_slice = 1 << 26;                     // one slice: more K tiles than any contraction (2^30) has
     hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(Cfg::NT), Cfg::LDS_BYTES, stream, a);
     return hipGetLastError();
 }

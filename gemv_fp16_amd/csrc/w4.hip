@@ -15,7 +15,7 @@ int w4_status(hipError_t e) { return e == hipSuccess ? GF_OK : GF_ERR_HIP; }
 // Sizes and groups of an N x K weight.
 int validate_w4(int N, int K, int group)
 {
-    if (N < 0 || K < 0 || K % 8 != 0) return GF_ERR_INVALID_ARG;
+    if (N < 0 || K < 0 || K % 8 != 0 || N > kMaxExtent || K > kMaxExtent) return GF_ERR_INVALID_ARG;
     if (group != 32 && group != 64 && group != 128) return GF_ERR_INVALID_ARG;
     if ((int64_t)N * K > kW4MaxElems) return GF_ERR_INVALID_ARG;
     return GF_OK;
@@ -311,7 +311,7 @@ int gemm_w4_f16_nt(const void* A, const void* Q, const void* S, const void* Z, v
 {
     const int rc = validate_w4(N, K, group);
     if (rc) return rc;
-    if (M < 0 || (int64_t)M * K > kW4MaxElems || (int64_t)M * N > kW4MaxElems) return GF_ERR_INVALID_ARG;
+    if (M < 0 || M > kMaxExtent || (int64_t)M * K > kW4MaxElems || (int64_t)M * N > kW4MaxElems) return GF_ERR_INVALID_ARG;
     if (M == 0 || N == 0) return GF_OK;
     if (w4_bad(C, 2)) return GF_ERR_INVALID_ARG;
     hipStream_t s = (hipStream_t)stream;
@@ -337,7 +337,8 @@ int gemm_w4_f16_grouped_nt(const void* A, const void* Q, const void* S, const vo
 {
     const int rc = validate_w4(N, K, group);
     if (rc) return rc;
-    if (T < 0 || E < 0 || (int64_t)T * K > kW4MaxElems || (int64_t)T * N > kW4MaxElems) return GF_ERR_INVALID_ARG;
+    if (T < 0 || E < 0 || T > kMaxExtent || E > kMaxGroups) return GF_ERR_INVALID_ARG;
+    if ((int64_t)T * K > kW4MaxElems || (int64_t)T * N > kW4MaxElems) return GF_ERR_INVALID_ARG;
     if (E > 0 && w4_bad(offsets, 4)) return GF_ERR_INVALID_ARG;
     if (T == 0 || E == 0 || N == 0) return GF_OK;
     if (w4_bad(C, 2)) return GF_ERR_INVALID_ARG;

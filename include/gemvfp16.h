@@ -352,7 +352,8 @@ int gf_sp_default_config(int M, int N, int K, gf_sp_cfg* out);
  * left as they were.  Offsets that break the contract give unspecified values
  * in C, but no access outside the operands.
  * Every group's part of an operand, and each of A and C as a whole, must be
- * smaller than 2^31 elements; B as a whole may be larger.  fp32 accumulation,
+ * smaller than 2^31 elements; B as a whole may be larger.  At most 65536 groups,
+ * and no size above 2^30.  fp32 accumulation,
  * one rounding at the end.  A group's results do not depend on the other groups'
  * rows or sizes except through the form the library picks from T / E: the tiles
  * add the same products in the same order, the streaming form (up to 12 rows a
@@ -416,7 +417,7 @@ int gemm_f16_grouped_tn(const void* A, const void* B, void* C, const int* offset
  * group) the fastest form needs K % 512 == 0, K <= 8192, A, Q and S 16-byte and Z
  * 8-byte aligned; the tiles need A 16-byte aligned and run best with K % 256 == 0; a
  * general form takes the rest.  M == 0 or N == 0 is a no-op; K == 0 writes +0.  Each operand (a group's part of Q) must stand for
- * fewer than 2^31 elements.  GF_ERR_INVALID_ARG for K % 8 != 0, another group
+ * fewer than 2^31 elements, and no size of a product may pass 2^30.  GF_ERR_INVALID_ARG for K % 8 != 0, another group
  * size, negative sizes, NULL or misaligned pointers, or sizes past the limit.
  */
 int w4_quantize_f16(const void* W, void* Q, void* S, void* Z, int N, int K, int group, void* stream);

@@ -272,3 +272,20 @@ def test_rows_of_nearly_2_to_the_31_elements(T, N, K):
     C = gf.gemm_w4_f16_grouped_nt(A, torch.stack([Q, Q]), torch.stack([S, S]), torch.stack([Z, Z]), off, group=32)
     torch.cuda.synchronize()
     _check(C[rows][:, n], A[rows], _weights(Q[n], S[n], Z[n], 32).t().contiguous(), K, "w4 grouped", rounded=True)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+def test_weight_gradient_of_nearly_2_to_the_31_elements(f32):
+    """A's row offsets pass 2^32 bytes within a group; 128 x 128 tiles in 32-row steps, then 256 x 256."""
+    T, M, N = 8000, 250000, 64
+    A, B = _half(24, T, M), _half(25, T, N)
+    n = _columns(M)
+    for ends in ((0, 1, T), tuple(range(0, 8001, 250))):
+        off = dev(np.array(ends, dtype=np.int32))
+        _say("large gradient", len(ends) - 1, f32)
+        C = gf.gemm_f16_grouped_tn(A, B, off, out_f32=f32)
+        torch.cuda.synchronize()
+        for e in (0, 1, len(ends) - 2):
+            r = slice(ends[e], ends[e + 1])
+            _check(C[e][n], A[r][:, n].t().contiguous(), B[r], ends[e + 1] - ends[e], "group %d" % e,
+                   plain.F32 if f32 else plain.F16)

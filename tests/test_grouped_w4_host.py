@@ -101,6 +101,24 @@ def test_w4_refusals(L):
     assert f(P, P, P, P, P, NULL, 4, 0, 8, 64, 32, NULL) == OK
 
 
+def test_sizes_past_the_limits(L):
+    """What the kernels round up in 32 bits, and how many groups they look through."""
+    big = 2 ** 30 + 8
+    for f in (L.gemm_f16_grouped_nt, L.gemm_f16_grouped_nn):
+        assert f(P, P, P, P, big, 1, 1, 1, NULL) == BAD
+        assert f(P, P, P, P, 1, 1, big, 1, NULL) == BAD
+        assert f(P, P, P, P, 1, 1, 1, big, NULL) == BAD
+        assert f(P, P, P, P, 1, 65537, 1, 1, NULL) == BAD
+    assert L.gemm_f16_grouped_tn(P, P, P, P, big, 1, 1, 1, 0, NULL) == BAD
+    assert L.gemm_f16_grouped_tn(P, P, P, P, 1, 65537, 1, 1, 0, NULL) == BAD
+    assert L.gemm_w4_f16_nt(P, P, P, P, P, 1, 1, big, 32, NULL) == BAD
+    assert L.gemm_w4_f16_nt(P, P, P, P, P, 1, big, 0, 32, NULL) == BAD
+    assert L.gemm_w4_f16_nt(P, P, P, P, P, big, 1, 0, 32, NULL) == BAD
+    assert L.gemm_w4_f16_grouped_nt(P, P, P, P, P, P, 1, 65537, 1, 8, 32, NULL) == BAD
+    assert L.gemm_w4_f16_grouped_nt(P, P, P, P, P, P, big, 1, 1, 0, 32, NULL) == BAD
+    assert L.w4_quantize_f16(P, P, P, P, 1, big, 32, NULL) == BAD
+
+
 def test_binding_refusals():
     """The binding's own checks come before the library is called."""
     torch = pytest.importorskip("torch")
