@@ -91,8 +91,10 @@ int run_band(const GroupRowArgs& a, hipStream_t stream)
 //    57 for every tile at T = 48, E = 16, 4096 x 2048; 41 against 59 at T = 16,
 //    E = 8, 4096 x 4096; 16 against 20 at T = 18, E = 17, 488 x 2672.  At a mean
 //    of 19 the 64 x 64 tile is ahead of it (34 against 39);
-//  * then 64 x 64 up to a mean of 64 (64 against 68 at T = 500, E = 16), 128 x 128
-//    with three stages beyond (45 against 56 at T = 1111, E = 8, 2048 x 4096);
+//  * then 64 x 64 up to a mean of 64 (64 against 68 at T = 500, E = 16) and where
+//    there are few of 128 x 128 (46 against 74 at T = 1284, E = 2, 448 x 7072; 18
+//    against 23 at T = 400, E = 4, 2048 x 2048), 128 x 128 with three stages beyond
+//    (45 against 56 at T = 1111, E = 8, 2048 x 4096);
 //  * 256 x 256 where the groups fill several of them, they fill the CUs and K is
 //    long enough to fill their pipeline (278 against 330 at T = 8191, E = 8, 4096 x
 //    4096; 98 against 121 for K x N B at T = 4096, 2048 x 4096; but 50 against 46
@@ -120,7 +122,8 @@ int rows_dispatch(const GroupRowArgs& a, bool al, hipStream_t stream)
     if (mean >= 192 && a.K > 1024 && ((int64_t)a.g.T / 256) * ceil_div(a.N, 256) >= 128)
         return run_rounds<LB>(a, al, stream);
     if constexpr (LB == 0)
-        if (mean < 64) return run_rows<GemmCfg<64, 64, 64, 3, 256, 0, 0, 0>>(a, al, stream);
+        if (mean < 64 || most_tiles<GemmCfg<128, 128, 64, 3, 256, 2, 0, 0>>(a) < 128)
+            return run_rows<GemmCfg<64, 64, 64, 3, 256, 0, 0, 0>>(a, al, stream);
     if constexpr (LB == 1)
         if (mean < (a.K > 1024 ? 16 : 64))
             return run_rows<GemmCfg<64, 128, 64, 2, 256, 2, 0, LB>>(a, al, stream);

@@ -129,6 +129,21 @@ def test_weight_gradients_shallow_and_deep(sizes, f32):
         _check(C[e], A[r].t().contiguous(), B[r], sizes[e], "group %d" % e, plain.F32 if f32 else plain.F16)
 
 
+@pytest.mark.parametrize("sizes,N,K", [((700, 584), 448, 1032), ((90, 0, 200, 110), 300, 2048), ((400, 0, 3, 700), 2309, 200)])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_groups_of_many_rows_and_few_tiles(sizes, N, K, shift):
+    """64 x 64 tiles where 128 x 128 ones are few, and a case with enough of those."""
+    T, E, off = sum(sizes), len(sizes), plain.offsets_of(sizes)
+    A, B = _half(26, T, K), _half(27, E, N, K, scale=0.03)
+    _say("few tiles", sizes, N, K, shift)
+    C = gf.gemm_f16_grouped_nt(_shifted(A, shift), B, dev(off))
+    torch.cuda.synchronize()
+    for e in range(E):
+        r = slice(int(off[e]), int(off[e + 1]))
+        if sizes[e]:
+            _check(C[r], A[r], B[e].t().contiguous(), K, "group %d" % e)
+
+
 # ---- launches of the 4-bit products ---------------------------------------
 
 # 256 x 256, 128 x 256, 128 x 128, 64 x 128, 32 x 128; the general form; K by windows of 256 and not
