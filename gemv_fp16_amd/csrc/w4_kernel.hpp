@@ -1011,20 +1011,20 @@ __global__ __launch_bounds__(Cfg::NT) void w4_tile_kernel(W4Args a)
             }
         }
     };
-    // In the last step: whether any of this lane's 32 k lie inside K, and how many
-    // words its codes, loaded from inside the row, are ahead of their place.
+    // In the last step: how many words of this lane's 32 k lie inside K, and how
+    // many words its codes, loaded from inside the row, are ahead of their place.
     const int last_k = (nk - 1) * BK + 32 * h;
-    const bool last_some = WINDOW || last_k < K;
+    const int last_words = WINDOW ? 4 : max(K - last_k, 0) / 8;
     const int last_ahead = max(last_k - (K - 32), 0) / 8;
     half2v off[FN], sc[FN];
-    // Scale and offset of step t, which is step i of the D unrolled.
-    auto scale = [&](int t, auto i_c) __attribute__((always_inline)) {
+    // Scale and offset of step i of the D unrolled.
+    auto scale = [&](auto i_c) __attribute__((always_inline)) {
         constexpr int i = decltype(i_c)::value;
 #pragma unroll
         for (int f = 0; f < FN; ++f) {
             uint32_t sb, z;
             if constexpr (!WINDOW) {
-                sb = t < nk - 1 || last_some ? sw[i][f][0] : 0u;
+                sb = sw[i][f][0];
                 z = zw[i][f][0];
             } else if constexpr (GROUP == 32) {
                 sb = sw[0][f][i % SW] >> (16 * h);
@@ -1037,6 +1037,16 @@ __global__ __launch_bounds__(Cfg::NT) void w4_tile_kernel(W4Args a)
             sc[f] = w4_twice(sb);
             off[f] = w4_offsets(a.Z ? z : 8u);
         }
+    };
+
+    // The operand of column block f for 16 k j of step t, which is step i of the D
+    // unrolled.  A word past K stands for zeros: its codes are 0, but 0 - z times a
+    // large scale would pass the fp16 range, and infinity times the cleared A is NaN.
+    auto operand = [&](int t, auto i_c, auto f_c, auto j_c) __attribute__((always_inline)) {
+        constexpr int i = decltype(i_c)::value, f = decltype(f_c)::value, j = decltype(j_c)::value;
+        half2v s = sc[f];
+        if constexpr (!WINDOW) s = t < nk - 1 || j < last_words ? s : w4_twice(0u);
+        return w4_weights(codes[i][f][j], off[f], s);
     };
 
     // ---- fragments of A ----
@@ -1078,8 +1088,9 @@ __global__ __launch_bounds__(Cfg::NT) void w4_tile_kernel(W4Args a)
     lds_barrier();                                        // step 0 has landed
     issue_a(S - 1, S - 1);
     read_x(0, std::integral_constant<int, 0>{});
-    scale(0, std::integral_constant<int, 0>{});
-    b = w4_weights(codes[0][0][0], off[0], sc[0]);
+    scale(std::integral_constant<int, 0>{});
+    constexpr std::integral_constant<int, 0> zero_c;
+    b = operand(0, zero_c, zero_c, zero_c);
 
     int st = 0;                                           // buffer of step t
     auto step = [&](int t, auto p) __attribute__((always_inline)) {
@@ -1104,7 +1115,7 @@ __global__ __launch_bounds__(Cfg::NT) void w4_tile_kernel(W4Args a)
                             u32x4 q = codes[i1][f];
                             if (last_ahead & 1) q = u32x4{q[1], q[2], q[3], 0u};
                             if (last_ahead & 2) q = u32x4{q[2], q[3], 0u, 0u};
-                            codes[i1][f] = q;             // (a lane wholly past K has a scale of 0)
+                            codes[i1][f] = q;
                         }
                         lds_barrier();
                     }
@@ -1120,12 +1131,12 @@ __global__ __launch_bounds__(Cfg::NT) void w4_tile_kernel(W4Args a)
                 // the next operand: the next column block's, or the next 16 k's first
                 half8 next;
                 if constexpr (f + 1 < FN) {
-                    next = w4_weights(codes[i][f + 1][j], off[f + 1], sc[f + 1]);
+                    next = operand(t, p, std::integral_constant<int, f + 1>{}, j_c);
                 } else if constexpr (j < 3) {
-                    next = w4_weights(codes[i][0][j + 1], off[0], sc[0]);
+                    next = operand(t, p, zero_c, std::integral_constant<int, j + 1>{});
                 } else {
-                    scale(t + 1, std::integral_constant<int, i1>{});
-                    next = w4_weights(codes[i1][0][0], off[0], sc[0]);
+                    scale(std::integral_constant<int, i1>{});
+                    next = operand(t + 1, std::integral_constant<int, i1>{}, zero_c, zero_c);
                 }
                 mfmas(f_c, j_c, b);
                 b = next;
@@ -1139,7 +1150,7 @@ __global__ __launch_bounds__(Cfg::NT) void w4_tile_kernel(W4Args a)
                 load_codes(t + 3, std::integral_constant<int, i - 1>{});
                 load_codes(t + 4, p);
             }
-            if constexpr (i == 2) load_scales(t + 2, p);  // the window's last use was scale(t + 1)
+            if constexpr (i == 2) load_scales(t + 2, p);  // the window's last use was the next step's scale()
         }
         st = st1;
     };
