@@ -100,6 +100,22 @@ __device__ __forceinline__ float w4_quotient(float a, float b, float r)
     return fmaf(fmaf(-q, b, a), r, q);
 }
 
+// q = (hi - lo) / 15 in fp32, on the side of a tie between two fp16 scales where
+// the exact quotient is.  hi - lo can need more than 24 bits; fp32 loses up to half
+// a unit of its last place.  A tie t times 15 is a whole number of these units, so
+// unless the rounded difference is 15 t itself, it is a unit away from it at least:
+// then exact and rounded difference lie on the same side of 15 t, and the fp32
+// quotient, which a 15th of a unit is enough to move, on that side of t.  If it is
+// 15 t, q is t, and what the difference lost decides: q moves one fp32 step that
+// way.  (Ties have 12 significant bits.  The other numbers that end in 12 zeros are
+// fp16 numbers, and round to themselves from a step beside.)
+__device__ __forceinline__ float w4_beside_tie(float q, float lost)
+{
+    const uint32_t b = __builtin_bit_cast(uint32_t, q);
+    const uint32_t beside = lost > 0.0f ? b + 1u : b - 1u;
+    return __builtin_bit_cast(float, lost != 0.0f && (b & 0xfffu) == 0u ? beside : b);
+}
+
 // One thread holds 8 consecutive k (a word of codes), GROUP / 8 neighbouring
 // lanes one group.  Rows are padded to whole groups in the thread index, so a
 // group never straddles two rows; the lanes past K hold zeros, which change
@@ -166,7 +182,13 @@ __global__ __launch_bounds__(256) void w4_quantize_kernel(const uint16_t* __rest
         const float hi = f16_bits_to_f32((uint16_t)both), lo = -f16_bits_to_f32((uint16_t)(both >> 16));
         // (a zero scale is +0, whatever the signs of the zeros it came from)
         const float span = ASYM ? hi - lo : __builtin_fmaxf(hi, -lo);
-        const uint16_t sb = f32_to_f16_bits(w4_quotient(span, ASYM ? 15.0f : 7.0f, ASYM ? 1.0f / 15.0f : 1.0f / 7.0f));
+        float quot = w4_quotient(span, ASYM ? 15.0f : 7.0f, ASYM ? 1.0f / 15.0f : 1.0f / 7.0f);
+        if constexpr (ASYM) {
+            const float big = __builtin_fmaxf(hi, -lo), small = __builtin_fminf(hi, -lo);
+            const float lost = small - (span - big);      // hi - lo is span + lost, exactly
+            if (__ballot(lost != 0.0f)) quot = w4_beside_tie(quot, lost);   // rare
+        }
+        const uint16_t sb = f32_to_f16_bits(quot);
         const float s = f16_bits_to_f32(sb);
         const bool flat = s == 0.0f || bad;               // all codes are z
         const float r0 = __builtin_amdgcn_rcpf(flat ? 1.0f : s), r = fmaf(fmaf(-s, r0, 1.0f), r0, r0);

@@ -395,7 +395,8 @@ int gemm_f16_grouped_tn(const void* A, const void* B, void* C, const int* offset
  * w4_quantize_f16: codes, scales and zero points of an fp16 W.  With Z, lo and
  * hi the group's least and largest value and 0: s = fp16((hi - lo) / 15),
  * z = min(15, rint(-lo / s)); without, s = fp16(max |w| / 7), z = 8.  Then
- * q = clamp(rint(w / s) + z, 0, 15), the quotient exact and ties to even.
+ * q = clamp(rint(w / s) + z, 0, 15).  Differences and quotients are exact and
+ * rounded once, ties to even.
  * s == 0 gives q = z (0 with Z).  A group that holds an infinity or a NaN gets
  * s = NaN, so that products with it show it.  Bit-exact, deterministic.
  * w4_dequantize_f16: W = fp16((q - z) * s), rounded once.
