@@ -21,10 +21,30 @@ namespace gf {
 constexpr int kMaxExtent = 1 << 30;    // of each size: the kernels round sizes up in 32 bits
 constexpr int kMaxGroups = 1 << 16;    // each workgroup looks through the groups
 
+// A launch has fewer than 2^32 threads: one of 2^32 is refused, a larger one wraps.
+// So work runs as launches of at most this many workgroups (of 512 threads or
+// fewer), each told the number of its first.  A multiple of 8, so that the mapping
+// to the XCDs goes on where the launch before ended.
+constexpr int kMaxLaunch = 1 << 22;
+
+template <class Launch>
+hipError_t launch_in_parts(int64_t grid, Launch launch)
+{
+    for (int64_t first = 0; first < grid; first += kMaxLaunch) {
+        const int64_t n = grid - first < kMaxLaunch ? grid - first : kMaxLaunch;
+        const hipError_t e = launch((int)first, dim3((unsigned)n));
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
 // The groups, and what every kernel that walks them shares.
 struct Groups {
     const int* offsets;   // E + 1 entries
     int E, T;
+    int first;            // number of the launch's first workgroup
+
+    __device__ __forceinline__ int workgroup() const { return first + (int)blockIdx.x; }
 
     // Rows of group e.  Entries outside 0 .. T and a group whose end comes
     // before its begin (both against the contract) still name no row outside A
@@ -114,7 +134,7 @@ struct GroupRowShare : GemmArgs {
         constexpr int F = SHARE == 2 ? 2 : 1;             // tiles are F * BM x F * BN
         const int tiles_n = ceil_div(N, F * BN);
         int e, lo, hi, item;
-        if (!g.find<F * BM, SHARE>(blockIdx.x, tiles_n, e, lo, hi, item)) return false;
+        if (!g.find<F * BM, SHARE>(g.workgroup(), tiles_n, e, lo, hi, item)) return false;
         M = hi - lo;
         A += (size_t)lo * K;
         B += (size_t)e * N * K;
@@ -148,8 +168,9 @@ struct GroupDepthArgs : GemmArgs {
     __device__ __forceinline__ bool locate(int& tm, int& tn)
     {
         const int run = run_length<BM, BN>(M, N);
-        const int i = blockIdx.x / 8, e = i / run;
-        const int t = (blockIdx.x % 8) * run + i % run;
+        const unsigned w = g.workgroup();
+        const int i = w / 8, e = i / run;
+        const int t = (w % 8) * run + i % run;
         const int tiles_m = ceil_div(M, BM), tiles_n = ceil_div(N, BN);
         if (t >= tiles_m * tiles_n) return false;
         int lo, hi;
@@ -173,8 +194,11 @@ hipError_t launch_grouped(Args a, int64_t grid, hipStream_t stream)
     a.slices = 1;
     a.raster = 0;
     a.kt_per_slice = 1 << 26;                     // one slice: more K tiles than any contraction (2^30) has
-    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(Cfg::NT), Cfg::LDS_BYTES, stream, a);
-    return hipGetLastError();
+    return launch_in_parts(grid, [&](int first, dim3 n) {
+        a.g.first = first;
+        hipLaunchKernelGGL(kern, n, dim3(Cfg::NT), Cfg::LDS_BYTES, stream, a);
+        return hipGetLastError();
+    });
 }
 
 // ---------------------------------------------------------------------------
@@ -214,7 +238,7 @@ __global__ __launch_bounds__(Cfg::WAVES * 64) void group_band_kernel(GroupRowArg
     const int r16 = lane % 16, c4 = lane / 16;
     const int N = a.N, K = a.K;
     int e, lo, hi, item;
-    if (!a.g.template find<MR>(blockIdx.x, parts, e, lo, hi, item)) return;
+    if (!a.g.template find<MR>(a.g.workgroup(), parts, e, lo, hi, item)) return;
     const int passes = ceil_div(hi - lo, MR), part = item / passes;
     const int begin = lo + item % passes * MR, M = min(hi - begin, MR);
     const uint16_t* A = a.A + (size_t)begin * K;
@@ -317,7 +341,7 @@ __global__ __launch_bounds__(Cfg::WAVES * 64) void group_band_kernel(GroupRowArg
 }
 
 template <class Cfg>
-hipError_t launch_group_band(const GroupRowArgs& a, int ring, int parts, int64_t grid, hipStream_t stream)
+hipError_t launch_group_band(GroupRowArgs a, int ring, int parts, int64_t grid, hipStream_t stream)
 {
     auto kern = group_band_kernel<Cfg>;
     static std::atomic<uint64_t> lds_opt_in{0};
@@ -325,8 +349,11 @@ hipError_t launch_group_band(const GroupRowArgs& a, int ring, int parts, int64_t
     static_assert(Cfg::lds_bytes(Cfg::MAX_RING) <= 160 * 1024, "one CU's LDS");
     const hipError_t e = opt_in_lds((const void*)kern, Cfg::lds_bytes(Cfg::MAX_RING), lds_opt_in, stream);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(Cfg::WAVES * kWave), lds, stream, a, ring, parts);
-    return hipGetLastError();
+    return launch_in_parts(grid, [&](int first, dim3 n) {
+        a.g.first = first;
+        hipLaunchKernelGGL(kern, n, dim3(Cfg::WAVES * kWave), lds, stream, a, ring, parts);
+        return hipGetLastError();
+    });
 }
 
 }  // namespace gf

@@ -86,7 +86,7 @@ __global__ void w4_zero_kernel(uint16_t* __restrict__ p, int64_t n)
 }
 
 template <class Cfg, int GROUP, bool WINDOW, bool GROUPED>
-int launch_tile_of(const W4Args& a, hipStream_t stream)
+int launch_tile_of(W4Args a, hipStream_t stream)
 {
     auto kern = w4_tile_kernel<Cfg, GROUP, WINDOW, GROUPED>;
     static std::atomic<uint64_t> lds_opt_in{0};
@@ -96,8 +96,11 @@ int launch_tile_of(const W4Args& a, hipStream_t stream)
     if (GROUPED) blocks = a.g.T / Cfg::BM + (a.g.E < a.g.T ? a.g.E : a.g.T);
     const int64_t grid = blocks * ceil_div(a.N, Cfg::BN);
     if (grid > kW4MaxGrid) return GF_ERR_INVALID_ARG;
-    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(Cfg::NT), Cfg::LDS_BYTES, stream, a);
-    return w4_status(hipGetLastError());
+    return w4_status(launch_in_parts(grid, [&](int first, dim3 n) {
+        a.g.first = first;
+        hipLaunchKernelGGL(kern, n, dim3(Cfg::NT), Cfg::LDS_BYTES, stream, a);
+        return hipGetLastError();
+    }));
 }
 
 template <class Cfg, int GROUP, bool GROUPED>
@@ -109,7 +112,7 @@ int launch_tile(const W4Args& a, hipStream_t stream)
 }
 
 template <class Cfg, bool GROUPED>
-int launch_rows(const W4Args& a, hipStream_t stream)
+int launch_rows(W4Args a, hipStream_t stream)
 {
     auto kern = w4_rows_kernel<Cfg, GROUPED>;
     static_assert(Cfg::LDS_BYTES <= 64 * 1024, "no opt-in for large LDS");
@@ -117,14 +120,17 @@ int launch_rows(const W4Args& a, hipStream_t stream)
     if (GROUPED) blocks = a.g.T / (16 * Cfg::MB) + (a.g.E < a.g.T ? a.g.E : a.g.T);
     const int64_t grid = blocks * ceil_div(a.N, 16 * Cfg::NB);
     if (grid > kW4MaxGrid) return GF_ERR_INVALID_ARG;
-    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(Cfg::WAVES * 64), Cfg::LDS_BYTES, stream, a);
-    return w4_status(hipGetLastError());
+    return w4_status(launch_in_parts(grid, [&](int first, dim3 n) {
+        a.g.first = first;
+        hipLaunchKernelGGL(kern, n, dim3(Cfg::WAVES * 64), Cfg::LDS_BYTES, stream, a);
+        return hipGetLastError();
+    }));
 }
 
 // parts: workgroups that share the row groups of one weight (and 16 MB rows of A),
 // at most one each.
 template <class Cfg, bool GROUPED>
-int launch_band(const W4Args& a, int ring, int parts, hipStream_t stream)
+int launch_band(W4Args a, int ring, int parts, hipStream_t stream)
 {
     auto kern = w4_band_kernel<Cfg, GROUPED>;
     static std::atomic<uint64_t> lds_opt_in{0};
@@ -138,8 +144,11 @@ int launch_band(const W4Args& a, int ring, int parts, hipStream_t stream)
     int64_t grid = Cfg::XLDS ? parts : (int64_t)ceil_div(parts, 8) * 8 * ceil_div(a.M, 16 * Cfg::MB);
     if (GROUPED) grid = (int64_t)parts * (a.g.T / (16 * Cfg::MB) + (a.g.E < a.g.T ? a.g.E : a.g.T));
     if (grid > kW4MaxGrid) return GF_ERR_INVALID_ARG;
-    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(Cfg::WAVES * 64), lds, stream, a, ring, parts);
-    return w4_status(hipGetLastError());
+    return w4_status(launch_in_parts(grid, [&](int first, dim3 n) {
+        a.g.first = first;
+        hipLaunchKernelGGL(kern, n, dim3(Cfg::WAVES * 64), lds, stream, a, ring, parts);
+        return hipGetLastError();
+    }));
 }
 
 // The band form's launch.  One weight: two workgroups to a CU, with as much in
@@ -322,7 +331,7 @@ int gemm_w4_f16_nt(const void* A, const void* Q, const void* S, const void* Z, v
     }
     if (w4_bad(A, 2) || w4_bad(Q, 4) || w4_bad(S, 2)) return GF_ERR_INVALID_ARG;
     W4Args a = {(const uint16_t*)A, (const uint32_t*)Q, (const uint16_t*)S, (const uint8_t*)Z, (uint16_t*)C,
-                M, N, K, ceil_div(K, group), {nullptr, 0, 0}};
+                M, N, K, ceil_div(K, group), {nullptr, 0, 0, 0}};
     return product_by_group<false>(a, group, s);
 }
 
@@ -345,7 +354,7 @@ int gemm_w4_f16_grouped_nt(const void* A, const void* Q, const void* S, const vo
     // K == 0: the kernel never reads A, Q or S, and stores the empty sums of the groups' rows
     if (K > 0 && (w4_bad(A, 2) || w4_bad(Q, 4) || w4_bad(S, 2))) return GF_ERR_INVALID_ARG;
     W4Args a = {(const uint16_t*)A, (const uint32_t*)Q, (const uint16_t*)S, (const uint8_t*)Z, (uint16_t*)C,
-                0, N, K, ceil_div(K, group), {offsets, E, T}};
+                0, N, K, ceil_div(K, group), {offsets, E, T, 0}};
     return product_by_group<true>(a, group, (hipStream_t)stream);
 }
 

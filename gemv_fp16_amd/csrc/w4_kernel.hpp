@@ -297,7 +297,7 @@ struct W4Args {
     const uint8_t* Z;     // N x G or null
     uint16_t* C;          // M x N
     int M, N, K, G;
-    Groups g;             // grouped form: the rows of A and C by group; M unused
+    Groups g;             // grouped form: the rows of A and C by group, M unused; else only `first`
 };
 
 // The eight q - z of a word, in order, as fp16 subnormals (times 2^-24).  A byte
@@ -406,7 +406,7 @@ __global__ __launch_bounds__(Cfg::WAVES * 64) void w4_rows_kernel(W4Args a)
     int tm, tn, M = a.M;
     if constexpr (GROUPED) {
         int e, lo, hi, item;
-        if (!a.g.template find<16 * MB>(blockIdx.x, tiles_n, e, lo, hi, item)) return;
+        if (!a.g.template find<16 * MB>(a.g.workgroup(), tiles_n, e, lo, hi, item)) return;
         M = hi - lo;
         a.A += (size_t)lo * a.K;
         a.C += (size_t)lo * a.N;
@@ -416,8 +416,9 @@ __global__ __launch_bounds__(Cfg::WAVES * 64) void w4_rows_kernel(W4Args a)
         tm = item % ceil_div(M, 16 * MB);
         tn = item / ceil_div(M, 16 * MB);
     } else {
-        tm = blockIdx.x / tiles_n;
-        tn = blockIdx.x % tiles_n;
+        const unsigned w = a.g.workgroup();
+        tm = w / tiles_n;
+        tn = w % tiles_n;
     }
     const int m0 = tm * 16 * MB, n0 = tn * 16 * NB;
     const int K = a.K, nblk = K / Cfg::BK, rest = ceil_div(K - nblk * Cfg::BK, 128);
@@ -636,10 +637,10 @@ __global__ __launch_bounds__(Cfg::WAVES * 64) void w4_band_kernel(W4Args a, int 
     const int r16 = lane % 16, c4 = lane / 16;
     const int N = a.N, K = a.K, G = a.G;
 
-    int part = blockIdx.x, M = a.M;
+    int part = a.g.workgroup(), M = a.M;
     if constexpr (GROUPED) {
         int e, lo, hi, item;
-        if (!a.g.template find<16 * MB>(blockIdx.x, parts, e, lo, hi, item)) return;
+        if (!a.g.template find<16 * MB>(part, parts, e, lo, hi, item)) return;
         const int passes = ceil_div(hi - lo, 16 * MB);
         part = item / passes;
         const int first = lo + item % passes * 16 * MB;
@@ -953,7 +954,7 @@ __global__ __launch_bounds__(Cfg::NT) void w4_tile_kernel(W4Args a)
     int tm, tn, M = a.M;
     if constexpr (GROUPED) {
         int e, lo, hi, item;
-        if (!a.g.template find<Cfg::BM>(blockIdx.x, tiles_n, e, lo, hi, item)) return;
+        if (!a.g.template find<Cfg::BM>(a.g.workgroup(), tiles_n, e, lo, hi, item)) return;
         M = hi - lo;
         a.A += (size_t)lo * a.K;
         a.C += (size_t)lo * a.N;
@@ -963,7 +964,7 @@ __global__ __launch_bounds__(Cfg::NT) void w4_tile_kernel(W4Args a)
         grouped_tile(item, ceil_div(M, Cfg::BM), tiles_n, kGroupPanel, tm, tn);
     } else {
         const int tiles_m = ceil_div(M, Cfg::BM);
-        grouped_tile(xcd_remap(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, kGroupPanel, tm, tn);
+        grouped_tile(xcd_remap(a.g.workgroup(), tiles_m * tiles_n), tiles_m, tiles_n, kGroupPanel, tm, tn);
     }
     const int m0 = tm * Cfg::BM, n0 = tn * Cfg::BN;
     const int K = a.K, nk = ceil_div(K, BK);
