@@ -584,6 +584,13 @@ def _launch(name, tensors, stream, *args):
         _check(rc, name)
 
 
+def _ints(bits):
+    """Refuse sizes that the library's ints cannot hold (ctypes would cut them to
+    32 bits).  bits: all of them, or-ed together."""
+    if bits >> 31:
+        raise ValueError("every size must be below 2^31")
+
+
 def _out(t, like, shape, dtype, stream, name):
     """The caller's output, checked, or a new one on `like`'s device."""
     if t is None:
@@ -610,6 +617,7 @@ def gemm_f16_grouped_nt(A, B, offsets, C=None, stream=None):
     if A.dim() != 2 or B.dim() != 3 or A.shape[1] != B.shape[2]:
         raise ValueError("A must be (T, K) and B (E, N, K)")
     (T, K), (E, N, _) = A.shape, B.shape
+    _ints(T | E | N | K)
     f16 = torch.float16
     C = _out(C, A, (T, N), f16, stream, "C")
     _launch("gemm_f16_grouped_nt", (A, B, offsets, C), stream, _ptr(A, f16, "A"), _ptr(B, f16, "B"),
@@ -625,6 +633,7 @@ def gemm_f16_grouped_nn(A, B, offsets, C=None, stream=None):
     if A.dim() != 2 or B.dim() != 3 or A.shape[1] != B.shape[1]:
         raise ValueError("A must be (T, K) and B (E, K, N)")
     (T, K), (E, _, N) = A.shape, B.shape
+    _ints(T | E | N | K)
     f16 = torch.float16
     C = _out(C, A, (T, N), f16, stream, "C")
     _launch("gemm_f16_grouped_nn", (A, B, offsets, C), stream, _ptr(A, f16, "A"), _ptr(B, f16, "B"),
@@ -643,6 +652,7 @@ def gemm_f16_grouped_tn(A, B, offsets, C=None, out_f32=None, stream=None):
     if offsets.dim() != 1 or offsets.shape[0] < 1:
         raise ValueError("offsets must hold one entry more than there are groups")
     (T, M), N, E = A.shape, B.shape[1], offsets.shape[0] - 1
+    _ints(T | E | M | N)
     if out_f32 is None:
         out_f32 = C is not None and C.dtype == torch.float32
     f16, dt = torch.float16, torch.float32 if out_f32 else torch.float16
@@ -693,6 +703,8 @@ def w4_quantize_f16(W, group: int = 128, symmetric: bool = False, Q=None, S=None
     if symmetric and Z is not None:
         raise ValueError("symmetric codes have no Z")
     lead, K = W.shape[:-1], W.shape[-1]
+    N = _rows(lead)
+    _ints(N | K)
     w = _ptr(W, torch.float16, "W")
     per_group = lead + ((K + group - 1) // group,)
     Q = _out(Q, W, lead + (K // 8,), torch.int32, stream, "Q")
@@ -700,7 +712,7 @@ def w4_quantize_f16(W, group: int = 128, symmetric: bool = False, Q=None, S=None
     if not symmetric:
         Z = _out(Z, W, per_group, torch.uint8, stream, "Z")
     _launch("w4_quantize_f16", (W, Q, S) if Z is None else (W, Q, S, Z), stream, w, *_w4_ptrs(Q, S, Z),
-            _rows(lead), K, group)
+            N, K, group)
     return Q, S, Z
 
 
@@ -710,10 +722,12 @@ def w4_dequantize_f16(Q, S, Z=None, group: int = 128, W=None, stream=None):
     if Q.dim() not in (2, 3):
         raise ValueError("Q must be (N, K/8) or (E, N, K/8)")
     lead, K = _w4_check(Q, S, Z, group, Q.dim())
+    N = _rows(lead)
+    _ints(N | K)
     ptrs = _w4_ptrs(Q, S, Z)
     W = _out(W, Q, lead + (K,), torch.float16, stream, "W")
     _launch("w4_dequantize_f16", (Q, S, W) if Z is None else (Q, S, W, Z), stream, *ptrs,
-            _ptr(W, torch.float16, "W"), _rows(lead), K, group)
+            _ptr(W, torch.float16, "W"), N, K, group)
     return W
 
 
@@ -725,6 +739,7 @@ def gemm_w4_f16_nt(A, Q, S, Z=None, C=None, group: int = 128, stream=None):
     if A.dim() != 2 or A.shape[1] != K:
         raise ValueError("A must be (M, %d)" % K)
     M, f16 = A.shape[0], torch.float16
+    _ints(M | N | K)
     C = _out(C, A, (M, N), f16, stream, "C")
     _launch("gemm_w4_f16_nt", (A, Q, S, C) if Z is None else (A, Q, S, C, Z), stream, _ptr(A, f16, "A"),
             *_w4_ptrs(Q, S, Z), _ptr(C, f16, "C"), M, N, K, group)
@@ -737,6 +752,7 @@ def gemv_w4_f16(Q, S, Z, x, y=None, group: int = 128, stream=None):
     (N,), K = _w4_check(Q, S, Z, group, 2)
     if x.dim() != 1 or x.shape[0] != K:
         raise ValueError("x must be (%d,)" % K)
+    _ints(N | K)
     f16 = torch.float16
     y = _out(y, x, (N,), f16, stream, "y")
     _launch("gemv_w4_f16", (x, Q, S, y) if Z is None else (x, Q, S, y, Z), stream, *_w4_ptrs(Q, S, Z),
@@ -751,6 +767,7 @@ def gemm_w4_f16_grouped_nt(A, Q, S, Z, offsets, C=None, group: int = 128, stream
     if A.dim() != 2 or A.shape[1] != K:
         raise ValueError("A must be (T, %d)" % K)
     T, f16 = A.shape[0], torch.float16
+    _ints(T | E | N | K)
     C = _out(C, A, (T, N), f16, stream, "C")
     _launch("gemm_w4_f16_grouped_nt", (A, Q, S, offsets, C) if Z is None else (A, Q, S, offsets, C, Z), stream,
             _ptr(A, f16, "A"), *_w4_ptrs(Q, S, Z), _ptr(C, f16, "C"), _offsets(offsets, E), T, E, N, K, group)
