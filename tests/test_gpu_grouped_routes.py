@@ -131,3 +131,60 @@ def test_no_rows_and_no_contraction():
         gf.gemm_w4_f16_grouped_nt(z(T, 0), z(2, 24, 0, dt=torch.int32), z(2, 24, 0), None, o, C, group=32)
         assert not C[1:4].view(torch.int16).any()
         assert (C[:1].view(torch.int16) == SENTINEL).all() and (C[4:].view(torch.int16) == SENTINEL).all()
+
+
+def _check_groups(C, A, B, off, groups, depth, what):
+    for e in groups:
+        r = slice(int(off[e]), int(off[e + 1]))
+        a, b = A[r].double(), B[e].double().contiguous()
+        plain.check(C[r].cpu().numpy(), (a @ b).cpu().numpy(), (a.abs() @ b.abs()).cpu().numpy(), depth, plain.F16,
+                    "%s group %d" % (what, e))
+
+
+def test_as_many_groups_as_may_be():
+    """65536 groups of no, one or two rows; sampled groups, the first and the last."""
+    E, N, K = 65536, 16, 32
+    rng = np.random.default_rng(7)
+    off = plain.offsets_of(rng.integers(0, 3, E), 1)
+    T = int(off[-1]) + 2
+    A, B, D, o = _half(8, T, K), _half(9, E, N, K), _half(10, T, N), dev(off)
+    groups = [0, 1, 63, 64, E - 65, E - 64, E - 2, E - 1] + [int(e) for e in rng.integers(0, E, 40)]
+    _say("65536 groups")
+    C = gf.gemm_f16_grouped_nt(A, B, o, _sentinel((T, N)))
+    dA = gf.gemm_f16_grouped_nn(D, B, o, _sentinel((T, K)))
+    dB = gf.gemm_f16_grouped_tn(D, A, o)
+    torch.cuda.synchronize()
+    for t in (C, dA):
+        v = t.view(torch.int16)
+        assert (v[:1] == SENTINEL).all() and (v[-2:] == SENTINEL).all() and not (v[1:-2] == SENTINEL).all(1).any()
+    _check_groups(C, A, B.transpose(1, 2), off, groups, K, "nt")
+    _check_groups(dA, D, B, off, groups, N, "nn")
+    for e in groups:
+        r = slice(int(off[e]), int(off[e + 1]))
+        d, a = D[r].double(), A[r].double()
+        plain.check(dB[e].cpu().numpy(), (d.t() @ a).cpu().numpy(), (d.abs().t() @ a.abs()).cpu().numpy(),
+                    max(1, r.stop - r.start), plain.F16, "tn group %d" % e)
+    for group in (32, 128):
+        Q, S, Z = gf.w4_quantize_f16(B, group)
+        C = gf.gemm_w4_f16_grouped_nt(A, Q, S, Z, o, _sentinel((T, N)), group)
+        torch.cuda.synchronize()
+        at = torch.tensor(groups, device="cuda")
+        q = plain.unpack(Q[at].flatten(0, 1).cpu().numpy())
+        W = plain.weights(q, S[at].flatten(0, 1).cpu().numpy(), Z[at].flatten(0, 1).cpu().numpy(), group)
+        W = torch.from_numpy(W).cuda().view(len(groups), N, K).transpose(1, 2)
+        _check_groups(C, A, dict(zip(groups, W)), off, groups, K, "w4")
+
+
+@pytest.mark.parametrize("form", ["nt", "nn"])
+def test_rounds_of_tiles_over_more_groups_than_lanes(form):
+    """The launch in two parts, with the scan over the groups in two passes."""
+    E, N, K = 70, 700, 1032
+    sizes = np.random.default_rng(11).integers(0, 430, E)
+    sizes[[0, 63, 64, 69]] = 257, 1, 0, 400
+    sizes[5] += 196 * E - min(int(sizes.sum()), 196 * E)    # a mean of 196 rows at least
+    off, T = plain.offsets_of(sizes), int(sizes.sum())
+    A, B = _half(12, T, K), _half(13, E, *((N, K) if form == "nt" else (K, N)), scale=0.03)
+    _say("rounds", form, T)
+    C = (gf.gemm_f16_grouped_nt if form == "nt" else gf.gemm_f16_grouped_nn)(A, B, dev(off), _sentinel((T, N)))
+    torch.cuda.synchronize()
+    _check_groups(C, A, B.transpose(1, 2) if form == "nt" else B, off, [e for e in range(E) if sizes[e]], K, form)
