@@ -612,7 +612,8 @@ def _offsets(offsets, E):
 def gemm_f16_grouped_nt(A, B, offsets, C=None, stream=None):
     """C[r] = A[r] . B[e]^T for the rows r = offsets[e] .. offsets[e+1]-1 of
     group e: A (T, K), B (E, N, K), offsets (E+1,) int32 on the device.
-    Returns C (T, N) fp16; rows of no group are left as they were."""
+    Returns C (T, N) fp16; rows of no group are left as they were (in a C made
+    here: not set)."""
     import torch
     if A.dim() != 2 or B.dim() != 3 or A.shape[1] != B.shape[2]:
         raise ValueError("A must be (T, K) and B (E, N, K)")

@@ -90,7 +90,9 @@ int run_band(const GroupRowArgs& a, hipStream_t stream)
 //  * a handful of rows a group, K-contiguous B: the streaming form, 36 against
 //    57 for every tile at T = 48, E = 16, 4096 x 2048; 41 against 59 at T = 16,
 //    E = 8, 4096 x 4096; 16 against 20 at T = 18, E = 17, 488 x 2672.  At a mean
-//    of 19 the 64 x 64 tile is ahead of it (34 against 39);
+//    of 19 the 64 x 64 tile is ahead of it (34 against 39).  It ends at K = 8192,
+//    where each wave's part of A fills its registers (16 rows over 8 of 4096 x 14336
+//    in the 64 x 64 tile 169, of 14336 x 4096 here 137);
 //  * then 64 x 64 up to a mean of 64 (64 against 68 at T = 500, E = 16) and where
 //    there are few of 128 x 128 (46 against 74 at T = 1284, E = 2, 448 x 7072; 18
 //    against 23 at T = 400, E = 4, 2048 x 2048), 128 x 128 with three stages beyond

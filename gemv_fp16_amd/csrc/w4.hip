@@ -231,6 +231,9 @@ int tile(const W4Args& a, int64_t rows, hipStream_t stream)
 //    against 33 at 200 rows over 8 groups of 2048 x 4096; 39 against 24 at 600 over
 //    16 of 2048 x 2048), in passes of 32 rows from a mean of 9 on (42 against 55 at
 //    150 over 16 of 4096 x 4096); then tiles, but for few blocks.
+//    Both band forms end at K = 8192: each wave keeps its part of A, and two blocks of
+//    512 k are what its registers hold (16 x 4096 x 14336 in the general form 24, 16 x
+//    4096 x 8192 here 8.5; by expert 93 at 24 rows over 8 of 4096 x 14336).
 //  * what is left takes the general form, with 16 rows of A by 32 of Q (16 by 16
 //    for few rows of both; 32 by 64 for many rows of both where groups of 128
 //    leave the registers for it: 23 against 38 at 32 x 16384 x 5000, but 40 against

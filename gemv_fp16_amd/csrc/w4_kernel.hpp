@@ -129,8 +129,8 @@ __device__ __forceinline__ float w4_beside_tie(float q, float lost)
 // Bound by HBM and the vector ALU alike (2 bytes read and half a byte written
 // for about 10 instructions), so the codes are put together as exact fp32
 // integers, six to a sum, and the zero point is added to all eight at once.
-// 8192 x 8192 in groups of 128 with zero points: 42 us, 4.0 TB/s, the vector ALU
-// busy for 72 % of it.
+// 8192 x 8192 in groups of 128 with zero points: 41 us, 4.1 TB/s, the vector ALU
+// busy for 74 % of it.
 template <int GROUP, bool ASYM, bool VEC, bool SHORT>
 __global__ __launch_bounds__(256) void w4_quantize_kernel(const uint16_t* __restrict__ W,
                                                           uint32_t* __restrict__ Q,
@@ -918,7 +918,7 @@ __global__ __launch_bounds__(Cfg::WAVES * 64) void w4_band_kernel(W4Args a, int 
 //    cleared once the last step has landed.  No load stands under a branch or
 //    goes through the flat path: the compiler would then wait for all of them
 //    wherever it needs one.
-// 2048 x 8192 x 4096 in groups of 128: 127 us, 1080 TFLOP/s (gemm_f16_nt's tiles
+// 2048 x 8192 x 4096 in groups of 128: 129 us, 1065 TFLOP/s (gemm_f16_nt's tiles
 // reach 1280 to 1370 at 8192 x 8192 x 8192).
 template <int FM_, int FN_, int WM_, int WN_, int STAGES_>
 struct W4TileCfg {

@@ -15,11 +15,13 @@ Ops (inputs are the seeded uniform[-1,1] fp16 workloads):
           once on the GPU from a dense uniform A; default tile config)
   compress  2:4 compression of an 8192 x 8192 A, rotating 3 copies (384 MiB)
   w4      4-bit weights with zero points in groups of 128: quantize and back (8192 x 8192, 3
-          copies), one token against 8192 x 8192 (16 copies), 24 rows against 11008 x 4096 (24
-          copies) and 2048 rows against 8192 x 4096
+          copies), one token against 1024 x 1024 (64 copies) and 8192 x 8192 (16), 24 rows against
+          11008 x 4096 (24; the same without zero points in groups of 64) and 2048 rows against
+          8192 x 4096
   grouped products by expert over uneven groups: a decode batch of 48 rows over 16 experts of
           4096 x 2048, 8191 rows over 8 of 4096 x 4096, both gradients of 4096 rows over 8 of
-          4096 x 2048 and of 2999 over 32 of 1024 x 2048, and with 4-bit weights 24 rows over 16
+          4096 x 2048 and of 2999 over 32 of 1024 x 2048 (the one of the weights in fp32 and in
+          fp16), and with 4-bit weights 24 rows over 16
           of 4096 x 4096 and 1111 over 8 of 2048 x 4096 (weights of the small ones: 3 copies)
   copy    torch copy of a 512 MiB buffer: a plain copy kernel of known size,
           the calibration for the HBM byte counters
@@ -135,11 +137,12 @@ def main(argv=None):
             gf.w4_quantize_f16(Ws[i % 3], Q=Q, S=S, Z=Z)
             gf.w4_dequantize_f16(Q, S, Z, W=Ws[i % 3])
         del Ws, outs
-        for m, n, k, copies in ((1, 8192, 8192, 16), (24, 11008, 4096, 24), (2048, 8192, 4096, 1)):
-            w = [gf.w4_quantize_f16(half(torch, i, n, k)) for i in range(copies)]
+        for m, n, k, group, copies in ((1, 1024, 1024, 128, 64), (1, 8192, 8192, 128, 16), (24, 11008, 4096, 128, 24),
+                                       (24, 11008, 4096, 64, 24), (2048, 8192, 4096, 128, 1)):
+            w = [gf.w4_quantize_f16(half(torch, i, n, k), group, symmetric=group == 64) for i in range(copies)]
             A, C = half(torch, 99, m, k), torch.empty((m, n), dtype=torch.float16, device="cuda")
             for i in range(a.iters):
-                gf.gemm_w4_f16_nt(A, *w[i % copies], C=C)
+                gf.gemm_w4_f16_nt(A, *w[i % copies], C=C, group=group)
     elif a.op == "grouped":
         for rows, e, n, k, copies in ((48, 16, 4096, 2048, 3), (8191, 8, 4096, 4096, 1)):
             off, A = offsets(torch, rows, e), half(torch, 98, rows, k)
@@ -150,10 +153,11 @@ def main(argv=None):
         for rows, e, n, k in ((4096, 8, 4096, 2048), (2999, 32, 1024, 2048)):
             off, A, B, D = offsets(torch, rows, e), half(torch, 97, rows, k), half(torch, 0, e, n, k), half(torch, 96, rows, n)
             dA = torch.empty_like(A)
-            dB = torch.empty((e, n, k), dtype=torch.float32, device="cuda")
+            dBs = [torch.empty((e, n, k), dtype=t, device="cuda") for t in (torch.float32, torch.float16)]
             for _ in range(a.iters):
                 gf.gemm_f16_grouped_nn(D, B, off, dA)
-                gf.gemm_f16_grouped_tn(D, A, off, dB)
+                for dB in dBs:
+                    gf.gemm_f16_grouped_tn(D, A, off, dB)
         for rows, e, n, k, copies in ((24, 16, 4096, 4096, 3), (1111, 8, 2048, 4096, 3)):
             off, A = offsets(torch, rows, e), half(torch, 95, rows, k)
             w = [gf.w4_quantize_f16(half(torch, i, e, n, k)) for i in range(copies)]
