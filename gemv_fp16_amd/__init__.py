@@ -17,6 +17,7 @@ LIB_PATH = os.environ.get("GEMVFP16_LIB") or os.path.join(_HERE, "libgemvfp16.so
 
 GF_OK, GF_ERR_INVALID_ARG, GF_ERR_HIP, GF_ERR_UNSUPPORTED, GF_ERR_TOO_LARGE = 0, 1, 2, 3, 4
 GF_SPLITK_ATOMIC, GF_SPLITK_TWOPASS, GF_SPLITK_F16 = 0, 1, 2
+GF_ROUTE_SOFTMAX, GF_ROUTE_SIGMOID = 0, 1
 
 EXPORTS = (
     "gemm_f16_nt", "gemm_f16_nt_splitk", "gemv_f16",
@@ -30,6 +31,9 @@ EXPORTS = (
     "gf_sp_config_get", "gf_sp_default_config",
     "gemm_f16_grouped_nt", "gemm_f16_grouped_nn", "gemm_f16_grouped_tn",
     "w4_quantize_f16", "w4_dequantize_f16", "gemm_w4_f16_nt", "gemv_w4_f16", "gemm_w4_f16_grouped_nt",
+    "route_workspace_bytes", "route_topk", "route_rows", "route_topk_bwd",
+    "dispatch_f16", "combine_f16", "combine_f16_bwd",
+    "lora_workspace_bytes", "gemm_f16_nt_lora", "lora_add_f16",
 )
 
 
@@ -57,6 +61,11 @@ class GemvCfg(ctypes.Structure):
 
     def as_dict(self):
         return {n: getattr(self, n) for n, _ in self._fields_}
+
+
+class RouteCfg(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("score", "renorm", "groups", "top_groups", "group_best")] + \
+        [("scale", ctypes.c_float)]
 
 
 _lib = None
@@ -108,10 +117,21 @@ def lib() -> ctypes.CDLL:
     L.gemm_w4_f16_nt.argtypes = [vp, vp, vp, vp, vp, ci, ci, ci, ci, vp]
     L.gemv_w4_f16.argtypes = [vp, vp, vp, vp, vp, ci, ci, ci, vp]
     L.gemm_w4_f16_grouped_nt.argtypes = [vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, vp]
+    L.route_workspace_bytes.argtypes = [ci, ci, ci]
+    L.route_topk.argtypes = [vp, ci, vp, ci, ci, ci, ctypes.POINTER(RouteCfg), vp, vp, vp, vp, vp, sz, vp]
+    L.route_rows.argtypes = [vp, ci, ci, ci, vp, vp, vp, sz, vp]
+    L.route_topk_bwd.argtypes = [vp, ci, vp, vp, ci, ci, ci, ctypes.POINTER(RouteCfg), vp, vp]
+    L.dispatch_f16.argtypes = [vp, vp, vp, ci, ci, ci, ci, vp]
+    L.combine_f16.argtypes = [vp, vp, vp, vp, ci, ci, ci, ci, vp]
+    L.combine_f16_bwd.argtypes = [vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, vp]
+    L.lora_workspace_bytes.argtypes = [ci, ci, ci, ci]
+    L.gemm_f16_nt_lora.argtypes = [vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, vp, sz, vp]
+    L.lora_add_f16.argtypes = [vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, vp, sz, vp]
     L.gf_status_string.argtypes = [ci]
     L.gf_status_string.restype = ctypes.c_char_p
+    L.route_workspace_bytes.restype = L.lora_workspace_bytes.restype = sz
     for name in EXPORTS:
-        if name not in ("gemm_f16_nt_splitk_workspace_bytes", "gf_noalloc_scratch_bytes", "gf_status_string"):
+        if not name.endswith("_bytes") and name != "gf_status_string":
             getattr(L, name).restype = ci
     _lib = L
     return L
@@ -773,3 +793,244 @@ def gemm_w4_f16_grouped_nt(A, Q, S, Z, offsets, C=None, group: int = 128, stream
     _launch("gemm_w4_f16_grouped_nt", (A, Q, S, offsets, C) if Z is None else (A, Q, S, offsets, C, Z), stream,
             _ptr(A, f16, "A"), *_w4_ptrs(Q, S, Z), _ptr(C, f16, "C"), _offsets(offsets, E), T, E, N, K, group)
     return C
+
+
+# ---------------------------------------------------------------------------
+# routing to experts, rows to experts and back
+# ---------------------------------------------------------------------------
+
+_SCORES = {"softmax": GF_ROUTE_SOFTMAX, "sigmoid": GF_ROUTE_SIGMOID}
+_route_cfgs = {}      # a call's options as the library takes them, built once
+
+
+def _route_cfg(*options):
+    ref = _route_cfgs.get(options)
+    if ref is None:
+        score, renorm, groups, top_groups, group_best, scale = options
+        if score not in _SCORES:
+            raise ValueError("score must be softmax or sigmoid")
+        if scale != scale:
+            raise ValueError("scale is not a number")
+        if len(_route_cfgs) > 1000:
+            _route_cfgs.clear()
+        ref = _route_cfgs[options] = ctypes.byref(RouteCfg(_SCORES[score], 1 if renorm else 0, groups, top_groups,
+                                                           group_best, scale))
+    return ref
+
+
+def _logits(x):
+    import torch
+    f32 = x.dtype is torch.float32
+    return _ptr(x, torch.float32 if f32 else torch.float16, "logits"), 1 if f32 else 0
+
+
+def _workspace(t, like, need, stream):
+    """Address and bytes of a workspace of `need` bytes: the caller's, checked, or
+    a new one (returned too, to be kept for the call), nothing for 0."""
+    import torch
+    if t is not None:
+        if t.dim() != 1:
+            raise ValueError("workspace must have one dimension")
+        p = _ptr(t, torch.uint8, "workspace")
+        if t.shape[0] < need:
+            raise ValueError("workspace must hold %d bytes" % need)
+        return p, t.shape[0], t
+    if need == 0:
+        return None, 0, None
+    t = _out(None, like, (need,), torch.uint8, stream, "workspace")
+    return t.data_ptr(), need, t
+
+
+def route_workspace_bytes(T: int, E: int, k: int) -> int:
+    _ints(T | E | k)
+    return int(lib().route_workspace_bytes(T, E, k))
+
+
+def route_topk(logits, k: int, bias=None, score: str = "softmax", groups: int = 1, top_groups: int = 1,
+               group_best: int = 1, renorm: bool = True, scale: float = 1.0, rows: bool = True, ids=None,
+               weights=None, offsets=None, place=None, workspace=None, stream=None):
+    """The k experts of each token's logits (T, E), fp16 or fp32, and their weights.
+
+    Scores are softmax or sigmoid; the experts of the largest score + bias (E,)
+    fp32 are taken, of the top_groups best of `groups` groups (by the sum of a
+    group's group_best largest), in descending order, ties to the lower index.
+    Weights: scale * score, over the sum of the taken scores with renorm.  An
+    expert whose logit is -inf is never taken; where none is left the id is -1
+    and the weight 0.  Returns (ids (T, k) int32, weights (T, k) fp32, offsets
+    (E+1,) int32, place (T, k) int32): the experts' row groups, and each choice's
+    row when they are sorted by expert (None, None with rows=False)."""
+    import torch
+    if logits.dim() != 2 or not 1 <= k <= logits.shape[1]:
+        raise ValueError("logits must be (T, E) and k 1 to E")
+    T, E = logits.shape
+    _ints(T | E | groups | top_groups | group_best)
+    cfg = _route_cfg(score, bool(renorm), groups, top_groups, group_best, scale)
+    x, f32 = _logits(logits)
+    i32, f = torch.int32, torch.float32
+    if bias is not None and bias.shape != (E,):
+        raise ValueError("bias must be (%d,)" % E)
+    if not rows and (offsets is not None or place is not None):
+        raise ValueError("offsets and place need rows=True")
+    ids = _out(ids, logits, (T, k), i32, stream, "ids")
+    weights = _out(weights, logits, (T, k), f, stream, "weights")
+    tensors = [logits, ids, weights]
+    b = o = p = w = None
+    need = 0
+    if bias is not None:
+        b = _ptr(bias, f, "bias")
+        tensors.append(bias)
+    if rows:
+        offsets = _out(offsets, logits, (E + 1,), i32, stream, "offsets")
+        place = _out(place, logits, (T, k), i32, stream, "place")
+        o, p = _ptr(offsets, i32, "offsets"), _ptr(place, i32, "place")
+        w, need, keep = _workspace(workspace, logits, (_lib or lib()).route_workspace_bytes(T, E, k), stream)
+        tensors += (offsets, place) if keep is None else (offsets, place, keep)
+    _launch("route_topk", tensors, stream, x, f32, b, T, E, k, cfg, _ptr(ids, i32, "ids"),
+            _ptr(weights, f, "weights"), o, p, w, need)
+    return ids, weights, offsets, place
+
+
+def route_rows(ids, E: int, offsets=None, place=None, workspace=None, stream=None):
+    """The choices ids (T, k) int32 sorted by expert, as route_topk sorts its own:
+    (offsets (E+1,), place (T, k)); an id outside 0 .. E-1 is none (place -1)."""
+    import torch
+    if ids.dim() != 2:
+        raise ValueError("ids must be (T, k)")
+    T, k = ids.shape
+    _ints(T | k | E)
+    i32 = torch.int32
+    offsets = _out(offsets, ids, (E + 1,), i32, stream, "offsets")
+    place = _out(place, ids, (T, k), i32, stream, "place")
+    w, need, keep = _workspace(workspace, ids, (_lib or lib()).route_workspace_bytes(T, E, k), stream)
+    _launch("route_rows", (ids, offsets, place) if keep is None else (ids, offsets, place, keep), stream,
+            _ptr(ids, i32, "ids"), T, k, E, _ptr(offsets, i32, "offsets"), _ptr(place, i32, "place"), w, need)
+    return offsets, place
+
+
+def route_topk_bwd(logits, ids, dweights, score: str = "softmax", renorm: bool = True, scale: float = 1.0,
+                   dlogits=None, stream=None):
+    """The gradient of route_topk's weights, dweights (T, k) fp32, to that of its
+    logits (T, E); ids (T, k) as it gave them, score, renorm and scale as it took
+    them.  Returns dlogits (T, E) of the logits' type."""
+    import torch
+    if logits.dim() != 2 or ids.dim() != 2 or ids.shape[0] != logits.shape[0] or dweights.shape != ids.shape:
+        raise ValueError("logits must be (T, E), ids and dweights (T, k)")
+    (T, E), k = logits.shape, ids.shape[1]
+    x, f32 = _logits(logits)
+    _ints(T | E | k)
+    cfg = _route_cfg(score, bool(renorm), 1, 1, 1, scale)
+    dlogits = _out(dlogits, logits, (T, E), logits.dtype, stream, "dlogits")
+    _launch("route_topk_bwd", (logits, ids, dweights, dlogits), stream, x, f32, _ptr(ids, torch.int32, "ids"),
+            _ptr(dweights, torch.float32, "dweights"), T, E, k, cfg, _ptr(dlogits, logits.dtype, "dlogits"))
+    return dlogits
+
+
+def dispatch_f16(X, place, A=None, stream=None):
+    """A[place[t][j]] = X[t]: each token's row (T, D) to its choices' rows, place
+    (T, k) int32 as route_topk gives it.  Returns A, the caller's (R, D) or a new
+    (T*k, D); rows that place does not name are left as they were (in an A made
+    here: not set).  Its gradient is combine_f16 without weights."""
+    import torch
+    if X.dim() != 2 or place.dim() != 2 or place.shape[0] != X.shape[0]:
+        raise ValueError("X must be (T, D) and place (T, k)")
+    (T, D), k = X.shape, place.shape[1]
+    f16 = torch.float16
+    if A is None:
+        A = _out(None, X, (T * k, D), f16, stream, "A")
+    elif A.dim() != 2 or A.shape[1] != D:
+        raise ValueError("A must be (R, %d)" % D)
+    R = A.shape[0]
+    _ints(T | D | k | R)
+    _launch("dispatch_f16", (X, place, A), stream, _ptr(X, f16, "X"), _ptr(place, torch.int32, "place"),
+            _ptr(A, f16, "A"), T, k, R, D)
+    return A
+
+
+def combine_f16(C, place, weights=None, Y=None, stream=None):
+    """Y[t] = sum over j of weights[t][j] * C[place[t][j]] (weights (T, k) fp32, or
+    None for 1), in fp32, rounded once: the experts' rows C (R, D) back to their
+    tokens.  Returns Y (T, D); a token whose choices name no row gets zeros."""
+    import torch
+    if C.dim() != 2 or place.dim() != 2:
+        raise ValueError("C must be (R, D) and place (T, k)")
+    (R, D), (T, k) = C.shape, place.shape
+    if weights is not None and weights.shape != place.shape:
+        raise ValueError("weights must be (%d, %d)" % (T, k))
+    _ints(R | D | T | k)
+    f16 = torch.float16
+    Y = _out(Y, C, (T, D), f16, stream, "Y")
+    w = None if weights is None else _ptr(weights, torch.float32, "weights")
+    _launch("combine_f16", (C, place, Y) if w is None else (C, place, Y, weights), stream, _ptr(C, f16, "C"),
+            _ptr(place, torch.int32, "place"), w, _ptr(Y, f16, "Y"), T, k, R, D)
+    return Y
+
+
+def combine_f16_bwd(dY, C, place, weights, dC=None, dweights=None, stream=None):
+    """combine_f16's gradients: dC[place[t][j]] = weights[t][j] * dY[t] and
+    dweights[t][j] = dY[t] . C[place[t][j]].  Returns (dC (R, D) fp16, dweights
+    (T, k) fp32); rows that place does not name are left as they were (in a dC
+    made here: not set)."""
+    import torch
+    if dY.dim() != 2 or C.dim() != 2 or place.dim() != 2 or dY.shape[1] != C.shape[1] or place.shape[0] != dY.shape[0]:
+        raise ValueError("dY must be (T, D), C (R, D) and place (T, k)")
+    (R, D), (T, k) = C.shape, place.shape
+    if weights.shape != place.shape:
+        raise ValueError("weights must be (%d, %d)" % (T, k))
+    _ints(R | D | T | k)
+    f16, f32 = torch.float16, torch.float32
+    dC = _out(dC, C, (R, D), f16, stream, "dC")
+    dweights = _out(dweights, weights, (T, k), f32, stream, "dweights")
+    _launch("combine_f16_bwd", (dY, C, place, weights, dC, dweights), stream, _ptr(dY, f16, "dY"), _ptr(C, f16, "C"),
+            _ptr(place, torch.int32, "place"), _ptr(weights, f32, "weights"), _ptr(dC, f16, "dC"),
+            _ptr(dweights, f32, "dweights"), T, k, R, D)
+    return dC, dweights
+
+
+# ---------------------------------------------------------------------------
+# low-rank adapters
+# ---------------------------------------------------------------------------
+
+def lora_workspace_bytes(M: int, N: int, K: int, r: int) -> int:
+    _ints(M | N | K | r)
+    return int(lib().lora_workspace_bytes(M, N, K, r))
+
+
+def _lora(name, A, B, ids, Down, Up, C, scales, workspace, stream):
+    import torch
+    if Down.dim() != 3 or Up.dim() != 3 or Down.shape[0] != Up.shape[0] or Down.shape[1] != Up.shape[2]:
+        raise ValueError("Down must be (L, r, K) and Up (L, N, r)")
+    (L, r, K), N = Down.shape, Up.shape[1]
+    if A.dim() != 2 or A.shape[1] != K or ids.shape != A.shape[:1]:
+        raise ValueError("A must be (M, %d) and ids (M,)" % K)
+    if B is not None and B.shape != (N, K):
+        raise ValueError("B must be (%d, %d)" % (N, K))
+    if scales is not None and scales.shape != (L,):
+        raise ValueError("scales must be (%d,)" % L)
+    M, f16 = A.shape[0], torch.float16
+    _ints(M | N | K | r | L)
+    if not 1 <= r <= 256:
+        raise ValueError("the rank must be 1 to 256")
+    C = _out(C, A, (M, N), f16, stream, "C")
+    w, size, keep = _workspace(workspace, A, (_lib or lib()).lora_workspace_bytes(M, N, K, r), stream)
+    tensors = [t for t in (A, B, ids, Down, Up, C, scales, keep) if t is not None]
+    head = (_ptr(A, f16, "A"),) if B is None else (_ptr(A, f16, "A"), _ptr(B, f16, "B"))
+    _launch(name, tensors, stream, *head, _ptr(ids, torch.int32, "ids"), _ptr(Down, f16, "Down"), _ptr(Up, f16, "Up"),
+            None if scales is None else _ptr(scales, torch.float32, "scales"), _ptr(C, f16, "C"), M, N, K, r, L, w, size)
+    return C
+
+
+def gemm_f16_nt_lora(A, B, ids, Down, Up, scales=None, C=None, workspace=None, stream=None):
+    """C[m] = A[m] . B^T + scales[a] * (A[m] . Down[a]^T) . Up[a]^T with the adapter
+    a = ids[m] of each row: A (M, K), B (N, K), ids (M,) int32 (outside 0 .. L-1:
+    none), Down (L, r, K), Up (L, N, r), scales (L,) fp32 or None for 1.  Returns C
+    (M, N) fp16.  workspace: uint8, lora_workspace_bytes(M, N, K, r) of them."""
+    return _lora("gemm_f16_nt_lora", A, B, ids, Down, Up, C, scales, workspace, stream)
+
+
+def lora_add_f16(A, ids, Down, Up, C, scales=None, workspace=None, stream=None):
+    """C[m] += scales[a] * (A[m] . Down[a]^T) . Up[a]^T in place, as in
+    gemm_f16_nt_lora, after a projection with 4-bit or 2:4 sparse weights.
+    Returns C (M, N) fp16; rows without an adapter are left as they were."""
+    if C is None:
+        raise ValueError("C must be given")
+    return _lora("lora_add_f16", A, None, ids, Down, Up, C, scales, workspace, stream)

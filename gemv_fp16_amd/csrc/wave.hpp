@@ -1,0 +1,90 @@
+// Reductions over the 64 lanes of a wave, through DPP moves (no LDS).
+#pragma once
+#include "common.hpp"
+
+namespace gf {
+
+// One DPP move of 32 bits; lanes without a source keep `old`.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_move(int old, int v)
+{
+    return __builtin_amdgcn_update_dpp(old, v, CTRL, ROWS, 0xF, false);
+}
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_move(float old, float v)
+{
+    return __builtin_bit_cast(float, dpp_move<CTRL, ROWS>(__builtin_bit_cast(int, old), __builtin_bit_cast(int, v)));
+}
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_move(double old, double v)
+{
+    typedef int int2v __attribute__((ext_vector_type(2)));
+    const int2v o = __builtin_bit_cast(int2v, old), x = __builtin_bit_cast(int2v, v);
+    int2v r;
+    r.x = dpp_move<CTRL, ROWS>(o.x, x.x);
+    r.y = dpp_move<CTRL, ROWS>(o.y, x.y);
+    return __builtin_bit_cast(double, r);
+}
+
+__device__ __forceinline__ int lane_value(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+
+__device__ __forceinline__ float lane_value(float v, int lane)
+{
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+
+__device__ __forceinline__ double lane_value(double v, int lane)
+{
+    typedef int int2v __attribute__((ext_vector_type(2)));
+    int2v x = __builtin_bit_cast(int2v, v);
+    x.x = __builtin_amdgcn_readlane(x.x, lane);
+    x.y = __builtin_amdgcn_readlane(x.y, lane);
+    return __builtin_bit_cast(double, x);
+}
+
+// op over all lanes (every lane must be active): within the rows of 16 by quad
+// permutes and mirrors, then row 0 into 1 and 2 into 3, then both into lane 63.
+// `id` is op's identity.  Wave-uniform, always the same order.
+template <class T, class Op>
+__device__ __forceinline__ T wave_reduce(T v, T id, Op op)
+{
+    v = op(v, dpp_move<0xB1, 0xF>(id, v));     // lanes 1 0 3 2
+    v = op(v, dpp_move<0x4E, 0xF>(id, v));     // lanes 2 3 0 1
+    v = op(v, dpp_move<0x141, 0xF>(id, v));    // mirrored within 8
+    v = op(v, dpp_move<0x140, 0xF>(id, v));    // mirrored within 16
+    v = op(v, dpp_move<0x142, 0xA>(id, v));    // lane 15 of rows 0, 2 into rows 1, 3
+    v = op(v, dpp_move<0x143, 0xC>(id, v));    // lane 31 into rows 2, 3
+    return lane_value(v, kWave - 1);
+}
+
+// A NaN loses to any number.
+__device__ __forceinline__ float wave_max(float v)
+{
+    return wave_reduce(v, -__builtin_inff(), [](float a, float b) { return __builtin_fmaxf(a, b); });
+}
+
+__device__ __forceinline__ double wave_max(double v)
+{
+    return wave_reduce(v, -__builtin_inf(), [](double a, double b) { return __builtin_fmax(a, b); });
+}
+
+template <class T>
+__device__ __forceinline__ T wave_sum(T v)
+{
+    return wave_reduce(v, T(0), [](T a, T b) { return a + b; });
+}
+
+// Inclusive sums over the lanes.
+__device__ __forceinline__ int wave_scan(int v, int lane)
+{
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) {
+        const int u = __shfl_up(v, d);
+        if (lane >= d) v += u;
+    }
+    return v;
+}
+
+}  // namespace gf

@@ -431,6 +431,110 @@ int gemv_w4_f16(const void* Q, const void* S, const void* Z, const void* x, void
 int gemm_w4_f16_grouped_nt(const void* A, const void* Q, const void* S, const void* Z, void* C,
                            const int* offsets, int T, int E, int N, int K, int group, void* stream);
 
+/*
+ * Routing to experts, and the rows that the grouped products read.
+ *
+ * route_topk: of the logits x (T x E, fp16 or, with logits_f32 = 1, float) of T
+ * tokens, each token's k experts and their weights.  Scores s are the softmax of
+ * the token's logits or their sigmoids (cfg->score).  The k experts of the
+ * largest s + bias (bias: E floats, or NULL) are taken, in descending order,
+ * equal ones by the lower index; the sums are compared in 64 bits.  With
+ * cfg->groups > 1 the experts form that many groups of E / groups consecutive
+ * ones, a group ranks by the sum of its cfg->group_best (1 or 2) largest s +
+ * bias, and only the cfg->top_groups best groups' experts are taken (equal
+ * groups by the lower index).  An expert whose logit or bias is -infinity is
+ * never taken, and where fewer than k are left the id is -1 and the weight 0; a
+ * NaN ranks above every number.
+ * ids: T x k ints.  weights: T x k floats, scale * s of the taken experts, or
+ * scale * s / (the sum of the token's taken s) with cfg->renorm = 1; NaN where
+ * the scores are (under a softmax, a NaN or +infinity among the logits).
+ * offsets and place, both NULL or both not: the T * k choices sorted by expert,
+ * stable in (token, choice), as route_rows gives them.
+ *
+ * route_rows: the same of ids (T x k) from elsewhere.  offsets: E + 1 ints, the
+ * row groups of gemm_f16_grouped_nt and its kin.  place: T x k ints, the sorted row
+ * of each choice.  An id outside 0 .. E - 1 is none: it has place -1 and no row, so
+ * rows from offsets[E] on belong to no group.  T == 0 writes offsets of zero.
+ *
+ * route_topk_bwd: the gradient of the weights (dweights, T x k floats) to that of
+ * the logits (dlogits, T x E, every entry written, of the logits' type), the ids
+ * being constants; an id outside 0 .. E - 1 or an expert of logit -infinity gets
+ * nothing.  Reads score, renorm and scale of cfg.  The bias has no gradient.
+ *
+ * At most 1024 experts, 64 choices and 64 groups, T at most 2^30, T * E and T * k
+ * below 2^31, 1 <= k <= E, and the groups kept must hold k experts.
+ * workspace: caller-owned device memory of at least route_workspace_bytes(T, E, k)
+ * bytes, 4-byte aligned, which may be 0 (then NULL does); route_topk without
+ * offsets needs none.  Every result repeats bit for bit.  GF_ERR_INVALID_ARG for
+ * sizes, flags or groups outside these, NULL or misaligned pointers (logits by
+ * their type, all else 4 bytes), or a short workspace.
+ */
+enum { GF_ROUTE_SOFTMAX = 0, GF_ROUTE_SIGMOID = 1 };
+typedef struct gf_route_cfg {
+    int score, renorm, groups, top_groups, group_best;
+    float scale;
+} gf_route_cfg;
+size_t route_workspace_bytes(int T, int E, int k);
+int route_topk(const void* logits, int logits_f32, const float* bias, int T, int E, int k, const gf_route_cfg* cfg,
+               int* ids, float* weights, int* offsets, int* place, void* workspace, size_t workspace_bytes,
+               void* stream);
+int route_rows(const int* ids, int T, int k, int E, int* offsets, int* place, void* workspace,
+               size_t workspace_bytes, void* stream);
+int route_topk_bwd(const void* logits, int logits_f32, const int* ids, const float* dweights, int T, int E, int k,
+                   const gf_route_cfg* cfg, void* dlogits, void* stream);
+
+/*
+ * Rows to experts and back.  place: T x k ints in device memory, each the row of
+ * one choice of a token among R sorted rows (route_topk, route_rows); entries
+ * outside 0 .. R - 1 are no row.  Rows that place does not name are left as they
+ * were; if it names a row twice, that row holds either.  All matrices are fp16 with
+ * rows of D, at any 2-byte alignment (16 bytes and D % 8 == 0 are fastest).
+ *
+ * dispatch_f16: A[place[t][j]] = X[t], X T x D, A R x D.  Its gradient is
+ * combine_f16 without weights.
+ * combine_f16: Y[t] = sum over j, ascending, of weights[t][j] * C[place[t][j]], in
+ * fp32, rounded once; weights: T x k floats, or NULL for 1.  A choice of no row adds
+ * nothing, whatever its weight; a token of none gets +0.
+ * combine_f16_bwd: dC[place[t][j]] = weights[t][j] * dY[t], rounded once, and
+ * dweights[t][j] = dY[t] . C[place[t][j]] in fp32 (0 for a choice of no row).
+ *
+ * T, R and D at most 2^30, k at most 64, T * k, T * D and R * D below 2^31.
+ * GF_ERR_INVALID_ARG for sizes past these or negative, k < 1, NULL or misaligned
+ * pointers.  T == 0 or D == 0 is a no-op, but for dweights, which D == 0 sets to 0.
+ */
+int dispatch_f16(const void* X, const int* place, void* A, int T, int k, int R, int D, void* stream);
+int combine_f16(const void* C, const int* place, const float* weights, void* Y, int T, int k, int R, int D,
+                void* stream);
+int combine_f16_bwd(const void* dY, const void* C, const int* place, const float* weights, void* dC,
+                    float* dweights, int T, int k, int R, int D, void* stream);
+
+/*
+ * Low-rank adapters of many requests beside a shared projection.  Row m of A (M x
+ * K) has the adapter a = ids[m] (M ints in device memory): Down[a] (r x K) and
+ * Up[a] (N x r), of L adapters (Down L x r x K, Up L x N x r, all fp16), and
+ * scales[a] (L floats, or NULL for 1).  An id outside 0 .. L - 1 is none.
+ *
+ * gemm_f16_nt_lora: C[m] = A[m] . B^T + scales[a] * (A[m] . Down[a]^T) . Up[a]^T, B
+ * and C as in gemm_f16_nt.
+ * lora_add_f16: C[m] = C[m] + scales[a] * (A[m] . Down[a]^T) . Up[a]^T in place,
+ * after a projection that has no such form (4-bit or 2:4 sparse weights); the rows
+ * without an adapter are left as they were.
+ *
+ * fp32 accumulation.  Ranks 1 <= r <= 256; K % 8 == 0, r % 8 == 0 and 16-byte
+ * aligned A, Down and Up are fastest, everything else runs a general form.  The
+ * adapters as a whole may pass 2^31 elements, one adapter's part and every other
+ * operand may not; no size above 2^30.  workspace: caller-owned device memory, 16-byte
+ * aligned, of at least lora_workspace_bytes(M, N, K, r) bytes.  M == 0 or N == 0 is a
+ * no-op.  Results repeat bit for bit.  GF_ERR_INVALID_ARG for sizes outside these,
+ * NULL or misaligned pointers, or a short workspace.
+ */
+size_t lora_workspace_bytes(int M, int N, int K, int r);
+int gemm_f16_nt_lora(const void* A, const void* B, const int* ids, const void* Down, const void* Up,
+                     const float* scales, void* C, int M, int N, int K, int r, int L, void* workspace,
+                     size_t workspace_bytes, void* stream);
+int lora_add_f16(const void* A, const int* ids, const void* Down, const void* Up, const float* scales, void* C,
+                 int M, int N, int K, int r, int L, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static string naming a status code. */
 const char* gf_status_string(int status);
 
