@@ -45,6 +45,9 @@ struct GemmArgs {
     int raster;         // 0: plain tile order; > 0: XCD remap + panel of this many rows
     int slices;         // split-K slices (set by launch_gemm); the grid is (tiles, slices)
     static constexpr bool PER_GROUP = false;   // one product
+    static constexpr bool LOW_RANK = false;    // nothing is added to it
+    struct Nothing {};
+    template <class MF, int MT, int KS, int FM, int FN> using Low = Nothing;
 };
 
 // 16 zero bytes: the source of direct-to-LDS chunks that lie beyond K.
@@ -648,7 +651,8 @@ __device__ __forceinline__ void mfma_tile(typename Mfma<Cfg::MT>::acc_t (&acc)[C
 
 // Args: GemmArgs, or a form of it that names one of several products
 // (PER_GROUP; grouped_kernel.hpp): its locate() then picks the workgroup's
-// product and tile, and narrows the operands to it.
+// product and tile, and narrows the operands to it; or a form with low-rank
+// adapters (LOW_RANK; lora_kernel.hpp), whose sums `low` adds before the rounding.
 template <class Cfg, int EPI, bool ALIGNED, class Args = GemmArgs>
 __global__ __launch_bounds__(Cfg::NT) void gemm_nt_kernel(Args a)
 {
@@ -912,16 +916,28 @@ __global__ __launch_bounds__(Cfg::NT) void gemm_nt_kernel(Args a)
         lds_barrier();                           // operand buffers are free now
         constexpr int LDW = Cfg::WTN + Cfg::EPAD;  // fp16 per LDS row
         GF_LDS uint16_t* reg = (GF_LDS uint16_t*)(smem + wave * (Cfg::WTM * LDW * 2));
-#pragma unroll
-        for (int fm = 0; fm < Cfg::FM; ++fm)
-#pragma unroll
-            for (int fn = 0; fn < Cfg::FN; ++fn)
+        [[maybe_unused]] typename Args::template Low<MF, MT, Cfg::KS, Cfg::FM, Cfg::FN> low;
+        if constexpr (Args::LOW_RANK) low.init(a.low, wrow0, wcol0, a.M, a.N);
+        static_for<Cfg::FM>([&](auto fm_c) {
+            constexpr int fm = decltype(fm_c)::value;
+            [[maybe_unused]] acc_t add[2];
+            static_for<Cfg::FN>([&](auto fn_c) {
+                constexpr int fn = decltype(fn_c)::value;
+                if constexpr (Args::LOW_RANK) {
+                    constexpr int FB = std::remove_reference_t<decltype(low)>::FB;
+                    if constexpr (fn % FB == 0)
+                        low.template sums<fm, fn>(a.low, (acc_t(&)[FB])add, wrow0, wcol0, a.M, a.N);
+                }
 #pragma unroll
                 for (int i = 0; i < MF::NACC; ++i) {
                     const int r = fm * MT + MF::row(i, lane);
                     const int c = fn * MT + lane % MT;
-                    reg[r * LDW + c] = f32_to_f16_bits(acc[fm][fn][i]);
+                    float v = acc[fm][fn][i];
+                    if constexpr (Args::LOW_RANK) v += add[fn % std::remove_reference_t<decltype(low)>::FB][i];
+                    reg[r * LDW + c] = f32_to_f16_bits(v);
                 }
+            });
+        });
         asm volatile("" ::: "memory");
         wait_lgkmcnt0();
         constexpr int CPR = Cfg::WTN / 8;        // 16-byte chunks per sub-tile row

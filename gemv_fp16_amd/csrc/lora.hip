@@ -13,7 +13,23 @@ bool off_grid(const void* p, uintptr_t a) { return !p || (reinterpret_cast<uintp
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 int status(hipError_t e) { return e == hipSuccess ? GF_OK : GF_ERR_HIP; }
 
-size_t workspace_need(int M, int r) { return (size_t)M * r * sizeof(float); }
+// Parts of K that the products by Down are split in, for one CU takes in no more than
+// about 40 GB/s: up to 32 rows as many as make 256 workgroups of them (the streaming
+// form adds them in LDS, which holds all), beyond as many as make 512 of 16-row blocks,
+// but no more than the tiles' epilogue loads at once (100 rows of 8 adapters at 4096 x
+// 4096: 35 us with 4 parts, 40 with one).
+constexpr int most_floats(int M) { return M <= 16 ? 3840 : 7936; }
+int parts_of(int M, int K, int r)
+{
+    if (M < 1) return 1;
+    int s = M <= 32 ? 256 / M : 512 / ceil_div(M, 16);
+    const int most = M <= 32 ? kLoraParts : kLoraTileParts;
+    if (s > K / 512) s = K / 512;
+    if (M <= 32 && s > most_floats(M) / (M * r)) s = most_floats(M) / (M * r);
+    return s < 1 ? 1 : (s > most ? most : s);
+}
+
+size_t workspace_need(int M, int K, int r) { return (size_t)parts_of(M, K, r) * M * r * sizeof(float); }
 
 int check(const void* A, const int* ids, const void* Down, const void* Up, const float* scales, const void* C, int M,
           int N, int K, int r, int L, const void* workspace, size_t workspace_bytes)
@@ -29,23 +45,151 @@ int check(const void* A, const int* ids, const void* Down, const void* Up, const
     if (K > 0 && off_grid(A, 2)) return GF_ERR_INVALID_ARG;
     if (L > 0 && (off_grid(Up, 2) || (K > 0 && off_grid(Down, 2)))) return GF_ERR_INVALID_ARG;
     if (scales && off_grid(scales, 4)) return GF_ERR_INVALID_ARG;
-    if (off_grid(workspace, 16) || workspace_bytes < workspace_need(M, r)) return GF_ERR_INVALID_ARG;
+    if (off_grid(workspace, 16) || workspace_bytes < workspace_need(M, K, r)) return GF_ERR_INVALID_ARG;
     return GF_OK;
 }
 
-int add(const LoraArgs& a, hipStream_t stream)
+LoraArgs args(const void* A, const void* B, const int* ids, const void* Down, const void* Up, const float* scales,
+              void* C, int M, int N, int K, int r, int L, void* workspace)
 {
-    const bool al = on16(a.A) && on16(a.Down) && a.K % 8 == 0;
-    const int rows = a.M < (1 << 20) ? a.M : 1 << 20;
-    if (al)
-        hipLaunchKernelGGL(lora_down_kernel<true>, dim3(rows), dim3(256), 0, stream, a);
-    else
-        hipLaunchKernelGGL(lora_down_kernel<false>, dim3(rows), dim3(256), 0, stream, a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return GF_ERR_HIP;
-    const int64_t groups = ((int64_t)a.M * a.N + 255) / 256;
-    hipLaunchKernelGGL(lora_up_kernel, dim3((unsigned)(groups < (1 << 20) ? groups : 1 << 20)), dim3(256), 0, stream, a);
+    LoraArgs a;
+    a.A = (const uint16_t*)A; a.B = (const uint16_t*)B; a.ids = ids;
+    a.Down = (const uint16_t*)Down; a.Up = (const uint16_t*)Up; a.scales = scales;
+    a.C = (uint16_t*)C; a.H = (float*)workspace;
+    a.M = M; a.N = N; a.K = K; a.r = r; a.L = L;
+    // the general forms leave K whole, and read H as one part
+    const bool split = on16(A) && on16(Down) && K % 8 == 0 && on16(Up) && r % 8 == 0;
+    a.S = split ? parts_of(M, K, r) : 1;
+    a.part = (int64_t)M * r;
+    return a;
+}
+
+constexpr int kGrid = 1 << 20;   // workgroups at most (a launch has fewer than 2^32 threads)
+int grid_of(int64_t n) { return (int)(n < kGrid ? n : kGrid); }
+
+// H = scale * A . Down^T for every row with an adapter.
+int down(const LoraArgs& a, hipStream_t stream)
+{
+    if (on16(a.A) && on16(a.Down) && a.K % 8 == 0 && a.K > 0) {
+        // a block has up to 16 adapters: as many workgroups, in about 512 of them
+        const int blocks = ceil_div(a.M, 16);
+        int Z = a.M <= 32 ? 16 : 512 / (blocks * a.S);
+        if (Z > 16) Z = 16;
+        if (Z > a.L) Z = a.L;
+        if (Z < 1) Z = 1;
+        const dim3 grid(grid_of((int64_t)blocks * Z), a.S);
+        return status(a.r <= 16 ? launch_lora_down<LoraDownCfg<8, 1>>(a, grid, Z, stream)
+                                : (a.r <= 32 ? launch_lora_down<LoraDownCfg<8, 2>>(a, grid, Z, stream)
+                                             : launch_lora_down<LoraDownCfg<4, 4>>(a, grid, Z, stream)));
+    } else {
+        hipLaunchKernelGGL(lora_down_any_kernel, dim3(grid_of(a.M)), dim3(256), 0, stream, a);
+    }
     return status(hipGetLastError());
+}
+
+// C += H . Up^T.
+int up(const LoraArgs& a, hipStream_t stream)
+{
+    if (on16(a.Up) && a.r % 8 == 0) {
+        const int vec = (reinterpret_cast<uintptr_t>(a.C) & 7) == 0 && a.N % 4 == 0;
+        const int64_t waves = (int64_t)ceil_div(a.M, 16) * ceil_div(a.N, 16);
+        if (waves <= 8192)
+            hipLaunchKernelGGL(lora_up_kernel<1>, dim3(grid_of((waves + 3) / 4)), dim3(256), 0, stream, a, vec);
+        else
+            hipLaunchKernelGGL(lora_up_kernel<4>, dim3(grid_of((waves / 4 + 3) / 4)), dim3(256), 0, stream, a, vec);
+    } else {
+        hipLaunchKernelGGL(lora_up_any_kernel, dim3(grid_of(((int64_t)a.M * a.N + 255) / 256)), dim3(256), 0, stream, a);
+    }
+    return status(hipGetLastError());
+}
+
+// Base and adapters in tiles: default_gemm_cfg's choice among four of its tiles.
+template <class Cfg>
+int tiles(const LoraArgs& a, int raster, hipStream_t stream)
+{
+    LoraTileArgs t;
+    t.A = a.A; t.B = a.B; t.C = a.C;
+    t.M = a.M; t.N = a.N; t.K = a.K;
+    t.raster = raster;
+    t.low = {a.H, a.ids, a.Up, a.part, a.S, a.r, a.L};
+    return status(launch_lora_tile<Cfg>(t, stream));
+}
+
+int tiles(const LoraArgs& a, hipStream_t stream)
+{
+    const int64_t t25612 = (int64_t)ceil_div(a.M, 256) * ceil_div(a.N, 128);
+    const int64_t t128 = (int64_t)ceil_div(a.M, 128) * ceil_div(a.N, 128);
+    const int64_t t256 = (int64_t)ceil_div(a.M, 256) * ceil_div(a.N, 256);
+    if (t256 >= 256 && a.K > 1536) return tiles<GemmCfg<256, 256, 64, 2, 256, 2>>(a, a.K <= 4096 ? 10 : (a.K < 16384 ? 0 : 4), stream);
+    if (t25612 >= 256 && a.K >= 2048) return tiles<GemmCfg<256, 128, 64, 3, 256, 2>>(a, t25612 >= 512 ? 10 : 0, stream);
+    if (t128 > 256) return tiles<GemmCfg<128, 128, 64, 2, 256, 0>>(a, 0, stream);
+    if (t128 >= 128) return tiles<GemmCfg<128, 128, 64, 4, 256, 2>>(a, 0, stream);
+    return tiles<GemmCfg<64, 64, 64, 3, 256, 0>>(a, 0, stream);
+}
+
+// Base and adapters, B in vectors; GF_ERR_UNSUPPORTED where it does not fit.  Up to 2
+// rows (4096 x 4096, rank 16: 10.9 us for one and 14.8 for two, the streaming form
+// 15.0 and 15.2; at 4 rows 18.6 against 15.1).  It works out H itself up to 64 ranks in
+// all: 10.9 us against 15.1 with a launch for it at one row, 14.8 against 17.0 at two,
+// 16.5 against 18.0 at rank 64; at 128 ranks 29 against 19.
+constexpr int kVecRows = 2, kVecSelf = 64;
+
+template <int MV, int UNROLL>
+int vec(const LoraArgs& a, hipStream_t stream)
+{
+    constexpr int WAVES = 8;
+    const int groups = ceil_div(a.N, WAVES), grid = groups < 256 ? groups : 256, iters = ceil_div(groups, grid);
+    const int64_t most = a.M < a.L ? a.M : a.L;          // adapters in use
+    const int64_t up_bytes = most * iters * WAVES * a.r * 2, sums = (int64_t)iters * WAVES * MV * 4;
+    if (up_bytes > 100 * 1024 || sums > 64 * 1024 || (int64_t)MV * lora_vec_pad(a.K, UNROLL) * 16 > 128 * 1024)
+        return GF_ERR_UNSUPPORTED;
+    const LoraVecLds at(MV, WAVES, a.K, a.r, UNROLL, iters * WAVES, (int)most);
+    if (at.total > 159 * 1024) return GF_ERR_UNSUPPORTED;
+    if (most * a.r <= kVecSelf)
+        return status(launch_lora_vec<MV, UNROLL, WAVES, true>(a, grid, iters, (int)most, at.total, stream));
+    const int rc = down(a, stream);
+    return rc ? rc : status(launch_lora_vec<MV, UNROLL, WAVES, false>(a, grid, iters, (int)most, at.total, stream));
+}
+
+template <int MV>
+int vec(const LoraArgs& a, hipStream_t stream)
+{
+    if (a.K % 4096 == 0) return vec<MV, 8>(a, stream);
+    return a.K >= 2048 ? vec<MV, 4>(a, stream) : vec<MV, 2>(a, stream);
+}
+
+// Base and adapters, B streamed once: up to 16 rows of K <= 8192, 32 of K <= 4096
+// (a wave holds its part of A in registers).
+bool band_takes(int M, int N, int K) { return N >= 16 && ((M <= 16 && K <= 8192) || (M <= 32 && K <= 4096)); }
+
+// Whether the streaming form works out H itself: one adapter of up to 16 ranks (32
+// rows at 4096 x 2048: 13.2 us against 17.0 with a launch for it, 16 at 4096 x 4096
+// 17.6 against 19.0; with two blocks of ranks 18.4 against 15.2).
+bool band_self(const LoraArgs& a)
+{
+    const int64_t most = a.M < a.L ? a.M : a.L;
+    return most * ceil_div(a.r, 16) <= 1 && a.M * a.r <= most_floats(a.M);
+}
+
+template <int MB, int XB>
+int band(const LoraArgs& a, hipStream_t stream)
+{
+    constexpr int RING = MB == 1 ? 4 : 3;
+    if constexpr (MB * XB <= 4)                  // Down's ranks in registers beside A
+        if (band_self(a)) return status(launch_lora_band<LoraBandCfg<MB, XB, RING>, true>(a, stream));
+    const int rc = down(a, stream);
+    if (rc) return rc;
+    // a smaller ring where H takes its place: 16 rows of rank 256, 32 of rank 248 on
+    if (LoraBandCfg<MB, XB, RING>::lds_bytes(a.S * a.M * a.r) <= 160 * 1024)
+        return status(launch_lora_band<LoraBandCfg<MB, XB, RING>, false>(a, stream));
+    return status(launch_lora_band<LoraBandCfg<MB, XB, RING - 1>, false>(a, stream));
+}
+
+int band(const LoraArgs& a, hipStream_t stream)
+{
+    if (a.M > 16) return a.K <= 2048 ? band<2, 2>(a, stream) : band<2, 4>(a, stream);
+    if (a.K <= 2048) return band<1, 2>(a, stream);
+    return a.K <= 4096 ? band<1, 4>(a, stream) : band<1, 8>(a, stream);
 }
 
 }  // namespace
@@ -58,19 +202,17 @@ extern "C" {
 size_t lora_workspace_bytes(int M, int N, int K, int r)
 {
     if (M < 0 || N < 0 || K < 0 || r < 1 || r > kMaxRank) return 0;
-    return workspace_need(M, r);
+    return workspace_need(M, K, r);
 }
 
 int lora_add_f16(const void* A, const int* ids, const void* Down, const void* Up, const float* scales, void* C, int M,
                  int N, int K, int r, int L, void* workspace, size_t workspace_bytes, void* stream)
 {
-    const int rc = check(A, ids, Down, Up, scales, C, M, N, K, r, L, workspace, workspace_bytes);
+    int rc = check(A, ids, Down, Up, scales, C, M, N, K, r, L, workspace, workspace_bytes);
     if (rc || M == 0 || N == 0 || L == 0) return rc;
-    LoraArgs a;
-    a.A = (const uint16_t*)A; a.ids = ids; a.Down = (const uint16_t*)Down; a.Up = (const uint16_t*)Up;
-    a.scales = scales; a.C = (uint16_t*)C; a.H = (float*)workspace;
-    a.M = M; a.N = N; a.K = K; a.r = r; a.L = L;
-    return add(a, (hipStream_t)stream);
+    const LoraArgs a = args(A, nullptr, ids, Down, Up, scales, C, M, N, K, r, L, workspace);
+    rc = down(a, (hipStream_t)stream);
+    return rc ? rc : up(a, (hipStream_t)stream);
 }
 
 int gemm_f16_nt_lora(const void* A, const void* B, const int* ids, const void* Down, const void* Up,
@@ -79,9 +221,23 @@ int gemm_f16_nt_lora(const void* A, const void* B, const int* ids, const void* D
 {
     int rc = check(A, ids, Down, Up, scales, C, M, N, K, r, L, workspace, workspace_bytes);
     if (rc || M == 0 || N == 0) return rc;
+    if (K > 0 && off_grid(B, 2)) return GF_ERR_INVALID_ARG;
+    if (L == 0) return gemm_f16_nt(A, B, C, M, N, K, stream);
+    const LoraArgs a = args(A, B, ids, Down, Up, scales, C, M, N, K, r, L, workspace);
+    const bool al = on16(A) && on16(B) && on16(Down) && on16(Up) && K % 8 == 0 && r % 8 == 0 && K > 0;
+    if (al && M <= kVecRows) {
+        rc = M == 1 ? vec<1>(a, (hipStream_t)stream) : vec<2>(a, (hipStream_t)stream);
+        if (rc != GF_ERR_UNSUPPORTED) return rc;
+    }
+    if (al && band_takes(M, N, K)) return band(a, (hipStream_t)stream);
+    // From 33 to 64 rows the base's own streaming forms and a launch that adds to their
+    // results are ahead of tiles (64 rows of 24 adapters at 4096 x 4096: 28 us against 51).
+    if (al && on16(C) && M > 64) {
+        rc = down(a, (hipStream_t)stream);
+        return rc ? rc : tiles(a, (hipStream_t)stream);
+    }
     rc = gemm_f16_nt(A, B, C, M, N, K, stream);
-    if (rc || L == 0) return rc;
-    return lora_add_f16(A, ids, Down, Up, scales, C, M, N, K, r, L, workspace, workspace_bytes, stream);
+    return rc ? rc : lora_add_f16(A, ids, Down, Up, scales, C, M, N, K, r, L, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

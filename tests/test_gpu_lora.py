@@ -151,6 +151,31 @@ def test_rows_without_an_adapter_are_the_plain_product():
         p.check(C, base, size, "finite rows")
 
 
+@pytest.mark.parametrize("M", [2, 12, 30, 50, 100, 300, 600])
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+def test_an_adapter_that_is_not_finite_stays_in_its_rows(M, bad):
+    """NaN and infinity in one adapter reach the rows that have it and no others, whichever share a tile with them."""
+    for add in (False, True):
+        p = Problem(M, 520, 1024, 16, 4, "mixed", M + 1)
+        p.ids[:] = np.random.default_rng(M).choice([0, 2, 3, -1], M)
+        p.ids[M // 2] = 1
+        p.Up[1, ::3, 5] = bad
+        p.Down[1, 7, 9] = bad
+        (A, B), ids, (Down, Up), scales = p.operands()
+        _say("lora not finite", M, bad, add)
+        if add:
+            C = gf.lora_add_f16(A, ids, Down, Up, dev(p.C0), scales)
+            base, size = p.C0.astype(np.float64), np.abs(p.C0.astype(np.float64))
+        else:
+            C = gf.gemm_f16_nt_lora(A, B, ids, Down, Up, scales)
+            base, size = p.base()
+        got = C.cpu().numpy()
+        assert not np.isfinite(got[M // 2]).any()
+        p.Up[1], p.Down[1] = 0, 0
+        C[M // 2] = dev(base[M // 2].astype(np.float16))
+        p.check(C, base, size, "the other rows")
+
+
 @pytest.mark.parametrize("M", [1, 24, 100])
 def test_beside_4_bit_and_sparse_weights(M):
     p = Problem(M, 256, 512, 16, 5, "mixed", M)
