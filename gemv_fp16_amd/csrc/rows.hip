@@ -13,23 +13,28 @@ constexpr int kMaxTop = 64;          // lane j holds a token's j-th place
 constexpr int kMaxSize = 1 << 30;
 constexpr int64_t kMaxElems = (int64_t(1) << 31) - 1;
 constexpr int kWaves = 4;
+constexpr int kTogether = 4;         // rows whose loads are in flight together
 constexpr int kGrid = 1 << 20;       // workgroups at most (a launch has fewer than 2^32 threads)
 
-// 8 fp16 at any 2-byte alignment; n < 8 of them at a row's end, zeros for the rest.
-__device__ __forceinline__ half8 load8(const uint16_t* p, int n)
+// A lane's 8 fp16 of a row of D: from d on, or, where the row ends within them, its
+// last 8 (so every lane that has any moves 8 at a time, some a second time with the
+// same result); of a row shorter than 8, those that there are, zeros for the rest.
+__device__ __forceinline__ int first_of(int d, int D) { return max(min(d, D - 8), 0); }
+
+__device__ __forceinline__ half8 load8(const uint16_t* p, int D)
 {
     half8 v = {};
-    if (n >= 8) __builtin_memcpy(&v, p, 16);
+    if (D >= 8) __builtin_memcpy(&v, p, 16);
     else
-        for (int i = 0; i < n; ++i) v[i] = __builtin_bit_cast(_Float16, p[i]);
+        for (int i = 0; i < D; ++i) v[i] = __builtin_bit_cast(_Float16, p[i]);
     return v;
 }
 
-__device__ __forceinline__ void store8(uint16_t* p, half8 v, int n)
+__device__ __forceinline__ void store8(uint16_t* p, half8 v, int D)
 {
-    if (n >= 8) __builtin_memcpy(p, &v, 16);
+    if (D >= 8) __builtin_memcpy(p, &v, 16);
     else
-        for (int i = 0; i < n; ++i) p[i] = __builtin_bit_cast(uint16_t, (_Float16)v[i]);
+        for (int i = 0; i < D; ++i) p[i] = __builtin_bit_cast(uint16_t, (_Float16)v[i]);
 }
 
 struct MoveArgs {
@@ -49,10 +54,12 @@ __global__ __launch_bounds__(kWaves * kWave) void dispatch_kernel(MoveArgs a)
     for (int64_t it = (int64_t)blockIdx.x * kWaves + wave; it < items; it += (int64_t)gridDim.x * kWaves) {
         const int t = (int)(it / a.pieces), d = ((int)(it % a.pieces) * kWave + lane) * 8;
         const int at = lane < a.k ? a.place[(size_t)t * a.k + lane] : -1;
-        const half8 v = load8(a.in + (size_t)t * a.D + d, a.D - d);
+        if (d >= a.D) continue;
+        const int f = first_of(d, a.D);
+        const half8 v = load8(a.in + (size_t)t * a.D + f, a.D);
         for (int j = 0; j < a.k; ++j) {
             const int r = lane_value(at, j);
-            if ((unsigned)r < (unsigned)a.R) store8(a.out + (size_t)r * a.D + d, v, a.D - d);
+            if ((unsigned)r < (unsigned)a.R) store8(a.out + (size_t)r * a.D + f, v, a.D);
         }
     }
 }
@@ -67,20 +74,30 @@ __global__ __launch_bounds__(kWaves * kWave) void combine_kernel(MoveArgs a)
         const int t = (int)(it / a.pieces), d = ((int)(it % a.pieces) * kWave + lane) * 8;
         const int at = lane < a.k ? a.place[(size_t)t * a.k + lane] : -1;
         const float w = WEIGHTS && lane < a.k ? a.weights[(size_t)t * a.k + lane] : 1.0f;
+        if (d >= a.D) continue;
+        const int f = first_of(d, a.D);
         float acc[8] = {};
-#pragma unroll 4
-        for (int j = 0; j < a.k; ++j) {
-            const int r = lane_value(at, j);
-            if ((unsigned)r >= (unsigned)a.R) continue;
-            const float wj = lane_value(w, j);
-            const half8 v = load8(a.in + (size_t)r * a.D + d, a.D - d);
+        for (int j0 = 0; j0 < a.k; j0 += kTogether) {
+            half8 v[kTogether];
+            int r[kTogether];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] = WEIGHTS ? __builtin_fmaf(wj, (float)v[i], acc[i]) : acc[i] + (float)v[i];
+            for (int u = 0; u < kTogether; ++u) {
+                r[u] = lane_value(at, min(j0 + u, kMaxTop - 1));
+                if ((unsigned)r[u] < (unsigned)a.R) v[u] = load8(a.in + (size_t)r[u] * a.D + f, a.D);
+            }
+#pragma unroll
+            for (int u = 0; u < kTogether; ++u) {
+                if ((unsigned)r[u] >= (unsigned)a.R) continue;
+                const float wj = lane_value(w, min(j0 + u, kMaxTop - 1));
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    acc[i] = WEIGHTS ? __builtin_fmaf(wj, (float)v[u][i], acc[i]) : acc[i] + (float)v[u][i];
+            }
         }
         half8 o;
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] = (_Float16)acc[i];
-        store8(a.out + (size_t)t * a.D + d, o, a.D - d);
+        store8(a.out + (size_t)t * a.D + f, o, a.D);
     }
 }
 
@@ -94,46 +111,62 @@ struct CombineGradArgs {
     int T, k, R, D;
 };
 
-// A workgroup takes a token; its waves share the row's width, and their parts of
-// the dot products are added in wave order.
+// PER waves take a token and share the row's width; their parts of the dot products
+// are added in wave order.
+template <int PER>
 __global__ __launch_bounds__(kWaves * kWave) void combine_grad_kernel(CombineGradArgs a)
 {
     __shared__ float parts[kWaves][kMaxTop];
+    constexpr int TOKENS = kWaves / PER;
     const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+    const int sub = wave % PER;
+    for (int t0 = blockIdx.x * TOKENS; t0 < a.T; t0 += gridDim.x * TOKENS) {
+        const int t = t0 + wave / PER;
         const size_t row = (size_t)t * a.k;
-        const int at = lane < a.k ? a.place[row + lane] : -1;
-        const float w = lane < a.k ? a.weights[row + lane] : 0.0f;
+        const bool mine = t < a.T && lane < a.k;
+        const int at = mine ? a.place[row + lane] : -1;
+        const float w = mine ? a.weights[row + lane] : 0.0f;
         float dot = 0.0f;                        // lane j: this wave's part of choice j's
-        for (int d0 = wave * kWave * 8; d0 < a.D; d0 += kWaves * kWave * 8) {
-            const int d = d0 + lane * 8, n = a.D - d;
-            const half8 g = load8(a.dY + (size_t)t * a.D + d, n);
-            for (int j = 0; j < a.k; ++j) {
-                const int r = lane_value(at, j);
-                if ((unsigned)r >= (unsigned)a.R) continue;
-                const float wj = lane_value(w, j);
-                const half8 c = load8(a.C + (size_t)r * a.D + d, n);
-                half8 o;
-                float s = 0.0f;
+        for (int d0 = sub * kWave * 8; t < a.T && d0 < a.D; d0 += PER * kWave * 8) {
+            const int d = d0 + lane * 8, f = first_of(d, a.D);
+            const bool in = d < a.D;
+            const half8 g = in ? load8(a.dY + (size_t)t * a.D + f, a.D) : half8{};
+            for (int j0 = 0; j0 < a.k; j0 += kTogether) {
+                half8 c[kTogether];
+                int r[kTogether];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    o[i] = (_Float16)(wj * (float)g[i]);
-                    s = __builtin_fmaf((float)g[i], (float)c[i], s);
+                for (int u = 0; u < kTogether; ++u) {
+                    r[u] = lane_value(at, min(j0 + u, kMaxTop - 1));
+                    if (j0 + u >= a.k || (unsigned)r[u] >= (unsigned)a.R) r[u] = -1;
+                    c[u] = half8{};
+                    if (r[u] >= 0 && in) c[u] = load8(a.C + (size_t)r[u] * a.D + f, a.D);
                 }
-                store8(a.dC + (size_t)r * a.D + d, o, n);
-                s = wave_sum(s);
-                if (lane == j) dot += s;
+#pragma unroll
+                for (int u = 0; u < kTogether; ++u) {
+                    if (r[u] < 0) continue;
+                    const float wj = lane_value(w, j0 + u);
+                    half8 o;
+                    float s = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        o[i] = (_Float16)(wj * (float)g[i]);
+                        if (f + i >= d) s = __builtin_fmaf((float)g[i], (float)c[u][i], s);   // once where 8 overlap the 8 before
+                    }
+                    if (in) store8(a.dC + (size_t)r[u] * a.D + f, o, a.D);
+                    s = wave_sum(s);
+                    if (lane == j0 + u) dot += s;
+                }
             }
         }
-        parts[wave][lane] = dot;
-        __syncthreads();
-        if (wave == 0 && lane < a.k) {
-            float s = 0.0f;
+        if constexpr (PER > 1) {
+            parts[wave][lane] = dot;
+            __syncthreads();
+            if (sub == 0)
 #pragma unroll
-            for (int v = 0; v < kWaves; ++v) s += parts[v][lane];
-            a.dweights[row + lane] = s;
+                for (int v = 1; v < PER; ++v) dot += parts[wave + v][lane];
+            __syncthreads();
         }
-        __syncthreads();
+        if (sub == 0 && mine) a.dweights[row + lane] = dot;
     }
 }
 
@@ -202,8 +235,16 @@ int combine_f16_bwd(const void* dY, const void* C, const int* place, const float
     a.dY = (const uint16_t*)dY; a.C = (const uint16_t*)C; a.place = place; a.weights = weights;
     a.dC = (uint16_t*)dC; a.dweights = dweights;
     a.T = T; a.k = k; a.R = R; a.D = D;
-    hipLaunchKernelGGL(combine_grad_kernel, dim3(T < kGrid ? T : kGrid), dim3(kWaves * kWave), 0, (hipStream_t)stream, a);
-    return status(hipGetLastError());
+    const auto launch = [&](auto per) {
+        constexpr int PER = decltype(per)::value;
+        const int groups = ceil_div(T, kWaves / PER);
+        hipLaunchKernelGGL(combine_grad_kernel<PER>, dim3(groups < kGrid ? groups : kGrid), dim3(kWaves * kWave), 0,
+                           (hipStream_t)stream, a);
+        return status(hipGetLastError());
+    };
+    if (D <= 512) return launch(std::integral_constant<int, 1>{});
+    if (D <= 1024) return launch(std::integral_constant<int, 2>{});
+    return launch(std::integral_constant<int, 4>{});
 }
 
 }  // extern "C"
