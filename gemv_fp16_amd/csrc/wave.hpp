@@ -59,6 +59,16 @@ __device__ __forceinline__ T wave_reduce(T v, T id, Op op)
     return lane_value(v, kWave - 1);
 }
 
+// The same within each row of 16 lanes, where every lane gets its row's result.
+template <class T, class Op>
+__device__ __forceinline__ T row_reduce(T v, T id, Op op)
+{
+    v = op(v, dpp_move<0xB1, 0xF>(id, v));
+    v = op(v, dpp_move<0x4E, 0xF>(id, v));
+    v = op(v, dpp_move<0x141, 0xF>(id, v));
+    return op(v, dpp_move<0x140, 0xF>(id, v));
+}
+
 // A NaN loses to any number.
 __device__ __forceinline__ float wave_max(float v)
 {
@@ -76,14 +86,16 @@ __device__ __forceinline__ T wave_sum(T v)
     return wave_reduce(v, T(0), [](T a, T b) { return a + b; });
 }
 
-// Inclusive sums over the lanes.
-__device__ __forceinline__ int wave_scan(int v, int lane)
+// Inclusive sums over the lanes (every lane active): within the rows of 16, then rows
+// 0, 2 into 1, 3, and the first two into the others.
+__device__ __forceinline__ int wave_scan(int v)
 {
-#pragma unroll
-    for (int d = 1; d < kWave; d *= 2) {
-        const int u = __shfl_up(v, d);
-        if (lane >= d) v += u;
-    }
+    v += dpp_move<0x111, 0xF>(0, v);           // from the lane 1 below, 2, 4, 8
+    v += dpp_move<0x112, 0xF>(0, v);
+    v += dpp_move<0x114, 0xF>(0, v);
+    v += dpp_move<0x118, 0xF>(0, v);
+    v += dpp_move<0x142, 0xA>(0, v);
+    v += dpp_move<0x143, 0xC>(0, v);
     return v;
 }
 

@@ -32,6 +32,9 @@ def cfg(score=0, renorm=1, groups=1, top_groups=1, group_best=1, scale=1.0):
 
 
 def test_route_topk_refusals(L):
+    need = L.route_workspace_bytes(65, 8, 2)
+    assert need > 0
+
     def f(x=P, f32=0, bias=NULL, T=4, E=8, k=2, c=cfg(), ids=P, w=P, off=P, at=P, ws=P, n=1 << 20):
         return L.route_topk(x, f32, bias, T, E, k, c, ids, w, off, at, ws, n, NULL)
     for bad in (dict(T=-1), dict(E=0), dict(E=-8), dict(k=0), dict(k=-1), dict(k=9), dict(f32=2), dict(f32=-1),
@@ -42,11 +45,11 @@ def test_route_topk_refusals(L):
                 dict(c=cfg(groups=8), k=2), dict(E=65 * 2, c=cfg(groups=65)), dict(c=cfg(scale=float("nan"))),
                 dict(x=ODD), dict(x=TWO, f32=1), dict(x=NULL), dict(bias=TWO), dict(ids=NULL), dict(ids=TWO), dict(w=NULL),
                 dict(w=TWO), dict(off=NULL), dict(at=NULL), dict(off=TWO), dict(at=TWO), dict(T=65, ws=NULL),
-                dict(T=65, ws=TWO), dict(T=65, n=256 * 8 * 4 - 1)):
+                dict(T=65, ws=TWO), dict(T=65, n=need - 1)):
         assert f(**bad) == BAD, bad
     assert f(T=0, x=NULL, ids=NULL, w=NULL, off=NULL, at=NULL, ws=NULL, n=0) == OK
-    assert L.route_workspace_bytes(64, 8, 2) == 0
-    assert L.route_workspace_bytes(65, 8, 2) == 256 * 8 * 4
+    assert L.route_workspace_bytes(16, 8, 2) == 0
+    assert L.route_workspace_bytes(2 ** 30, 1, 1) >= 2 ** 30 // 65535 * 2      # no chunk past 16 bits
     assert L.route_workspace_bytes(-1, 8, 2) == 0
 
 
