@@ -46,8 +46,6 @@ struct GemmArgs {
     int slices;         // split-K slices (set by launch_gemm); the grid is (tiles, slices)
     static constexpr bool PER_GROUP = false;   // one product
     static constexpr bool LOW_RANK = false;    // nothing is added to it
-    struct Nothing {};
-    template <class MF, int MT, int KS, int FM, int FN> using Low = Nothing;
 };
 
 // 16 zero bytes: the source of direct-to-LDS chunks that lie beyond K.
@@ -916,24 +914,25 @@ __global__ __launch_bounds__(Cfg::NT) void gemm_nt_kernel(Args a)
         lds_barrier();                           // operand buffers are free now
         constexpr int LDW = Cfg::WTN + Cfg::EPAD;  // fp16 per LDS row
         GF_LDS uint16_t* reg = (GF_LDS uint16_t*)(smem + wave * (Cfg::WTM * LDW * 2));
-        [[maybe_unused]] typename Args::template Low<MF, MT, Cfg::KS, Cfg::FM, Cfg::FN> low;
-        if constexpr (Args::LOW_RANK) low.init(a.low, wrow0, wcol0, a.M, a.N);
+        // Adapters' sums, two blocks at a time: more beside 256 accumulators do not fit
+        // the registers.
+        constexpr int FB = Cfg::FN < 2 ? 1 : 2;
         static_for<Cfg::FM>([&](auto fm_c) {
             constexpr int fm = decltype(fm_c)::value;
-            [[maybe_unused]] acc_t add[2];
+            [[maybe_unused]] acc_t add[FB];
             static_for<Cfg::FN>([&](auto fn_c) {
                 constexpr int fn = decltype(fn_c)::value;
                 if constexpr (Args::LOW_RANK) {
-                    constexpr int FB = std::remove_reference_t<decltype(low)>::FB;
                     if constexpr (fn % FB == 0)
-                        low.template sums<fm, fn>(a.low, (acc_t(&)[FB])add, wrow0, wcol0, a.M, a.N);
+                        a.low.template block<MF, MT, Cfg::KS, FB, Cfg::FM * Cfg::FN == 1 ? 8 : 4, 4>(
+                            add, wrow0 + fm * MT, wcol0 + fn * MT, a.M, a.N);
                 }
 #pragma unroll
                 for (int i = 0; i < MF::NACC; ++i) {
                     const int r = fm * MT + MF::row(i, lane);
                     const int c = fn * MT + lane % MT;
                     float v = acc[fm][fn][i];
-                    if constexpr (Args::LOW_RANK) v += add[fn % std::remove_reference_t<decltype(low)>::FB][i];
+                    if constexpr (Args::LOW_RANK) v += add[fn % FB][i];
                     reg[r * LDW + c] = f32_to_f16_bits(v);
                 }
             });

@@ -29,7 +29,26 @@ int parts_of(int M, int K, int r)
     return s < 1 ? 1 : (s > most ? most : s);
 }
 
-size_t workspace_need(int M, int K, int r) { return (size_t)parts_of(M, K, r) * M * r * sizeof(float); }
+// The form in slices of K: from 3 to 32 rows, of 4 to 8 slices of K, up to 8192 columns;
+// 0 elsewhere.  32 rows of 8 adapters, rank 16: 12.2 us at 1024 x 4096 (streaming 19.8),
+// 17.1 at 4096 x 4096 (21.7), 25.3 at 8192 x 4096 (26.3), 12.8 at 4096 x 2048 (16.2); but
+// 32.5 at 11008 x 4096 (29.9), 12.0 at 4096 x 512 (11.8).  3 rows of one adapter: 8.9 us
+// at 1024 x 4096 (12.8), 9.4 at 4096 x 2048 (10.0), 8.9 at 4096 x 1024 (7.6).  16 rows of
+// 8192 x 8192, 16 slices: 40.6 (37.5).
+constexpr int kSliceColumns = 8192;
+int slices_of(int M, int N, int K)
+{
+    const int s = ceil_div(K, kLoraSlice);
+    return M > 2 && M <= 32 && N >= 16 && N <= kSliceColumns && s >= 4 && s <= kLoraSlices ? s : 0;
+}
+
+// Floats of the base's parts, H's parts behind them 16-byte aligned.
+size_t base_floats(int M, int N, int K) { return ((size_t)slices_of(M, N, K) * M * N + 3) / 4 * 4; }
+size_t workspace_need(int M, int N, int K, int r)
+{
+    const int s = slices_of(M, N, K), p = parts_of(M, K, r);
+    return (base_floats(M, N, K) + (size_t)(s > p ? s : p) * M * r) * sizeof(float);
+}
 
 int check(const void* A, const int* ids, const void* Down, const void* Up, const float* scales, const void* C, int M,
           int N, int K, int r, int L, const void* workspace, size_t workspace_bytes)
@@ -45,7 +64,7 @@ int check(const void* A, const int* ids, const void* Down, const void* Up, const
     if (K > 0 && off_grid(A, 2)) return GF_ERR_INVALID_ARG;
     if (L > 0 && (off_grid(Up, 2) || (K > 0 && off_grid(Down, 2)))) return GF_ERR_INVALID_ARG;
     if (scales && off_grid(scales, 4)) return GF_ERR_INVALID_ARG;
-    if (off_grid(workspace, 16) || workspace_bytes < workspace_need(M, K, r)) return GF_ERR_INVALID_ARG;
+    if (off_grid(workspace, 16) || workspace_bytes < workspace_need(M, N, K, r)) return GF_ERR_INVALID_ARG;
     return GF_OK;
 }
 
@@ -202,7 +221,7 @@ extern "C" {
 size_t lora_workspace_bytes(int M, int N, int K, int r)
 {
     if (M < 0 || N < 0 || K < 0 || r < 1 || r > kMaxRank) return 0;
-    return workspace_need(M, K, r);
+    return workspace_need(M, N, K, r);
 }
 
 int lora_add_f16(const void* A, const int* ids, const void* Down, const void* Up, const float* scales, void* C, int M,
@@ -228,6 +247,14 @@ int gemm_f16_nt_lora(const void* A, const void* B, const int* ids, const void* D
     if (al && M <= kVecRows) {
         rc = M == 1 ? vec<1>(a, (hipStream_t)stream) : vec<2>(a, (hipStream_t)stream);
         if (rc != GF_ERR_UNSUPPORTED) return rc;
+    }
+    const int slices = slices_of(M, N, K);
+    if (al && slices > 0) {
+        LoraArgs b = a;
+        b.S = slices;
+        b.H = (float*)workspace + base_floats(M, N, K);
+        return status(M <= 16 ? launch_lora_slices<LoraSliceCfg<1, 8>>(b, (float*)workspace, (hipStream_t)stream)
+                              : launch_lora_slices<LoraSliceCfg<2, 6>>(b, (float*)workspace, (hipStream_t)stream));
     }
     if (al && band_takes(M, N, K)) return band(a, (hipStream_t)stream);
     // From 33 to 64 rows the base's own streaming forms and a launch that adds to their

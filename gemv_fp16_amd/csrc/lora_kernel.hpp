@@ -243,8 +243,6 @@ __global__ __launch_bounds__(256) void lora_up_any_kernel(LoraArgs a)
 struct LoraTileArgs : GemmArgs {
     LowRank low;
     static constexpr bool LOW_RANK = true;
-    template <class MF, int MT, int KS, int FM, int FN>
-    using Low = LowRankTile<MF, MT, KS, FM, FN, FM * FN == 4 ? 1 : 2, kLoraTileParts>;   // 128 x 128: two workgroups to a CU
 };
 
 template <class Cfg>
@@ -744,6 +742,204 @@ hipError_t launch_lora_band(const LoraArgs& a, hipStream_t stream)
     if (e != hipSuccess) return e;
     const int blocks = ceil_div(a.N, 16);
     hipLaunchKernelGGL(kern, dim3(blocks < 256 ? blocks : 256), dim3(Cfg::WAVES * kWave), lds, stream, a, te);
+    return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// base and adapters, a decode batch: K in slices
+// ---------------------------------------------------------------------------
+//
+// The streaming form above has every CU read all of A (7 us for 32 rows of 4096, at 40
+// GB/s a CU), and the products by Down are a launch of their own.  Here a workgroup has
+// one slice of 512 k: its part of A (16 KB for 16 rows) in LDS, its waves taking 16-row
+// blocks of B, and 16 ranks of Down at a time like any of them, through a ring of tasks
+// as above.  A slice's sums go to memory, part by part; a second launch adds the parts
+// and the adapters, and rounds once.  The parts are M / 128 of B's bytes, written and
+// read again.  32 rows of 24 adapters at 4096 x 4096, rank 16: 19.0 us, 11.5 of them the
+// first launch (2.9 TB/s) and 6.5 the second, a chain of three loads with 13 adapters
+// for 16 rows; the base alone takes 12, the streaming form with the adapters 22.
+// K % 8 == 0, r % 8 == 0, N >= 16; A, B, Down and Up 16-byte aligned; M <= 16 * MB.
+constexpr int kLoraSlice = 512, kLoraSlices = 8;
+
+template <int MB_, int W_>
+struct LoraSliceCfg {
+    static constexpr int MB = MB_, W = W_, RING = 2, T = 4, SLICE = kLoraSlice, ROWS = 16 * MB, TASK_BYTES = 4096;
+    static constexpr int X_BYTES = ROWS * SLICE * 2, LDS_BYTES = X_BYTES + W * RING * TASK_BYTES;
+    static_assert(SLICE == 128 * T);
+    static_assert(LDS_BYTES <= 80 * 1024, "two workgroups to a CU");
+};
+
+// P: slices x M x N, the base's parts; a.H: slices x M x r, no more slices than
+// kLoraSlices.  hb: blocks of ranks there
+// can be (the launch takes them first), per: blocks a wave, parts: workgroups a slice.
+template <class Cfg>
+__global__ __launch_bounds__(Cfg::W * kWave) void lora_slice_kernel(LoraArgs a, float* P, int hb, int per, int parts)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    constexpr int MB = Cfg::MB, W = Cfg::W, RING = Cfg::RING, T = Cfg::T, L = 4;
+    extern __shared__ __attribute__((aligned(1024))) char smem_raw[];
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int r16 = lane % 16, c4 = lane / 16;
+    const int M = a.M, N = a.N, K = a.K, r = a.r;
+    const int slice = blockIdx.x / parts, part = blockIdx.x % parts, k0 = slice * Cfg::SLICE;
+    GF_LDS char* xs = (GF_LDS char*)smem_raw;                // row m: 64 chunks, c at slot c ^ (m % 16)
+    GF_LDS char* tasks = xs + Cfg::X_BYTES + wave * RING * Cfg::TASK_BYTES;
+    const int id = a.ids[min(lane, M - 1)];
+    for (int m = wave; m < Cfg::ROWS; m += W) {
+        const int k = k0 + (lane ^ (m % 16)) * 8;
+        const void* p = m < M && k < K ? (const void*)(a.A + (size_t)m * K + k) : (const void*)g_zero16;
+        __builtin_amdgcn_global_load_lds(p, (GF_LDS void*)(xs + m * 1024), 16, 0, 0);
+    }
+    const int rb = ceil_div(r, 16), blocks = hb + ceil_div(N, 16);
+    const uint64_t live = __ballot(lane < M && (unsigned)id < (unsigned)a.L);
+    // The rows of the d-th adapter in use, 0 past the last.
+    auto rows_of = [&](int d) __attribute__((always_inline)) {
+        uint64_t left = live, rows = 0;
+        for (int i = 0; i <= d && left; ++i) {
+            rows = left & __ballot(id == __builtin_amdgcn_readlane(id, __builtin_ctzll(left)));
+            left &= ~rows;
+            if (i < d) rows = 0;
+        }
+        return rows;
+    };
+    auto rank0 = [&](int b) __attribute__((always_inline)) { return max(min(b % rb * 16, r - 16), 0); };
+    auto block_of = [&](int i) __attribute__((always_inline)) { return (i * parts + part) * W + wave; };
+
+    const uint16_t* src = nullptr;               // of the block whose tasks are being issued
+    int ii = 0, it = 0, islot = 0, wrap = 15;
+    auto issue = [&]() __attribute__((always_inline)) {
+        if (it == 0) {
+            const int b = ii < per ? block_of(ii) : blocks;
+            src = nullptr;
+            wrap = 15;
+            if (b < hb) {
+                const uint64_t rows = rows_of(b / rb);
+                if (rows) {
+                    src = a.Down + ((size_t)__builtin_amdgcn_readlane(id, __builtin_ctzll(rows)) * r + rank0(b)) * K;
+                    wrap = r < 16 ? 7 : 15;      // rank 8: its ranks are there twice
+                }
+            } else if (b < blocks) {
+                src = a.B + (size_t)min((b - hb) * 16, N - 16) * K;
+            }
+        }
+        GF_LDS char* buf = tasks + islot * Cfg::TASK_BYTES;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = 4 * i + c4, k = k0 + it * 128 + (r16 ^ row) * 8;
+            const void* p = src && k < K ? (const void*)(src + (size_t)(row & wrap) * K + k) : (const void*)g_zero16;
+            __builtin_amdgcn_global_load_lds(p, (GF_LDS void*)(buf + i * 1024), 16, 0, 2);
+        }
+        if (++it == T) { it = 0; ++ii; }
+        if (++islot == RING) islot = 0;
+    };
+    static_for<RING>([&](auto) __attribute__((always_inline)) { issue(); });
+    wait_vmcnt<RING * L>();                      // this wave's rows of A are there
+    lds_barrier();                               // everyone's
+    int slot = 0;
+    for (int i = 0; i < per; ++i) {
+        const int b = block_of(i);
+        floatx4 acc[MB] = {};
+        static_for<T>([&](auto t_c) __attribute__((always_inline)) {
+            constexpr int t = decltype(t_c)::value;
+            wait_vmcnt<(RING - 1) * L>();
+            asm volatile("" ::: "memory");
+            const GF_LDS char* buf = tasks + slot * Cfg::TASK_BYTES;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const half8 w = *(const GF_LDS half8*)(buf + r16 * 256 + (((4 * s + c4) ^ r16) * 16));
+#pragma unroll
+                for (int m = 0; m < MB; ++m) {
+                    const half8 x = *(const GF_LDS half8*)(xs + (16 * m + r16) * 1024 + (((16 * t + 4 * s + c4) ^ r16) * 16));
+                    acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, w, acc[m], 0, 0, 0);
+                }
+            }
+            asm volatile("" ::: "memory");
+            wait_lgkmcnt0();                     // the buffer is read: it may be filled again
+            issue();
+            if (++slot == RING) slot = 0;
+        });
+        if (b >= blocks) break;
+        // accumulator e of lane l: row 4 * (l / 16) + e, column l % 16
+        if (b < hb) {
+            const uint64_t rows = rows_of(b / rb);
+            if (!rows) continue;
+            const int ad = __builtin_amdgcn_readlane(id, __builtin_ctzll(rows));
+            const float scale = a.scales ? scalar_load(a.scales + ad) : 1.0f;
+#pragma unroll
+            for (int m = 0; m < MB; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int row = 16 * m + 4 * c4 + e;
+                    if (((rows >> row) & 1) && r16 < r)
+                        a.H[slice * a.part + (size_t)row * r + rank0(b) + r16] = scale * acc[m][e];
+                }
+        } else {
+            float* out = P + ((size_t)slice * M) * N + min((b - hb) * 16, N - 16) + r16;
+#pragma unroll
+            for (int m = 0; m < MB; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int row = 16 * m + 4 * c4 + e;
+                    if (row < M) out[(size_t)row * N] = acc[m][e];
+                }
+        }
+    }
+    wait_vmcnt<0>();
+#endif
+}
+
+// C = the parts' sum and the adapters: a wave 16 rows by 16 columns.
+__global__ __launch_bounds__(256) void lora_finish_kernel(LoraArgs a, const float* P, int vec)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    const int lane = threadIdx.x % kWave, r16 = lane % 16, c4 = lane / 16;
+    const int across = ceil_div(a.N, 16), down = ceil_div(a.M, 16);
+    const int w = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + threadIdx.x / kWave);
+    if (w >= across * down) return;
+    const int row0 = w / across * 16, col0 = min(w % across * 16, a.N - 16);
+    const int m = row0 + r16;
+    const float* p = P + (size_t)min(m, a.M - 1) * a.N + col0 + 4 * c4;
+    const size_t part = (size_t)a.M * a.N;
+    floatx4 v[kLoraSlices], base = {}, sum[1];   // all parts in flight, added in order
+#pragma unroll
+    for (int s = 0; s < kLoraSlices; ++s) __builtin_memcpy(&v[s], p + min(s, a.S - 1) * part, 16);
+    a.low().template block<SwappedMfma, 16, 32, 1, 16, kLoraSlices>(sum, row0, col0, a.M, a.N);
+#pragma unroll
+    for (int s = 0; s < kLoraSlices; ++s)
+        if (s < a.S) base += v[s];
+    if (m >= a.M) return;
+    uint16_t* c = a.C + (size_t)m * a.N + col0 + 4 * c4;
+    typedef _Float16 half4 __attribute__((ext_vector_type(4)));
+    half4 o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = (_Float16)(base[i] + sum[0][i]);
+    if (vec) {
+        *(half4*)c = o;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = __builtin_bit_cast(uint16_t, (_Float16)o[i]);
+    }
+#endif
+}
+
+template <class Cfg>
+hipError_t launch_lora_slices(const LoraArgs& a, float* P, hipStream_t stream)
+{
+    auto kern = lora_slice_kernel<Cfg>;
+    static std::atomic<uint64_t> lds_opt_in{0};
+    hipError_t e = opt_in_lds((const void*)kern, Cfg::LDS_BYTES, lds_opt_in, stream);
+    if (e != hipSuccess) return e;
+    const int most = a.M < a.L ? a.M : a.L, hb = most * ceil_div(a.r, 16), blocks = hb + ceil_div(a.N, 16);
+    // about two workgroups to a CU, each wave with the same number of blocks
+    int per = (int)((int64_t)blocks * a.S / (512 * Cfg::W));
+    if (per < 1) per = 1;
+    const int parts = ceil_div(blocks, Cfg::W * per);
+    hipLaunchKernelGGL(kern, dim3(parts * a.S), dim3(Cfg::W * kWave), Cfg::LDS_BYTES, stream, a, P, hb, per, parts);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int waves = ceil_div(a.M, 16) * ceil_div(a.N, 16);
+    const int vec = (reinterpret_cast<uintptr_t>(a.C) & 7) == 0 && a.N % 4 == 0;
+    hipLaunchKernelGGL(lora_finish_kernel, dim3(ceil_div(waves, 4)), dim3(256), 0, stream, a, P, vec);
     return hipGetLastError();
 }
 

@@ -523,10 +523,10 @@ int combine_f16_bwd(const void* dY, const void* C, const int* place, const float
  * fp32 accumulation; the scaled products by Down stay in fp32 (for the matrix cores as
  * two fp16 each, 22 bits together: one past fp16's range becomes an infinity there).
  * One rounding at the end, but where the base is stored first and the adapters are
- * added to it: in lora_add_f16, from 33 to 64 rows, and in the general forms.  An
- * infinity or a NaN in an adapter reaches the rows that have it and no others.
- * Ranks 1 <= r <= 256; K % 8 == 0, r % 8 == 0 and 16-byte
- * aligned operands are fastest, everything else runs a general form.  The
+ * added to it: in lora_add_f16, from 33 to 64 rows, at fewer of a long K (past 8192, from
+ * 17 rows 4096), and in the general forms.  An infinity or a NaN in an adapter reaches
+ * the rows that have it and no others.  Ranks 1 <= r <= 256; K % 8 == 0, r % 8 == 0 and
+ * 16-byte aligned operands are fastest, everything else runs a general form.  The
  * adapters as a whole may pass 2^31 elements, one adapter's part and every other
  * operand may not; no size above 2^30.  workspace: caller-owned device memory, 16-byte
  * aligned, of at least lora_workspace_bytes(M, N, K, r) bytes.  M == 0 or N == 0 is a

@@ -103,7 +103,11 @@ CASES = [(1, 16, 64, 8, 1, "one"), (1, 1, 8, 1, 1, "one"), (1, 520, 1024, 16, 8,
          (65, 136, 520, 8, 3, "runs"), (100, 300, 128, 256, 2, "mixed"), (130, 256, 512, 16, 6, "runs"),
          (300, 520, 264, 24, 9, "stray"), (520, 264, 1032, 64, 4, "runs"), (700, 384, 256, 16, 500, "mixed"),
          (40, 64, 96, 8, 3, "none"), (8, 48, 0, 8, 2, "mixed"), (1100, 2064, 264, 16, 5, "runs"), (12, 40, 512, 5, 0, "one"),
-         (24, 4096, 72, 128, 7, "stray"), (200, 131, 1001, 7, 4, "stray")]
+         (24, 4096, 72, 128, 7, "stray"), (200, 131, 1001, 7, 4, "stray"),
+         # 3 to 32 rows, K in slices: ends inside one, ranks past a block, its bounds
+         (3, 16, 1544, 8, 2, "mixed"), (16, 1000, 3976, 24, 7, "stray"), (17, 263, 4096, 40, 20, "mixed"),
+         (32, 8192, 2048, 16, 1, "one"), (32, 8200, 2056, 16, 3, "runs"), (31, 130, 4104, 16, 4, "mixed"),
+         (5, 19, 2048, 256, 4, "none"), (9, 15, 2048, 16, 4, "mixed"), (32, 520, 1536, 16, 32, "mixed")]
 
 
 @pytest.mark.parametrize("M,N,K,r,L,kind", CASES)
@@ -133,8 +137,8 @@ def test_lora_add(M, N, K, r, L, kind):
 
 def test_rows_without_an_adapter_are_the_plain_product():
     """NaN and infinity in adapters that no row has, and in rows that have none, stay there."""
-    for M in (3, 40, 300):
-        p = Problem(M, 264, 512, 16, 4, "stray", M)
+    for M, K in ((3, 512), (11, 2048), (40, 512), (300, 512)):
+        p = Problem(M, 264, K, 16, 4, "stray", M)
         p.ids[p.ids == 2] = -1
         p.Down[2], p.Up[2] = np.nan, np.inf
         row = int(np.flatnonzero((p.ids < 0) | (p.ids >= 4))[0])
@@ -151,18 +155,19 @@ def test_rows_without_an_adapter_are_the_plain_product():
         p.check(C, base, size, "finite rows")
 
 
-@pytest.mark.parametrize("M", [2, 12, 30, 50, 100, 300, 600])
+@pytest.mark.parametrize("M,K", [(2, 1024), (12, 1024), (12, 2048), (30, 1024), (30, 2048), (50, 1024), (100, 1024),
+                                 (300, 1024), (600, 1024)])
 @pytest.mark.parametrize("bad", [np.nan, np.inf])
-def test_an_adapter_that_is_not_finite_stays_in_its_rows(M, bad):
+def test_an_adapter_that_is_not_finite_stays_in_its_rows(M, K, bad):
     """NaN and infinity in one adapter reach the rows that have it and no others, whichever share a tile with them."""
     for add in (False, True):
-        p = Problem(M, 520, 1024, 16, 4, "mixed", M + 1)
+        p = Problem(M, 520, K, 16, 4, "mixed", M + 1)
         p.ids[:] = np.random.default_rng(M).choice([0, 2, 3, -1], M)
         p.ids[M // 2] = 1
         p.Up[1, ::3, 5] = bad
         p.Down[1, 7, 9] = bad
         (A, B), ids, (Down, Up), scales = p.operands()
-        _say("lora not finite", M, bad, add)
+        _say("lora not finite", M, K, bad, add)
         if add:
             C = gf.lora_add_f16(A, ids, Down, Up, dev(p.C0), scales)
             base, size = p.C0.astype(np.float64), np.abs(p.C0.astype(np.float64))
@@ -205,17 +210,17 @@ def test_adapters_past_2_31_elements():
 
 
 def test_results_repeat_on_streams_and_in_graphs():
-    """Two graphs replayed in turn, each with a workspace of its own, a side
+    """Graphs replayed in turn, each with a workspace of its own, a side
     stream and a workspace that held something else: the same bits."""
     graphs, held, problems = [], [], []
-    for M, kind in ((24, "mixed"), (200, "runs")):
-        p = Problem(M, 520, 1024, 16, 6, kind, M)
+    for M, K, kind in ((24, 1024, "mixed"), (20, 2048, "mixed"), (200, 1024, "runs")):
+        p = Problem(M, 520, K, 16, 6, kind, M)
         ops = p.operands()
         (A, B), ids, (Down, Up), scales = ops
         want = gf.gemm_f16_nt_lora(A, B, ids, Down, Up, scales)
         side = torch.cuda.Stream()
         torch.cuda.synchronize()
-        need = gf.lora_workspace_bytes(M, 520, 1024, 16)
+        need = gf.lora_workspace_bytes(M, 520, K, 16)
         ws = torch.full((need + 64,), 255, dtype=torch.uint8, device="cuda")
         torch.cuda.synchronize()
         again = gf.gemm_f16_nt_lora(A, B, ids, Down, Up, scales, workspace=ws, stream=side)
