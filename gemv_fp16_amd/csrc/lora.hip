@@ -111,11 +111,17 @@ int up(const LoraArgs& a, hipStream_t stream)
 {
     if (on16(a.Up) && a.r % 8 == 0) {
         const int vec = (reinterpret_cast<uintptr_t>(a.C) & 7) == 0 && a.N % 4 == 0;
-        const int64_t waves = (int64_t)ceil_div(a.M, 16) * ceil_div(a.N, 16);
-        if (waves <= 8192)
-            hipLaunchKernelGGL(lora_up_kernel<1>, dim3(grid_of((waves + 3) / 4)), dim3(256), 0, stream, a, vec);
+        const int64_t items = (int64_t)ceil_div(a.M, 16) * ceil_div(a.N, 16);
+        if (items > 8192 && a.S <= kLoraTileParts)
+            hipLaunchKernelGGL(lora_up_kernel<kLoraTileParts>, dim3(grid_of((items / 4 + 3) / 4)), dim3(256), 0, stream, a, vec);
+        else if (items > 8192)
+            hipLaunchKernelGGL(lora_up_kernel<kLoraParts>, dim3(grid_of((items / 4 + 3) / 4)), dim3(256), 0, stream, a, vec);
+        else if (a.r <= 32)
+            hipLaunchKernelGGL(lora_up_few_kernel<1>, dim3((int)(items + 3) / 4), dim3(256), 0, stream, a, vec);
+        else if (a.r <= 64)
+            hipLaunchKernelGGL(lora_up_few_kernel<2>, dim3((int)(items + 1) / 2), dim3(256), 0, stream, a, vec);
         else
-            hipLaunchKernelGGL(lora_up_kernel<4>, dim3(grid_of((waves / 4 + 3) / 4)), dim3(256), 0, stream, a, vec);
+            hipLaunchKernelGGL(lora_up_few_kernel<4>, dim3((int)items), dim3(256), 0, stream, a, vec);
     } else {
         hipLaunchKernelGGL(lora_up_any_kernel, dim3(grid_of(((int64_t)a.M * a.N + 255) / 256)), dim3(256), 0, stream, a);
     }

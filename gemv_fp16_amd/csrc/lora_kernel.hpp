@@ -173,8 +173,10 @@ __global__ __launch_bounds__(256) void lora_down_any_kernel(LoraArgs a)
 // H . Up[a]^T added to C
 // ---------------------------------------------------------------------------
 //
-// A wave takes 16 rows and 16 * NB columns.  The operands are swapped (Up's rows in
-// the place of A's), so that a lane holds four neighbouring columns of one row.
+// The operands are swapped (Up's rows in the place of A's), so that a lane holds four
+// neighbouring columns of one row.  C is asked for before the sums are worked out, which
+// takes a chain of loads out of it (lora_add_f16, 2048 rows of 8 adapters, rank 64, at
+// 4096 x 4096: 43.4 us, was 57.5; rank 16 22.7, was 25.8; a copy of C takes 6.5).
 struct SwappedMfma {
     typedef floatx4 acc_t;
     static constexpr int NACC = 4;
@@ -185,10 +187,64 @@ struct SwappedMfma {
     static __device__ __forceinline__ int row(int, int lane) { return lane % 16; }
 };
 
-template <int NB>
-__global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a, int vec)
+// The adapters' sums of a wave's 16 rows and 16 columns, J waves to a block: each has
+// 32 ranks in turn, and the first adds what the others found, in order.  True for the
+// waves that have the sums.  All of a wave's adapters have their loads in flight: each
+// round of them is a chain of 3 us.  (lora_add_f16, 32 rows of 32 adapters, rank 64, at
+// 8192 x 4096: 23.7 us, with one wave to a block and 8 adapters at a time 27.0.)
+template <int J, int SP>
+__device__ __forceinline__ bool lora_join(const LowRank& low, floatx4 (&sum)[1], int row0, int col0, int M, int N)
+{
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, j = wave % J;
+    low.template block<SwappedMfma, 16, 32, 1, 16, SP>(sum, row0, col0, M, N, 32 * j, 32 * J);
+    if constexpr (J > 1) {
+        __shared__ floatx4 part[4][kWave];
+        part[wave][lane] = sum[0];
+        __syncthreads();
+        if (j > 0) return false;
+#pragma unroll
+        for (int i = 1; i < J; ++i) sum[0] += part[wave + i][lane];
+    }
+    return true;
+}
+
+// 16 rows by 16 columns, J waves each.
+template <int J>
+__global__ __launch_bounds__(256) void lora_up_few_kernel(LoraArgs a, int vec)
 {
 #if defined(__HIP_DEVICE_COMPILE__)
+    const int lane = threadIdx.x % kWave, r16 = lane % 16, c4 = lane / 16;
+    const int across = ceil_div(a.N, 16), items = across * ceil_div(a.M, 16);
+    const LowRank low = a.low();
+    const int w = __builtin_amdgcn_readfirstlane(min((int)(blockIdx.x * 4 + threadIdx.x / kWave) / J, items - 1));
+    const int row0 = w / across * 16, col0 = w % across * 16, m = row0 + r16, n = col0 + 4 * c4;
+    uint16_t* c = a.C + (size_t)min(m, a.M - 1) * a.N + n;
+    const bool four = vec && n + 4 <= a.N;
+    typedef _Float16 half4 __attribute__((ext_vector_type(4)));
+    half4 v = {};
+    if (four) v = *(const half4*)c;              // asked for before the sums are worked out
+    floatx4 sum[1];
+    if (!lora_join<J, kLoraParts>(low, sum, row0, col0, a.M, a.N)) return;
+    if ((int)(blockIdx.x * 4 + threadIdx.x / kWave) / J >= items || m >= a.M || low.adapter(m, a.M) < 0) return;
+    if (four) {
+        half4 o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = (_Float16)((float)v[i] + sum[0][i]);
+        *(half4*)c = o;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n + i < a.N) c[i] = f32_to_f16_bits(f16_bits_to_f32(c[i]) + sum[0][i]);
+    }
+#endif
+}
+
+// 16 rows by 64 columns a wave, S <= SP.
+template <int SP>
+__global__ __launch_bounds__(256, SP > 4 ? 3 : 4) void lora_up_kernel(LoraArgs a, int vec)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    constexpr int NB = 4;
     const int lane = threadIdx.x % kWave, r16 = lane % 16, c4 = lane / 16;
     const int across = ceil_div(a.N, 16 * NB), down = ceil_div(a.M, 16);
     const LowRank low = a.low();
@@ -196,20 +252,26 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a, int vec)
     for (int64_t w = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave; w < items; w += (int64_t)gridDim.x * 4) {
         const int row0 = __builtin_amdgcn_readfirstlane((int)(w / across) * 16);
         const int col0 = __builtin_amdgcn_readfirstlane((int)(w % across) * 16 * NB);
-        floatx4 sum[NB];
-        low.template block<SwappedMfma, 16, 32, NB, NB == 1 ? 8 : 2, kLoraParts>(sum, row0, col0, a.M, a.N);
         const int m = row0 + r16;
+        typedef _Float16 half4 __attribute__((ext_vector_type(4)));
+        half4 v[NB];                             // asked for before the sums are worked out
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const int n = col0 + 16 * b + 4 * c4;
+            v[b] = half4{};
+            if (vec && n + 4 <= a.N) v[b] = *(const half4*)(a.C + (size_t)min(m, a.M - 1) * a.N + n);
+        }
+        floatx4 sum[NB];
+        low.template block<SwappedMfma, 16, 32, NB, 2, SP>(sum, row0, col0, a.M, a.N);
         if (m >= a.M || low.adapter(m, a.M) < 0) continue;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             const int n = col0 + 16 * b + 4 * c4;
             uint16_t* c = a.C + (size_t)m * a.N + n;
-            typedef _Float16 half4 __attribute__((ext_vector_type(4)));
             if (vec && n + 4 <= a.N) {
-                const half4 v = *(const half4*)c;
                 half4 o;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) o[i] = (_Float16)((float)v[i] + sum[b][i]);
+                for (int i = 0; i < 4; ++i) o[i] = (_Float16)((float)v[b][i] + sum[b][i]);
                 *(half4*)c = o;
             } else {
 #pragma unroll
@@ -755,8 +817,8 @@ hipError_t launch_lora_band(const LoraArgs& a, hipStream_t stream)
 // blocks of B, and 16 ranks of Down at a time like any of them, through a ring of tasks
 // as above.  A slice's sums go to memory, part by part; a second launch adds the parts
 // and the adapters, and rounds once.  The parts are M / 128 of B's bytes, written and
-// read again.  32 rows of 24 adapters at 4096 x 4096, rank 16: 19.0 us, 11.5 of them the
-// first launch (2.9 TB/s) and 6.5 the second, a chain of three loads with 13 adapters
+// read again.  32 rows of 24 adapters at 4096 x 4096, rank 16: 18.4 us, 11.5 of them the
+// first launch (2.9 TB/s) and 6 the second, a chain of three loads with 13 adapters
 // for 16 rows; the base alone takes 12, the streaming form with the adapters 22.
 // K % 8 == 0, r % 8 == 0, N >= 16; A, B, Down and Up 16-byte aligned; M <= 16 * MB.
 constexpr int kLoraSlice = 512, kLoraSlices = 8;
@@ -888,26 +950,28 @@ __global__ __launch_bounds__(Cfg::W * kWave) void lora_slice_kernel(LoraArgs a, 
 #endif
 }
 
-// C = the parts' sum and the adapters: a wave 16 rows by 16 columns.
+// C = the parts' sum and the adapters: 16 rows by 16 columns, J waves each.
+template <int J>
 __global__ __launch_bounds__(256) void lora_finish_kernel(LoraArgs a, const float* P, int vec)
 {
 #if defined(__HIP_DEVICE_COMPILE__)
     const int lane = threadIdx.x % kWave, r16 = lane % 16, c4 = lane / 16;
     const int across = ceil_div(a.N, 16), down = ceil_div(a.M, 16);
-    const int w = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + threadIdx.x / kWave);
-    if (w >= across * down) return;
+    const int nth = (int)(blockIdx.x * 4 + threadIdx.x / kWave) / J;
+    const int w = __builtin_amdgcn_readfirstlane(min(nth, across * down - 1));
     const int row0 = w / across * 16, col0 = min(w % across * 16, a.N - 16);
     const int m = row0 + r16;
     const float* p = P + (size_t)min(m, a.M - 1) * a.N + col0 + 4 * c4;
     const size_t part = (size_t)a.M * a.N;
     floatx4 v[kLoraSlices], base = {}, sum[1];   // all parts in flight, added in order
 #pragma unroll
-    for (int s = 0; s < kLoraSlices; ++s) __builtin_memcpy(&v[s], p + min(s, a.S - 1) * part, 16);
-    a.low().template block<SwappedMfma, 16, 32, 1, 16, kLoraSlices>(sum, row0, col0, a.M, a.N);
+    for (int s = 0; s < kLoraSlices; ++s)
+        if (threadIdx.x / kWave % J == 0) __builtin_memcpy(&v[s], p + min(s, a.S - 1) * part, 16);
+    if (!lora_join<J, kLoraSlices>(a.low(), sum, row0, col0, a.M, a.N)) return;
 #pragma unroll
     for (int s = 0; s < kLoraSlices; ++s)
         if (s < a.S) base += v[s];
-    if (m >= a.M) return;
+    if (nth >= across * down || m >= a.M) return;
     uint16_t* c = a.C + (size_t)m * a.N + col0 + 4 * c4;
     typedef _Float16 half4 __attribute__((ext_vector_type(4)));
     half4 o;
@@ -937,9 +1001,14 @@ hipError_t launch_lora_slices(const LoraArgs& a, float* P, hipStream_t stream)
     hipLaunchKernelGGL(kern, dim3(parts * a.S), dim3(Cfg::W * kWave), Cfg::LDS_BYTES, stream, a, P, hb, per, parts);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int waves = ceil_div(a.M, 16) * ceil_div(a.N, 16);
+    const int items = ceil_div(a.M, 16) * ceil_div(a.N, 16);
     const int vec = (reinterpret_cast<uintptr_t>(a.C) & 7) == 0 && a.N % 4 == 0;
-    hipLaunchKernelGGL(lora_finish_kernel, dim3(ceil_div(waves, 4)), dim3(256), 0, stream, a, P, vec);
+    if (a.r <= 32)
+        hipLaunchKernelGGL(lora_finish_kernel<1>, dim3(ceil_div(items, 4)), dim3(256), 0, stream, a, P, vec);
+    else if (a.r <= 64)
+        hipLaunchKernelGGL(lora_finish_kernel<2>, dim3(ceil_div(items, 2)), dim3(256), 0, stream, a, P, vec);
+    else
+        hipLaunchKernelGGL(lora_finish_kernel<4>, dim3(items), dim3(256), 0, stream, a, P, vec);
     return hipGetLastError();
 }
 

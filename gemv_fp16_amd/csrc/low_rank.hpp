@@ -63,7 +63,8 @@ struct LowRank {
     // adapters, NA at a time, so that many have their loads in flight together.  All
     // lanes.
     template <class MF, int MT, int KS, int FN, int NA, int SP>
-    __device__ __forceinline__ void block(typename MF::acc_t (&sum)[FN], int row0, int col0, int M, int N) const
+    __device__ __forceinline__ void block(typename MF::acc_t (&sum)[FN], int row0, int col0, int M, int N,
+                                          int from = 0, int step = KS) const
     {
         const int lane = threadIdx.x % kWave, l = lane % MT, kq = lane / MT * 8;
         const int id = adapter(row0 + l, M), first = __builtin_amdgcn_readfirstlane(id);
@@ -73,7 +74,7 @@ struct LowRank {
         for (int g = 0; g < FN; ++g) sum[g] = typename MF::acc_t{};
         if (one && first >= 0) {
             const uint16_t* up = Up + (size_t)first * N * r;
-            for (int k0 = 0; k0 < r; k0 += KS) {
+            for (int k0 = from; k0 < r; k0 += step) {
                 const int k = min(k0 + kq, r - 8);
                 half8 hi, lo, u[FN];
 #pragma unroll
@@ -89,7 +90,7 @@ struct LowRank {
         } else if (!one) {
 #pragma unroll
             for (int g = 0; g < FN; ++g)
-                for (int k0 = 0; k0 < r; k0 += KS) {
+                for (int k0 = from; k0 < r; k0 += step) {
                     const int k = min(k0 + kq, r - 8), col = min(col0 + g * MT + l, N - 1);
                     const bool in = k0 + kq < r;
                     half8 hi, lo;
