@@ -23,6 +23,12 @@ Ops (inputs are the seeded uniform[-1,1] fp16 workloads):
           4096 x 2048 and of 2999 over 32 of 1024 x 2048 (the one of the weights in fp32 and in
           fp16), and with 4-bit weights 24 rows over 16
           of 4096 x 4096 and 1111 over 8 of 2048 x 4096 (weights of the small ones: 3 copies)
+  route   routing to experts: one token over 64, 96 over 256 in groups (fp32, a bias), 8192 over 128,
+          and the gradient of 8191 over 160; rows to experts and back: 16 and 4096 tokens of 8
+          choices, the gradients of 8191 of 2 choices and of 601 x 1001 of 5
+  lora    low-rank adapters: one row, 32 rows of 24 adapters at rank 32 over 8192 x 4096, 2048 rows
+          of 8, all beside fp16 weights, and 24 rows of 16 beside 4-bit weights of 11008 x 4096
+          (weights of the small ones: 8 copies)
   copy    torch copy of a 512 MiB buffer: a plain copy kernel of known size,
           the calibration for the HBM byte counters
 """
@@ -51,7 +57,8 @@ def offsets(torch, rows, experts):
 
 def main(argv=None):
     ap = argparse.ArgumentParser()
-    ap.add_argument("op", choices=["gemm", "gemv", "splitk", "skinny", "sparse", "compress", "w4", "grouped", "copy"])
+    ap.add_argument("op", choices=["gemm", "gemv", "splitk", "skinny", "sparse", "compress", "w4", "grouped", "route",
+                                   "lora", "copy"])
     ap.add_argument("--iters", type=int, default=10)
     ap.add_argument("--m", type=int, default=8192)
     ap.add_argument("--n", type=int, default=8192)
@@ -164,6 +171,48 @@ def main(argv=None):
             C = torch.empty((rows, n), dtype=torch.float16, device="cuda")
             for i in range(a.iters):
                 gf.gemm_w4_f16_grouped_nt(A, *w[i % copies], off, C)
+    elif a.op == "route":
+        for T, E, k, dtype, kw in ((1, 64, 8, torch.float16, dict(renorm=True)),
+                                   (96, 256, 8, torch.float32, dict(score="sigmoid", groups=8, top_groups=4, group_best=2,
+                                                                    renorm=True, scale=2.5)),
+                                   (8192, 128, 8, torch.float32, {})):
+            x = half(torch, 90, T, E).to(dtype)
+            bias = half(torch, 91, E).float() * 0.05 if "groups" in kw else None
+            for _ in range(a.iters):
+                gf.route_topk(x, k, bias=bias, **kw)
+        x = half(torch, 92, 8191, 160)
+        ids, w = gf.route_topk(x, 6)[:2]
+        for _ in range(a.iters):
+            gf.route_topk_bwd(x, ids, w)
+        for T, E, k, D, grad in ((16, 64, 8, 4096, False), (4096, 64, 8, 2048, False), (8191, 8, 2, 4096, True),
+                                 (601, 33, 5, 1001, True)):
+            w, place = gf.route_topk(half(torch, 93, T, E), k)[1::2]
+            X, C = half(torch, 94, T, D), half(torch, 89, T * k, D)
+            A, Y = torch.empty_like(C), torch.empty_like(X)
+            for _ in range(a.iters):
+                if grad:
+                    gf.combine_f16(C, place, Y=Y)
+                    gf.combine_f16_bwd(X, C, place, w, dC=A)
+                else:
+                    gf.dispatch_f16(X, place, A=A)
+                    gf.combine_f16(C, place, w, Y=Y)
+    elif a.op == "lora":
+        for m, n, k, r, adapters, bits, copies in ((1, 4096, 4096, 16, 8, 16, 8), (32, 8192, 4096, 32, 24, 16, 8),
+                                                   (2048, 4096, 4096, 16, 8, 16, 1), (24, 11008, 4096, 16, 16, 4, 8)):
+            w = [half(torch, i, n, k) for i in range(copies)]
+            if bits == 4:
+                w = [gf.w4_quantize_f16(v, 64) for v in w]
+            low = [(half(torch, i, adapters, r, k), half(torch, 50 + i, adapters, n, r)) for i in range(copies)]
+            A, C = half(torch, 88, m, k), torch.empty((m, n), dtype=torch.float16, device="cuda")
+            ids = (torch.arange(m, device="cuda") * adapters // m).int()
+            ids = ids[torch.randperm(m, device="cuda")] if m <= 64 else ids
+            for i in range(a.iters):
+                down, up = low[i % copies]
+                if bits == 4:
+                    gf.gemm_w4_f16_nt(A, *w[i % copies], C=C, group=64)
+                    gf.lora_add_f16(A, ids, down, up, C)
+                else:
+                    gf.gemm_f16_nt_lora(A, w[i % copies], ids, down, up, C=C)
     else:
         src = torch.ones(128 << 20, dtype=torch.float32, device="cuda")   # 512 MiB
         dst = torch.empty_like(src)
