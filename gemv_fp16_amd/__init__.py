@@ -858,7 +858,8 @@ def route_topk(logits, k: int, bias=None, score: str = "softmax", groups: int = 
     expert whose logit is -inf is never taken; where none is left the id is -1
     and the weight 0.  Returns (ids (T, k) int32, weights (T, k) fp32, offsets
     (E+1,) int32, place (T, k) int32): the experts' row groups, and each choice's
-    row when they are sorted by expert (None, None with rows=False)."""
+    row when they are sorted by expert (None, None with rows=False).  Where none of
+    them is given, they are parts of one allocation."""
     import torch
     if logits.dim() != 2 or not 1 <= k <= logits.shape[1]:
         raise ValueError("logits must be (T, E) and k 1 to E")

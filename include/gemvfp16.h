@@ -487,8 +487,8 @@ int route_topk_bwd(const void* logits, int logits_f32, const int* ids, const flo
  * Rows to experts and back.  place: T x k ints in device memory, each the row of
  * one choice of a token among R sorted rows (route_topk, route_rows); entries
  * outside 0 .. R - 1 are no row.  Rows that place does not name are left as they
- * were; if it names a row twice, that row holds either.  All matrices are fp16 with
- * rows of D, at any 2-byte alignment (16 bytes and D % 8 == 0 are fastest).
+ * were; if it names a row twice, each entry of that row is one or the other's.  All
+ * matrices are fp16 with rows of D, at any 2-byte alignment (16 bytes and D % 8 == 0 are fastest).
  *
  * dispatch_f16: A[place[t][j]] = X[t], X T x D, A R x D.  Its gradient is
  * combine_f16 without weights.

@@ -164,6 +164,30 @@ def test_results_repeat_on_streams_and_in_graphs():
             assert torch.equal(u, v)
 
 
+def test_a_row_that_two_choices_name():
+    """Each entry is one or the other's; the other rows, and each choice's dot product, are as ever."""
+    rng = np.random.default_rng(5)
+    T, k, D, R = 40, 3, 1100, 130
+    X, C = dev(_f16(rng, T, D)), dev(_f16(rng, R, D))
+    at = np.arange(T * k, dtype=np.int32).reshape(T, k)
+    at[7, 2], at[30, 0] = at[30, 1], at[30, 1]             # of two tokens, and twice of one
+    place = dev(at)
+    w = torch.ones((T, k), device="cuda")
+    _say("rows twice")
+    A = gf.dispatch_f16(X, place, A=torch.zeros((R, D), dtype=torch.float16, device="cuda"))
+    dC, dw = gf.combine_f16_bwd(X, C, place, w, dC=torch.zeros((R, D), dtype=torch.float16, device="cuda"))
+    for got in (A, dC):
+        row = int(at[30, 1])
+        assert ((got[row] == X[7]) | (got[row] == X[30])).all()
+        for t in range(T):
+            for r in at[t]:
+                assert r == row or torch.equal(got[int(r)], X[t])
+    want = (X.double().cpu()[:, None, :] * C.double().cpu()[torch.from_numpy(at).long()]).sum(2)
+    # each product exact in fp32; 1100 of them summed, in whatever order
+    bound = D * 2.0 ** -23 * (X.double().cpu().abs()[:, None, :] * C.double().cpu().abs()[torch.from_numpy(at).long()]).sum(2)
+    assert ((dw.double().cpu() - want).abs() <= bound).all()
+
+
 def test_elements_near_2_31():
     """Rows whose offset passes 2^30 elements (2^31 bytes), at both ends of the operand."""
     D, R = 8192, 262143                    # R * D = 2^31 - 8192 elements
