@@ -15,14 +15,16 @@ int status(hipError_t e) { return e == hipSuccess ? GF_OK : GF_ERR_HIP; }
 
 // Parts of K that the products by Down are split in, for one CU takes in no more than
 // about 40 GB/s: up to 32 rows as many as make 256 workgroups of them (the streaming
-// form adds them in LDS, which holds all), beyond as many as make 512 of 16-row blocks,
+// form adds them in LDS, which holds all), beyond as many as make 128 of 16-row blocks,
 // but no more than the tiles' epilogue loads at once (100 rows of 8 adapters at 4096 x
-// 4096: 35 us with 4 parts, 40 with one).
+// 4096: 35 us with 4 parts, 40 with one).  Tiles and lora_add_f16 read H, all parts of
+// it, again for every 64 columns: 2048 rows of rank 64 took 99 us with 4 parts, 91 with
+// one, rank 16 77 either way.
 constexpr int most_floats(int M) { return M <= 16 ? 3840 : 7936; }
 int parts_of(int M, int K, int r)
 {
     if (M < 1) return 1;
-    int s = M <= 32 ? 256 / M : 512 / ceil_div(M, 16);
+    int s = M <= 32 ? 256 / M : 128 / ceil_div(M, 16);
     const int most = M <= 32 ? kLoraParts : kLoraTileParts;
     if (s > K / 512) s = K / 512;
     if (M <= 32 && s > most_floats(M) / (M * r)) s = most_floats(M) / (M * r);
@@ -98,8 +100,7 @@ int down(const LoraArgs& a, hipStream_t stream)
         if (Z < 1) Z = 1;
         const dim3 grid(grid_of((int64_t)blocks * Z), a.S);
         return status(a.r <= 16 ? launch_lora_down<LoraDownCfg<8, 1>>(a, grid, Z, stream)
-                                : (a.r <= 32 ? launch_lora_down<LoraDownCfg<8, 2>>(a, grid, Z, stream)
-                                             : launch_lora_down<LoraDownCfg<4, 4>>(a, grid, Z, stream)));
+                                : launch_lora_down<LoraDownCfg<8, 2>>(a, grid, Z, stream));
     } else {
         hipLaunchKernelGGL(lora_down_any_kernel, dim3(grid_of(a.M)), dim3(256), 0, stream, a);
     }
@@ -112,9 +113,14 @@ int up(const LoraArgs& a, hipStream_t stream)
     if (on16(a.Up) && a.r % 8 == 0) {
         const int vec = (reinterpret_cast<uintptr_t>(a.C) & 7) == 0 && a.N % 4 == 0;
         const int64_t items = (int64_t)ceil_div(a.M, 16) * ceil_div(a.N, 16);
-        if (items > 8192 && a.S <= kLoraTileParts)
+        // 64 columns a wave (half the loads of H, a quarter of the waves), where there are
+        // many and most blocks of rows have one adapter: 512 rows of 8 adapters at 4096 x
+        // 4096 10.9 us against 16.8, 300 of them 13.1 against 13.9, 160 12.6 against 11.3;
+        // 300 rows of 300 adapters 56 against 29.
+        const bool wide = items > 8192 || (items > 4096 && a.L <= a.M / 16);
+        if (wide && a.S <= kLoraTileParts)
             hipLaunchKernelGGL(lora_up_kernel<kLoraTileParts>, dim3(grid_of((items / 4 + 3) / 4)), dim3(256), 0, stream, a, vec);
-        else if (items > 8192)
+        else if (wide)
             hipLaunchKernelGGL(lora_up_kernel<kLoraParts>, dim3(grid_of((items / 4 + 3) / 4)), dim3(256), 0, stream, a, vec);
         else if (a.r <= 32)
             hipLaunchKernelGGL(lora_up_few_kernel<1>, dim3((int)(items + 3) / 4), dim3(256), 0, stream, a, vec);

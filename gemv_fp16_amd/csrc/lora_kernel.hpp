@@ -1,9 +1,10 @@
 // Low-rank adapters: C[m] = base + scale[a] * (A[m] . Down[a]^T) . Up[a]^T, a = ids[m].
 //
 // Two launches: H, the scaled products by Down, in fp32; then the base product with
-// H . Up[a]^T added to its accumulators before its one rounding (up to 32 rows the
-// streaming form below, beyond the tiles of gemm_kernel.hpp), or, for a base that is
-// computed already, that sum alone.  Operands off the 16-byte grid, or K or r that
+// H . Up[a]^T added to its accumulators before its one rounding (one or two rows in
+// vectors, up to 32 streaming B, beyond the tiles of gemm_kernel.hpp), or, for a base that
+// is computed already, that sum alone.  From 3 to 32 rows of a narrow B the first launch
+// takes the base's parts as well (K in slices), and the second joins all.  Operands off the 16-byte grid, or K or r that
 // are not multiples of 8, take the general forms: an output or a lane at a time.
 #pragma once
 #include "gemm_kernel.hpp"
@@ -176,7 +177,8 @@ __global__ __launch_bounds__(256) void lora_down_any_kernel(LoraArgs a)
 // The operands are swapped (Up's rows in the place of A's), so that a lane holds four
 // neighbouring columns of one row.  C is asked for before the sums are worked out, which
 // takes a chain of loads out of it (lora_add_f16, 2048 rows of 8 adapters, rank 64, at
-// 4096 x 4096: 43.4 us, was 57.5; rank 16 22.7, was 25.8; a copy of C takes 6.5).
+// 4096 x 4096: 35 us, rank 16 21; a copy of C takes 6.5, the products by Down 7 to 14).
+// What bounds it past rank 16 are H's and Up's bytes through L2.
 struct SwappedMfma {
     typedef floatx4 acc_t;
     static constexpr int NACC = 4;

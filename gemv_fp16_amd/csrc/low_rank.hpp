@@ -42,7 +42,9 @@ struct LowRank {
         floatx4 a[SP][2];
 #pragma unroll
         for (int s = 0; s < SP; ++s) {
-            const float* p = H + (s < S ? s : 0) * part + (size_t)m * r + k;
+            a[s][0] = a[s][1] = floatx4{};
+            if (s > 0 && s >= S) continue;
+            const float* p = H + s * part + (size_t)m * r + k;
             a[s][0] = *(const floatx4*)p;
             a[s][1] = *(const floatx4*)(p + 4);
         }
@@ -50,7 +52,7 @@ struct LowRank {
         for (int i = 0; i < 8; ++i) {
             float v = a[0][i / 4][i % 4];
 #pragma unroll
-            for (int s = 1; s < SP; ++s) v = s < S ? v + a[s][i / 4][i % 4] : v;
+            for (int s = 1; s < SP; ++s) v += a[s][i / 4][i % 4];
             _Float16 h, rest;
             split(v, h, rest);
             hi[i] = h;

@@ -107,7 +107,10 @@ CASES = [(1, 16, 64, 8, 1, "one"), (1, 1, 8, 1, 1, "one"), (1, 520, 1024, 16, 8,
          # 3 to 32 rows, K in slices: ends inside one, ranks past a block, its bounds
          (3, 16, 1544, 8, 2, "mixed"), (16, 1000, 3976, 24, 7, "stray"), (17, 263, 4096, 40, 20, "mixed"),
          (32, 8192, 2048, 16, 1, "one"), (32, 8200, 2056, 16, 3, "runs"), (31, 130, 4104, 16, 4, "mixed"),
-         (5, 19, 2048, 256, 4, "none"), (9, 15, 2048, 16, 4, "mixed"), (32, 520, 1536, 16, 32, "mixed")]
+         (5, 19, 2048, 256, 4, "none"), (9, 15, 2048, 16, 4, "mixed"), (32, 520, 1536, 16, 32, "mixed"),
+         # stored results: 64 columns a wave, and many adapters in 16
+         (520, 2100, 520, 72, 4, "runs"), (300, 4096, 264, 40, 300, "mixed"), (32, 66000, 64, 16, 2, "mixed"),
+         (1500, 264, 4096, 128, 3, "runs")]
 
 
 @pytest.mark.parametrize("M,N,K,r,L,kind", CASES)
