@@ -879,12 +879,12 @@ def route_topk(logits, k: int, bias=None, score: str = "softmax", groups: int = 
         b = _ptr(bias, f, "bias")
         tensors.append(bias)
     if rows and ids is weights is offsets is place is workspace is stream is None:
-        # all four and the workspace from one allocation: each costs as much as the
-        # rest of a call's checks (1.5 us, a view of one 0.8)
-        n = T * k
-        buf = logits.new_empty((3 * n + E + 1 + (need + 3) // 4,), dtype=i32)
-        ids, place = buf.as_strided((T, k), (k, 1)), buf.as_strided((T, k), (k, 1), n)
-        offsets, weights = buf.as_strided((E + 1,), (1,), 3 * n), buf.view(f).as_strided((T, k), (k, 1), 2 * n)
+        # all four and the workspace from one allocation, in rows of k: each of its own
+        # would cost as much as the rest of a call's checks
+        n, rest = T * k, (E + k + (need + 3) // 4) // k
+        buf = logits.new_empty((3 * T + rest, k), dtype=i32)
+        ids, place, weights, tail = torch.split_with_sizes(buf, (T, T, T, rest))
+        weights, offsets = weights.view(f), tail.as_strided((E + 1,), (1,))
         i = buf.data_ptr()
         p, g, o = i + 4 * n, i + 8 * n, i + 12 * n
         w = o + 4 * (E + 1)
