@@ -138,6 +138,19 @@ def test_lora_add(M, N, K, r, L, kind):
         assert np.array_equal(C.cpu().view(torch.int16).numpy()[dead], p.C0.view(np.int16)[dead])
 
 
+def test_lora_add_wide_with_a_long_contraction():
+    """Few rows onto many columns, the products by Down in more parts than a tile takes."""
+    M, N, K, r, L = 20, 66000, 2560, 8, 2
+    p = Problem(M, N, 8, r, L, "mixed", 3)
+    q = Problem(M, 16, K, r, L, "mixed", 4)
+    p.K, p.A, p.Down = K, q.A, q.Down
+    C = dev(p.C0)
+    _say("lora add", M, N, K, r, L)
+    gf.lora_add_f16(dev(p.A), dev(p.ids), dev(p.Down), dev(p.Up), C, dev(p.scales))
+    c0 = p.C0.astype(np.float64)
+    p.check(C, c0, np.abs(c0), "lora_add_f16")
+
+
 def test_rows_without_an_adapter_are_the_plain_product():
     """NaN and infinity in adapters that no row has, and in rows that have none, stay there."""
     for M, K in ((3, 512), (11, 2048), (40, 512), (300, 512)):
