@@ -33,7 +33,7 @@ EXPORTS = (
     "w4_quantize_f16", "w4_dequantize_f16", "gemm_w4_f16_nt", "gemv_w4_f16", "gemm_w4_f16_grouped_nt",
     "route_workspace_bytes", "route_topk", "route_rows", "route_topk_bwd",
     "dispatch_f16", "combine_f16", "combine_f16_bwd",
-    "lora_workspace_bytes", "gemm_f16_nt_lora", "lora_add_f16",
+    "lora_workspace_bytes", "gemm_f16_nt_lora", "lora_add_f16", "lora_add_f32",
 )
 
 
@@ -127,6 +127,7 @@ def lib() -> ctypes.CDLL:
     L.lora_workspace_bytes.argtypes = [ci, ci, ci, ci]
     L.gemm_f16_nt_lora.argtypes = [vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, vp, sz, vp]
     L.lora_add_f16.argtypes = [vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, vp, sz, vp]
+    L.lora_add_f32.argtypes = [vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, vp, sz, vp]
     L.gf_status_string.argtypes = [ci]
     L.gf_status_string.restype = ctypes.c_char_p
     L.route_workspace_bytes.restype = L.lora_workspace_bytes.restype = sz
@@ -1008,7 +1009,7 @@ def lora_workspace_bytes(M: int, N: int, K: int, r: int) -> int:
     return int(lib().lora_workspace_bytes(M, N, K, r))
 
 
-def _lora(name, A, B, ids, Down, Up, C, scales, workspace, stream):
+def _lora(name, A, B, ids, Down, Up, C, scales, workspace, stream, base=None):
     import torch
     if Down.dim() != 3 or Up.dim() != 3 or Down.shape[0] != Up.shape[0] or Down.shape[1] != Up.shape[2]:
         raise ValueError("Down must be (L, r, K) and Up (L, N, r)")
@@ -1023,7 +1024,9 @@ def _lora(name, A, B, ids, Down, Up, C, scales, workspace, stream):
     _ints(M | N | K | r | L)
     if not 1 <= r <= 256:
         raise ValueError("the rank must be 1 to 256")
-    C = _out(C, A, (M, N), f16, stream, "C")
+    if base is not None and base.shape != (M, N):
+        raise ValueError("C must be (%d, %d)" % (M, N))
+    C = _out(C, A, (M, N), f16, stream, "C" if base is None else "out")
     w, size, keep = _workspace(workspace, A, (_lib or lib()).lora_workspace_bytes(M, N, K, r), stream)
     tensors = [A, ids, Down, Up, C]
     if scales is not None:
@@ -1031,7 +1034,10 @@ def _lora(name, A, B, ids, Down, Up, C, scales, workspace, stream):
     if keep is not None:
         tensors.append(keep)
     tail = (_ptr(ids, torch.int32, "ids"), _ptr(Down, f16, "Down"), _ptr(Up, f16, "Up"),
-            None if scales is None else _ptr(scales, torch.float32, "scales"), _ptr(C, f16, "C"), M, N, K, r, L, w, size)
+            None if scales is None else _ptr(scales, torch.float32, "scales"),
+            *(() if base is None else (_ptr(base, torch.float32, "C"),)), _ptr(C, f16, "C"), M, N, K, r, L, w, size)
+    if base is not None:
+        tensors.append(base)
     if B is None:
         _launch(name, tensors, stream, _ptr(A, f16, "A"), *tail)
     else:
@@ -1044,14 +1050,21 @@ def gemm_f16_nt_lora(A, B, ids, Down, Up, scales=None, C=None, workspace=None, s
     """C[m] = A[m] . B^T + scales[a] * (A[m] . Down[a]^T) . Up[a]^T with the adapter
     a = ids[m] of each row: A (M, K), B (N, K), ids (M,) int32 (outside 0 .. L-1:
     none), Down (L, r, K), Up (L, N, r), scales (L,) fp32 or None for 1.  Returns C
-    (M, N) fp16.  workspace: uint8, lora_workspace_bytes(M, N, K, r) of them."""
+    (M, N) fp16, rounded once.  workspace: uint8, lora_workspace_bytes(M, N, K, r) of them."""
     return _lora("gemm_f16_nt_lora", A, B, ids, Down, Up, C, scales, workspace, stream)
 
 
-def lora_add_f16(A, ids, Down, Up, C, scales=None, workspace=None, stream=None):
-    """C[m] += scales[a] * (A[m] . Down[a]^T) . Up[a]^T in place, as in
-    gemm_f16_nt_lora, after a projection with 4-bit or 2:4 sparse weights.
-    Returns C (M, N) fp16; rows without an adapter are left as they were."""
+def lora_add_f16(A, ids, Down, Up, C, scales=None, workspace=None, stream=None, out=None):
+    """C[m] + scales[a] * (A[m] . Down[a]^T) . Up[a]^T, as in gemm_f16_nt_lora, after
+    a projection with weights of another kind.  With C (M, N) fp16 in place: C is
+    the base's rounded result and is rounded again; rows without an adapter are left
+    as they were.  With C fp32 the sum is rounded once, to every row of out (M, N)
+    fp16, by default a new one.  Returns the fp16 result."""
+    import torch
     if C is None:
         raise ValueError("C must be given")
+    if C.dtype is torch.float32:
+        return _lora("lora_add_f32", A, None, ids, Down, Up, out, scales, workspace, stream, C)
+    if out is not None and out is not C:
+        raise ValueError("out needs a C in fp32")
     return _lora("lora_add_f16", A, None, ids, Down, Up, C, scales, workspace, stream)

@@ -445,6 +445,20 @@ int splitk_f16_impl(const void* A, const void* B, void* C, int M, int N, int K, 
     return splitk_reduce(ws, C, true, mn, slices, stream);
 }
 
+}  // namespace
+
+int gemm_f32_parts(const void* A, const void* B, float* parts, int M, int N, int K, int most, int* count,
+                   hipStream_t stream)
+{
+    const gf_gemm_cfg cfg = default_splitk_cfg(M, N, K, most);
+    int kt_per;
+    slice_plan(K, cfg.block_k, most, kt_per, *count);
+    if (*count == 0) return GF_OK;
+    return run_gemm(A, B, parts, M, N, K, cfg, EPI_F32_STORE, *count, kt_per, true, stream);
+}
+
+namespace {
+
 int find_skinny(const gf_skinny_cfg& c)
 {
     for (int i = 0; i < kNumSkinny; ++i)

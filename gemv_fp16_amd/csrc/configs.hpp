@@ -51,6 +51,11 @@ constexpr SkinnyDesc kSkinnyConfigs[] = {
 };
 constexpr int kNumSkinny = sizeof(kSkinnyConfigs) / sizeof(kSkinnyConfigs[0]);
 
+// The product A . B^T in fp32, as parts of K that are not added yet: parts[s] (M x N),
+// *count of them, at most `most` (none where K == 0).  Checked arguments; api.hip.
+int gemm_f32_parts(const void* A, const void* B, float* parts, int M, int N, int K, int most, int* count,
+                   hipStream_t stream);
+
 typedef hipError_t (*GemmLaunchFn)(const GemmArgs&, int slices, hipStream_t);
 typedef hipError_t (*SkinnyLaunchFn)(const uint16_t*, const uint16_t*, uint16_t*, int, int, int,
                                      hipStream_t);

@@ -1,5 +1,6 @@
 // Low-rank adapters: argument checks, launch choice and C-ABI entry points.
 #include "../../include/gemvfp16.h"
+#include "configs.hpp"
 #include "lora_kernel.hpp"
 
 namespace gf {
@@ -44,12 +45,37 @@ int slices_of(int M, int N, int K)
     return M > 2 && M <= 32 && N >= 16 && N <= kSliceColumns && s >= 4 && s <= kLoraSlices ? s : 0;
 }
 
-// Floats of the base's parts, H's parts behind them 16-byte aligned.
-size_t base_floats(int M, int N, int K) { return ((size_t)slices_of(M, N, K) * M * N + 3) / 4 * 4; }
+// Floats of n parts of the base, H's parts behind them 16-byte aligned.
+size_t base_floats(int n, int M, int N) { return ((size_t)n * M * N + 3) / 4 * 4; }
+
+// Where no fused form fits, the base comes in fp32: about 8 M floats of rows at a time,
+// and at least 64 rows, which are one tile's.
+int base_rows(int M, int N)
+{
+    const int rows = (1 << 23) / N / 64 * 64;
+    return M < 64 || rows < 64 ? (M < 64 ? M : 64) : (rows < M ? rows : M);
+}
+// Its parts of K: up to 64 rows as many as make 256 tiles of 64 x 64.
+int base_parts(int M, int N, int K)
+{
+    if (M > 64) return 1;
+    int s = 256 / ceil_div(N, 64);
+    if (s > K / 512) s = K / 512;
+    return s < 1 ? 1 : (s > kLoraBaseParts ? kLoraBaseParts : s);
+}
+size_t base_need(int M, int N, int K, int r)
+{
+    return base_floats(base_parts(M, N, K), M, N) + (size_t)parts_of(M, K, r) * M * r;
+}
 size_t workspace_need(int M, int N, int K, int r)
 {
+    if (M == 0 || N == 0) return 0;
     const int s = slices_of(M, N, K), p = parts_of(M, K, r);
-    return (base_floats(M, N, K) + (size_t)(s > p ? s : p) * M * r) * sizeof(float);
+    size_t need = base_floats(s, M, N) + (size_t)(s > p ? s : p) * M * r;
+    const int rows = base_rows(M, N), rest = M % rows;
+    const size_t whole = base_need(rows, N, K, r), tail = rest ? base_need(rest, N, K, r) : 0;
+    if (need < whole) need = whole;
+    return (need < tail ? tail : need) * sizeof(float);
 }
 
 int check(const void* A, const int* ids, const void* Down, const void* Up, const float* scales, const void* C, int M,
@@ -77,6 +103,7 @@ LoraArgs args(const void* A, const void* B, const int* ids, const void* Down, co
     a.A = (const uint16_t*)A; a.B = (const uint16_t*)B; a.ids = ids;
     a.Down = (const uint16_t*)Down; a.Up = (const uint16_t*)Up; a.scales = scales;
     a.C = (uint16_t*)C; a.H = (float*)workspace;
+    a.base = nullptr; a.parts = 0;
     a.M = M; a.N = N; a.K = K; a.r = r; a.L = L;
     // the general forms leave K whole, and read H as one part
     const bool split = on16(A) && on16(Down) && K % 8 == 0 && on16(Up) && r % 8 == 0;
@@ -107,7 +134,8 @@ int down(const LoraArgs& a, hipStream_t stream)
     return status(hipGetLastError());
 }
 
-// C += H . Up^T.
+// C = base + H . Up^T with BASE, else C += H . Up^T.
+template <bool BASE>
 int up(const LoraArgs& a, hipStream_t stream)
 {
     if (on16(a.Up) && a.r % 8 == 0) {
@@ -119,19 +147,37 @@ int up(const LoraArgs& a, hipStream_t stream)
         // 300 rows of 300 adapters 56 against 29.
         const bool wide = items > 8192 || (items > 4096 && a.L <= a.M / 16);
         if (wide && a.S <= kLoraTileParts)
-            hipLaunchKernelGGL(lora_up_kernel<kLoraTileParts>, dim3(grid_of((items / 4 + 3) / 4)), dim3(256), 0, stream, a, vec);
+            hipLaunchKernelGGL((lora_up_kernel<kLoraTileParts, BASE>), dim3(grid_of((items / 4 + 3) / 4)), dim3(256), 0, stream, a, vec);
         else if (wide)
-            hipLaunchKernelGGL(lora_up_kernel<kLoraParts>, dim3(grid_of((items / 4 + 3) / 4)), dim3(256), 0, stream, a, vec);
+            hipLaunchKernelGGL((lora_up_kernel<kLoraParts, BASE>), dim3(grid_of((items / 4 + 3) / 4)), dim3(256), 0, stream, a, vec);
         else if (a.r <= 32)
-            hipLaunchKernelGGL(lora_up_few_kernel<1>, dim3((int)(items + 3) / 4), dim3(256), 0, stream, a, vec);
+            hipLaunchKernelGGL((lora_up_few_kernel<1, BASE>), dim3((int)(items + 3) / 4), dim3(256), 0, stream, a, vec);
         else if (a.r <= 64)
-            hipLaunchKernelGGL(lora_up_few_kernel<2>, dim3((int)(items + 1) / 2), dim3(256), 0, stream, a, vec);
+            hipLaunchKernelGGL((lora_up_few_kernel<2, BASE>), dim3((int)(items + 1) / 2), dim3(256), 0, stream, a, vec);
         else
-            hipLaunchKernelGGL(lora_up_few_kernel<4>, dim3((int)items), dim3(256), 0, stream, a, vec);
+            hipLaunchKernelGGL((lora_up_few_kernel<4, BASE>), dim3((int)items), dim3(256), 0, stream, a, vec);
     } else {
-        hipLaunchKernelGGL(lora_up_any_kernel, dim3(grid_of(((int64_t)a.M * a.N + 255) / 256)), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL(lora_up_any_kernel<BASE>, dim3(grid_of(((int64_t)a.M * a.N + 255) / 256)), dim3(256), 0, stream, a);
     }
     return status(hipGetLastError());
+}
+
+// The base as fp32 parts, then the adapters and the one rounding, `rows` rows at a time.
+int by_parts(const LoraArgs& all, float* workspace, hipStream_t stream)
+{
+    const int rows = base_rows(all.M, all.N);
+    for (int m = 0; m < all.M; m += rows) {
+        const int n = all.M - m < rows ? all.M - m : rows, most = base_parts(n, all.N, all.K);
+        LoraArgs a = args(all.A + (size_t)m * all.K, all.B, all.ids + m, all.Down, all.Up, all.scales,
+                          all.C + (size_t)m * all.N, n, all.N, all.K, all.r, all.L,
+                          workspace + base_floats(most, n, all.N));
+        a.base = workspace;
+        int rc = gemm_f32_parts(a.A, a.B, workspace, n, a.N, a.K, most, &a.parts, stream);
+        if (!rc) rc = down(a, stream);
+        if (!rc) rc = up<true>(a, stream);
+        if (rc) return rc;
+    }
+    return GF_OK;
 }
 
 // Base and adapters in tiles: default_gemm_cfg's choice among four of its tiles.
@@ -243,7 +289,21 @@ int lora_add_f16(const void* A, const int* ids, const void* Down, const void* Up
     if (rc || M == 0 || N == 0 || L == 0) return rc;
     const LoraArgs a = args(A, nullptr, ids, Down, Up, scales, C, M, N, K, r, L, workspace);
     rc = down(a, (hipStream_t)stream);
-    return rc ? rc : up(a, (hipStream_t)stream);
+    return rc ? rc : up<false>(a, (hipStream_t)stream);
+}
+
+int lora_add_f32(const void* A, const int* ids, const void* Down, const void* Up, const float* scales,
+                 const float* base, void* C, int M, int N, int K, int r, int L, void* workspace,
+                 size_t workspace_bytes, void* stream)
+{
+    int rc = check(A, ids, Down, Up, scales, C, M, N, K, r, L, workspace, workspace_bytes);
+    if (rc || M == 0 || N == 0) return rc;
+    if (off_grid(base, 4)) return GF_ERR_INVALID_ARG;
+    LoraArgs a = args(A, nullptr, ids, Down, Up, scales, C, M, N, K, r, L, workspace);
+    a.base = base;
+    a.parts = 1;
+    if (L > 0) rc = down(a, (hipStream_t)stream);
+    return rc ? rc : up<true>(a, (hipStream_t)stream);
 }
 
 int gemm_f16_nt_lora(const void* A, const void* B, const int* ids, const void* Down, const void* Up,
@@ -264,19 +324,18 @@ int gemm_f16_nt_lora(const void* A, const void* B, const int* ids, const void* D
     if (al && slices > 0) {
         LoraArgs b = a;
         b.S = slices;
-        b.H = (float*)workspace + base_floats(M, N, K);
+        b.H = (float*)workspace + base_floats(slices, M, N);
         return status(M <= 16 ? launch_lora_slices<LoraSliceCfg<1, 8>>(b, (float*)workspace, (hipStream_t)stream)
                               : launch_lora_slices<LoraSliceCfg<2, 6>>(b, (float*)workspace, (hipStream_t)stream));
     }
     if (al && band_takes(M, N, K)) return band(a, (hipStream_t)stream);
-    // From 33 to 64 rows the base's own streaming forms and a launch that adds to their
-    // results are ahead of tiles (64 rows of 24 adapters at 4096 x 4096: 28 us against 51).
+    // From 33 to 64 rows the base in parts is ahead of tiles (64 rows of 24 adapters at
+    // 4096 x 4096: 23 us against 51).
     if (al && on16(C) && M > 64) {
         rc = down(a, (hipStream_t)stream);
         return rc ? rc : tiles(a, (hipStream_t)stream);
     }
-    rc = gemm_f16_nt(A, B, C, M, N, K, stream);
-    return rc ? rc : lora_add_f16(A, ids, Down, Up, scales, C, M, N, K, r, L, workspace, workspace_bytes, stream);
+    return by_parts(a, (float*)workspace, (hipStream_t)stream);
 }
 
 }  // extern "C"

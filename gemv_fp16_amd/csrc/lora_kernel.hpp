@@ -3,8 +3,10 @@
 // Two launches: H, the scaled products by Down, in fp32; then the base product with
 // H . Up[a]^T added to its accumulators before its one rounding (one or two rows in
 // vectors, up to 32 streaming B, beyond the tiles of gemm_kernel.hpp), or, for a base that
-// is computed already, that sum alone.  From 3 to 32 rows of a narrow B the first launch
-// takes the base's parts as well (K in slices), and the second joins all.  Operands off the 16-byte grid, or K or r that
+// is computed already, that sum alone: onto a base in fp32, which is rounded with it, or
+// in place.  From 3 to 32 rows of a narrow B the first launch takes the base's parts as
+// well (K in slices), and the second joins all.  Where none of these forms fits, the base
+// comes as fp32 parts from gemm_kernel.hpp.  Operands off the 16-byte grid, or K or r that
 // are not multiples of 8, take the general forms: an output or a lane at a time.
 #pragma once
 #include "gemm_kernel.hpp"
@@ -17,7 +19,7 @@ constexpr int kLoraParts = 8, kLoraTileParts = 4;   // of K in the products by D
 
 struct LoraArgs {
     const uint16_t* A;       // M x K
-    const uint16_t* B;       // N x K, or null: C holds the base
+    const uint16_t* B;       // N x K, or null: the base is there already
     const int* ids;          // M
     const uint16_t* Down;    // L x r x K
     const uint16_t* Up;      // L x N x r
@@ -25,7 +27,8 @@ struct LoraArgs {
     uint16_t* C;             // M x N
     float* H;                // S x M x r
     int64_t part;            // floats of one of the S
-    int M, N, K, r, L, S;
+    const float* base;       // parts x M x N (BASE forms), else C holds it
+    int M, N, K, r, L, S, parts;
 
     __device__ __forceinline__ LowRank low() const { return {H, ids, Up, part, S, r, L}; }
 };
@@ -210,8 +213,39 @@ __device__ __forceinline__ bool lora_join(const LowRank& low, floatx4 (&sum)[1],
     return true;
 }
 
-// 16 rows by 16 columns, J waves each.
-template <int J>
+// Parts of a base in fp32, at most.
+constexpr int kLoraBaseParts = 8;
+
+// Columns n .. n + 3 of row m of each part (zeros where there are none): all loads in flight.
+struct LoraBase {
+    floatx4 v[kLoraBaseParts];
+
+    __device__ __forceinline__ void load(const LoraArgs& a, int m, int n)
+    {
+        const float* p = a.base + (size_t)m * a.N + n;
+        const size_t part = (size_t)a.M * a.N;
+#pragma unroll
+        for (int s = 0; s < kLoraBaseParts; ++s) {
+            v[s] = floatx4{};
+            if (s >= a.parts) continue;
+            if (n + 4 <= a.N) __builtin_memcpy(&v[s], p + s * part, 16);
+            else
+                for (int i = 0; n + i < a.N; ++i) v[s][i] = p[s * part + i];
+        }
+    }
+    __device__ __forceinline__ floatx4 sum() const   // in order
+    {
+        floatx4 t = v[0];
+#pragma unroll
+        for (int s = 1; s < kLoraBaseParts; ++s) t += v[s];
+        return t;
+    }
+};
+
+// 16 rows by 16 columns, J waves each.  BASE: the base's parts and the adapters, rounded
+// once, to every row of C; else C, the base, gets the adapters added in its rows that
+// have one.
+template <int J, bool BASE>
 __global__ __launch_bounds__(256) void lora_up_few_kernel(LoraArgs a, int vec)
 {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -224,25 +258,40 @@ __global__ __launch_bounds__(256) void lora_up_few_kernel(LoraArgs a, int vec)
     const bool four = vec && n + 4 <= a.N;
     typedef _Float16 half4 __attribute__((ext_vector_type(4)));
     half4 v = {};
-    if (four) v = *(const half4*)c;              // asked for before the sums are worked out
+    [[maybe_unused]] LoraBase base;
+    if constexpr (BASE) {                        // asked for before the sums are worked out
+        if (threadIdx.x / kWave % J == 0) base.load(a, min(m, a.M - 1), n);
+    } else {
+        if (four) v = *(const half4*)c;
+    }
     floatx4 sum[1];
     if (!lora_join<J, kLoraParts>(low, sum, row0, col0, a.M, a.N)) return;
-    if ((int)(blockIdx.x * 4 + threadIdx.x / kWave) / J >= items || m >= a.M || low.adapter(m, a.M) < 0) return;
+    if ((int)(blockIdx.x * 4 + threadIdx.x / kWave) / J >= items || m >= a.M) return;
+    if constexpr (BASE) {
+        sum[0] = low.adapter(m, a.M) < 0 ? base.sum() : base.sum() + sum[0];
+    } else {
+        if (low.adapter(m, a.M) < 0) return;
+        if (four)
+            for (int i = 0; i < 4; ++i) sum[0][i] += (float)v[i];
+        else
+            for (int i = 0; i < 4; ++i) sum[0][i] += n + i < a.N ? f16_bits_to_f32(c[i]) : 0.0f;
+    }
     if (four) {
         half4 o;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = (_Float16)((float)v[i] + sum[0][i]);
+        for (int i = 0; i < 4; ++i) o[i] = (_Float16)sum[0][i];
         *(half4*)c = o;
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (n + i < a.N) c[i] = f32_to_f16_bits(f16_bits_to_f32(c[i]) + sum[0][i]);
+            if (n + i < a.N) c[i] = f32_to_f16_bits(sum[0][i]);
     }
 #endif
 }
 
-// 16 rows by 64 columns a wave, S <= SP.
-template <int SP>
+// 16 rows by 64 columns a wave, S <= SP; BASE as above, of one part (more are added one
+// after the other, each a round of loads).
+template <int SP, bool BASE>
 __global__ __launch_bounds__(256, SP > 4 ? 3 : 4) void lora_up_kernel(LoraArgs a, int vec)
 {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -256,29 +305,46 @@ __global__ __launch_bounds__(256, SP > 4 ? 3 : 4) void lora_up_kernel(LoraArgs a
         const int col0 = __builtin_amdgcn_readfirstlane((int)(w % across) * 16 * NB);
         const int m = row0 + r16;
         typedef _Float16 half4 __attribute__((ext_vector_type(4)));
-        half4 v[NB];                             // asked for before the sums are worked out
+        typedef typename std::conditional<BASE, floatx4, half4>::type base4;
+        base4 v[NB];                             // asked for before the sums are worked out
+        const int64_t at = (int64_t)min(m, a.M - 1) * a.N;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             const int n = col0 + 16 * b + 4 * c4;
-            v[b] = half4{};
-            if (vec && n + 4 <= a.N) v[b] = *(const half4*)(a.C + (size_t)min(m, a.M - 1) * a.N + n);
+            v[b] = base4{};
+            if constexpr (BASE) {
+                for (int s = 0; s < a.parts; ++s) {
+                    const float* p = a.base + (int64_t)s * a.M * a.N + at + n;
+                    floatx4 t = {};
+                    if (n + 4 <= a.N) __builtin_memcpy(&t, p, 16);
+                    else
+                        for (int i = 0; n + i < a.N; ++i) t[i] = p[i];
+                    v[b] += t;
+                }
+            } else {
+                if (vec && n + 4 <= a.N) v[b] = *(const half4*)(a.C + at + n);
+                else
+                    for (int i = 0; i < 4; ++i)
+                        if (n + i < a.N) v[b][i] = __builtin_bit_cast(_Float16, a.C[at + n + i]);
+            }
         }
         floatx4 sum[NB];
         low.template block<SwappedMfma, 16, 32, NB, 2, SP>(sum, row0, col0, a.M, a.N);
-        if (m >= a.M || low.adapter(m, a.M) < 0) continue;
+        const bool none = low.adapter(m, a.M) < 0;
+        if (m >= a.M || (!BASE && none)) continue;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             const int n = col0 + 16 * b + 4 * c4;
             uint16_t* c = a.C + (size_t)m * a.N + n;
-            if (vec && n + 4 <= a.N) {
-                half4 o;
+            half4 o;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) o[i] = (_Float16)((float)v[b][i] + sum[b][i]);
+            for (int i = 0; i < 4; ++i) o[i] = (_Float16)((float)v[b][i] + (none ? 0.0f : sum[b][i]));
+            if (vec && n + 4 <= a.N) {
                 *(half4*)c = o;
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (n + i < a.N) c[i] = f32_to_f16_bits(f16_bits_to_f32(c[i]) + sum[b][i]);
+                    if (n + i < a.N) c[i] = __builtin_bit_cast(uint16_t, (_Float16)o[i]);
             }
         }
     }
@@ -286,17 +352,28 @@ __global__ __launch_bounds__(256, SP > 4 ? 3 : 4) void lora_up_kernel(LoraArgs a
 }
 
 // Any alignment and r: a thread an output (S == 1).
+template <bool BASE>
 __global__ __launch_bounds__(256) void lora_up_any_kernel(LoraArgs a)
 {
     const int64_t total = (int64_t)a.M * a.N;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
         const int m = (int)(i / a.N), n = (int)(i % a.N), id = a.ids[m];
-        if ((unsigned)id >= (unsigned)a.L) continue;
-        const float* h = a.H + (size_t)m * a.r;
-        const uint16_t* u = a.Up + ((size_t)id * a.N + n) * a.r;
-        float s = 0.0f;
-        for (int j = 0; j < a.r; ++j) s = __builtin_fmaf(h[j], f16_bits_to_f32(u[j]), s);
-        a.C[i] = f32_to_f16_bits(f16_bits_to_f32(a.C[i]) + s);
+        const bool some = (unsigned)id < (unsigned)a.L;
+        float c = 0.0f;
+        if constexpr (BASE) {
+            for (int s = 0; s < a.parts; ++s) c += a.base[s * total + i];
+        } else {
+            if (!some) continue;
+            c = f16_bits_to_f32(a.C[i]);
+        }
+        if (some) {
+            const float* h = a.H + (size_t)m * a.r;
+            const uint16_t* u = a.Up + ((size_t)id * a.N + n) * a.r;
+            float s = 0.0f;
+            for (int j = 0; j < a.r; ++j) s = __builtin_fmaf(h[j], f16_bits_to_f32(u[j]), s);
+            c += s;
+        }
+        a.C[i] = f32_to_f16_bits(c);
     }
 }
 

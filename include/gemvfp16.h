@@ -517,14 +517,14 @@ int combine_f16_bwd(const void* dY, const void* C, const int* place, const float
  * gemm_f16_nt_lora: C[m] = A[m] . B^T + scales[a] * (A[m] . Down[a]^T) . Up[a]^T, B
  * and C as in gemm_f16_nt.
  * lora_add_f16: C[m] = C[m] + scales[a] * (A[m] . Down[a]^T) . Up[a]^T in place,
- * after a projection that has no such form (4-bit or 2:4 sparse weights); the rows
- * without an adapter are left as they were.
+ * after a projection that has no such form; the rows without an adapter are left as
+ * they were.  C is a rounded result there, and is rounded a second time.
+ * lora_add_f32: C[m] = base[m] + the same, rounded once, every row of C; base (M x N
+ * floats, 4-byte aligned) is not changed and does not overlap C.
  *
  * fp32 accumulation; the scaled products by Down stay in fp32 (for the matrix cores as
  * two fp16 each, 22 bits together: one past fp16's range becomes an infinity there).
- * One rounding at the end, but where the base is stored first and the adapters are
- * added to it: in lora_add_f16, from 33 to 64 rows, at fewer of a long K (past 8192, from
- * 17 rows 4096), and in the general forms.  An infinity or a NaN in an adapter reaches
+ * One rounding at the end.  An infinity or a NaN in an adapter reaches
  * the rows that have it and no others.  Ranks 1 <= r <= 256; K % 8 == 0, r % 8 == 0 and
  * 16-byte aligned operands are fastest, everything else runs a general form.  The
  * adapters as a whole may pass 2^31 elements, one adapter's part and every other
@@ -539,6 +539,9 @@ int gemm_f16_nt_lora(const void* A, const void* B, const int* ids, const void* D
                      size_t workspace_bytes, void* stream);
 int lora_add_f16(const void* A, const int* ids, const void* Down, const void* Up, const float* scales, void* C,
                  int M, int N, int K, int r, int L, void* workspace, size_t workspace_bytes, void* stream);
+int lora_add_f32(const void* A, const int* ids, const void* Down, const void* Up, const float* scales,
+                 const float* base, void* C, int M, int N, int K, int r, int L, void* workspace,
+                 size_t workspace_bytes, void* stream);
 
 /* Static string naming a status code. */
 const char* gf_status_string(int status);
