@@ -30,7 +30,8 @@ EXPORTS = (
     "sp24_compress_f16", "gemm_sp_f16_nt", "gemm_sp_f16_nt_cfg", "gf_sp_config_count",
     "gf_sp_config_get", "gf_sp_default_config",
     "gemm_f16_grouped_nt", "gemm_f16_grouped_nn", "gemm_f16_grouped_tn",
-    "w4_quantize_f16", "w4_dequantize_f16", "gemm_w4_f16_nt", "gemv_w4_f16", "gemm_w4_f16_grouped_nt",
+    "w4_quantize_f16", "w4_dequantize_f16", "gemm_w4_f16_nt", "gemm_w4_f16_nt_f32", "gemv_w4_f16",
+    "gemm_w4_f16_grouped_nt",
     "route_workspace_bytes", "route_topk", "route_rows", "route_topk_bwd",
     "dispatch_f16", "combine_f16", "combine_f16_bwd",
     "lora_workspace_bytes", "gemm_f16_nt_lora", "lora_add_f16", "lora_add_f32",
@@ -114,7 +115,7 @@ def lib() -> ctypes.CDLL:
     L.gemm_f16_grouped_tn.argtypes = [vp, vp, vp, vp, ci, ci, ci, ci, ci, vp]
     L.w4_quantize_f16.argtypes = [vp, vp, vp, vp, ci, ci, ci, vp]
     L.w4_dequantize_f16.argtypes = [vp, vp, vp, vp, ci, ci, ci, vp]
-    L.gemm_w4_f16_nt.argtypes = [vp, vp, vp, vp, vp, ci, ci, ci, ci, vp]
+    L.gemm_w4_f16_nt.argtypes = L.gemm_w4_f16_nt_f32.argtypes = [vp, vp, vp, vp, vp, ci, ci, ci, ci, vp]
     L.gemv_w4_f16.argtypes = [vp, vp, vp, vp, vp, ci, ci, ci, vp]
     L.gemm_w4_f16_grouped_nt.argtypes = [vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, vp]
     L.route_workspace_bytes.argtypes = [ci, ci, ci]
@@ -753,18 +754,22 @@ def w4_dequantize_f16(Q, S, Z=None, group: int = 128, W=None, stream=None):
     return W
 
 
-def gemm_w4_f16_nt(A, Q, S, Z=None, C=None, group: int = 128, stream=None):
-    """C = A . W^T (fp32 accumulate, fp16 out) with A (M, K) and the 4-bit
-    weights Q (N, K/8), S, Z of w4_quantize_f16.  Returns C (M, N)."""
+def gemm_w4_f16_nt(A, Q, S, Z=None, C=None, group: int = 128, stream=None, out_f32=None):
+    """C = A . W^T (fp32 accumulate) with A (M, K) and the 4-bit weights Q (N, K/8),
+    S, Z of w4_quantize_f16.  Returns C (M, N), fp16, or the unrounded fp32 sums with
+    out_f32=True (or a C of that type), for lora_add_f16 to add adapters to."""
     import torch
     (N,), K = _w4_check(Q, S, Z, group, 2)
     if A.dim() != 2 or A.shape[1] != K:
         raise ValueError("A must be (M, %d)" % K)
     M, f16 = A.shape[0], torch.float16
     _ints(M | N | K)
-    C = _out(C, A, (M, N), f16, stream, "C")
-    _launch("gemm_w4_f16_nt", (A, Q, S, C) if Z is None else (A, Q, S, C, Z), stream, _ptr(A, f16, "A"),
-            *_w4_ptrs(Q, S, Z), _ptr(C, f16, "C"), M, N, K, group)
+    if out_f32 is None:
+        out_f32 = C is not None and C.dtype is torch.float32
+    dt = torch.float32 if out_f32 else f16
+    C = _out(C, A, (M, N), dt, stream, "C")
+    _launch("gemm_w4_f16_nt_f32" if out_f32 else "gemm_w4_f16_nt", (A, Q, S, C) if Z is None else (A, Q, S, C, Z),
+            stream, _ptr(A, f16, "A"), *_w4_ptrs(Q, S, Z), _ptr(C, dt, "C"), M, N, K, group)
     return C
 
 

@@ -283,6 +283,26 @@ int product_by_group(const W4Args& a, int group, hipStream_t stream)
     }
 }
 
+// C = A . W^T, fp16 or (f32 = 1) the fp32 sums.
+int product_of_one(const void* A, const void* Q, const void* S, const void* Z, void* C, int f32, int M, int N, int K,
+                   int group, hipStream_t s)
+{
+    const int rc = validate_w4(N, K, group);
+    if (rc) return rc;
+    if (M < 0 || M > kMaxExtent || (int64_t)M * K > kW4MaxElems || (int64_t)M * N > kW4MaxElems) return GF_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return GF_OK;
+    if (w4_bad(C, f32 ? 4 : 2)) return GF_ERR_INVALID_ARG;
+    if (K == 0) {                                       // the empty sum
+        const int64_t mn = ((int64_t)M * N) << f32;
+        hipLaunchKernelGGL(w4_zero_kernel, dim3(w4_grid(mn)), dim3(256), 0, s, (uint16_t*)C, mn);
+        return w4_status(hipGetLastError());
+    }
+    if (w4_bad(A, 2) || w4_bad(Q, 4) || w4_bad(S, 2)) return GF_ERR_INVALID_ARG;
+    W4Args a = {(const uint16_t*)A, (const uint32_t*)Q, (const uint16_t*)S, (const uint8_t*)Z, (uint16_t*)C,
+                M, N, K, ceil_div(K, group), f32, {nullptr, 0, 0, 0}};
+    return product_by_group<false>(a, group, s);
+}
+
 }  // namespace
 }  // namespace gf
 
@@ -321,21 +341,13 @@ int w4_dequantize_f16(const void* Q, const void* S, const void* Z, void* W, int 
 int gemm_w4_f16_nt(const void* A, const void* Q, const void* S, const void* Z, void* C, int M, int N, int K,
                    int group, void* stream)
 {
-    const int rc = validate_w4(N, K, group);
-    if (rc) return rc;
-    if (M < 0 || M > kMaxExtent || (int64_t)M * K > kW4MaxElems || (int64_t)M * N > kW4MaxElems) return GF_ERR_INVALID_ARG;
-    if (M == 0 || N == 0) return GF_OK;
-    if (w4_bad(C, 2)) return GF_ERR_INVALID_ARG;
-    hipStream_t s = (hipStream_t)stream;
-    if (K == 0) {                                       // the empty sum
-        const int64_t mn = (int64_t)M * N;
-        hipLaunchKernelGGL(w4_zero_kernel, dim3(w4_grid(mn)), dim3(256), 0, s, (uint16_t*)C, mn);
-        return w4_status(hipGetLastError());
-    }
-    if (w4_bad(A, 2) || w4_bad(Q, 4) || w4_bad(S, 2)) return GF_ERR_INVALID_ARG;
-    W4Args a = {(const uint16_t*)A, (const uint32_t*)Q, (const uint16_t*)S, (const uint8_t*)Z, (uint16_t*)C,
-                M, N, K, ceil_div(K, group), {nullptr, 0, 0, 0}};
-    return product_by_group<false>(a, group, s);
+    return product_of_one(A, Q, S, Z, C, 0, M, N, K, group, (hipStream_t)stream);
+}
+
+int gemm_w4_f16_nt_f32(const void* A, const void* Q, const void* S, const void* Z, float* C, int M, int N, int K,
+                       int group, void* stream)
+{
+    return product_of_one(A, Q, S, Z, C, 1, M, N, K, group, (hipStream_t)stream);
 }
 
 int gemv_w4_f16(const void* Q, const void* S, const void* Z, const void* x, void* y, int N, int K, int group,
@@ -357,7 +369,7 @@ int gemm_w4_f16_grouped_nt(const void* A, const void* Q, const void* S, const vo
     // K == 0: the kernel never reads A, Q or S, and stores the empty sums of the groups' rows
     if (K > 0 && (w4_bad(A, 2) || w4_bad(Q, 4) || w4_bad(S, 2))) return GF_ERR_INVALID_ARG;
     W4Args a = {(const uint16_t*)A, (const uint32_t*)Q, (const uint16_t*)S, (const uint8_t*)Z, (uint16_t*)C,
-                0, N, K, ceil_div(K, group), {offsets, E, T, 0}};
+                0, N, K, ceil_div(K, group), 0, {offsets, E, T, 0}};
     return product_by_group<true>(a, group, (hipStream_t)stream);
 }
 

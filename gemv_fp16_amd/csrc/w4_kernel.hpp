@@ -297,8 +297,17 @@ struct W4Args {
     const uint8_t* Z;     // N x G or null
     uint16_t* C;          // M x N
     int M, N, K, G;
+    int f32;              // one weight: whether C is fp32 (its sums before they are rounded)
     Groups g;             // grouped form: the rows of A and C by group, M unused; else only `first`
 };
+
+// Entry i of C.
+template <bool GROUPED>
+__device__ __forceinline__ void w4_store(const W4Args& a, size_t i, float v)
+{
+    if (!GROUPED && a.f32) ((float*)a.C)[i] = v;
+    else a.C[i] = f32_to_f16_bits(v);
+}
 
 // The eight q - z of a word, in order, as fp16 subnormals (times 2^-24).  A byte
 // holds an even k's code in its low half and the next one's in its high half,
@@ -570,7 +579,7 @@ __global__ __launch_bounds__(Cfg::WAVES * 64) void w4_rows_kernel(W4Args a)
         float s = 0.0f;
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) s += red[w * PER_WAVE + at];
-        if (n0 + n < a.N) a.C[(size_t)(m0 + m) * a.N + n0 + n] = f32_to_f16_bits(s);
+        if (n0 + n < a.N) w4_store<GROUPED>(a, (size_t)(m0 + m) * a.N + n0 + n, s);
     }
 #endif
 }
@@ -658,7 +667,7 @@ __global__ __launch_bounds__(Cfg::WAVES * 64) void w4_band_kernel(W4Args a, int 
         const int first = x % passes * 16 * MB;
         M = min(M - first, 16 * MB);
         a.A += (size_t)first * K;
-        a.C += (size_t)first * N;
+        a.C += ((size_t)first * N) << a.f32;
     }
     const int red_rows = GROUPED ? 16 * MB : min(a.M, 16 * MB);
     GF_LDS char* tasks = (GF_LDS char*)w4_smem + wave * ring * Cfg::TASK_BYTES;
@@ -877,7 +886,7 @@ __global__ __launch_bounds__(Cfg::WAVES * 64) void w4_band_kernel(W4Args a, int 
             float s = 0.0f;
 #pragma unroll
             for (int w = 0; w < WAVES; ++w) s += mine[w * red_rows * 16 + t];
-            a.C[(size_t)(t / 16) * N + n0 + t % 16] = f32_to_f16_bits(s * kW4Unit);
+            w4_store<GROUPED>(a, (size_t)(t / 16) * N + n0 + t % 16, s * kW4Unit);
         }
     }
     wait_vmcnt<0>();
@@ -1184,9 +1193,23 @@ __global__ __launch_bounds__(Cfg::NT) void w4_tile_kernel(W4Args a)
         if (t < nk) step(t, std::integral_constant<int, 0>{});
     wait_vmcnt<0>();                                      // no load may land once the epilogue writes LDS
 
+    constexpr int WR = 32 * FM, WC = 32 * FN, LDW = WC + Cfg::EPAD;
+    if (!GROUPED && a.f32) {                              // 128 bytes of a row a store
+#pragma unroll
+        for (int f = 0; f < FM; ++f)
+#pragma unroll
+            for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int row = m0 + wm * WR + f * 32 + 8 * (i / 4) + 4 * h + i % 4;
+                    const int col = n0 + wn * WC + fn * 32 + r32;
+                    if (row < M && col < a.N) ((float*)a.C)[(size_t)row * a.N + col] = acc[f][fn][i];
+                }
+        return;
+    }
+
     // ---- epilogue: per-wave transpose in LDS, 16-byte stores ----
     lds_barrier();
-    constexpr int WR = 32 * FM, WC = 32 * FN, LDW = WC + Cfg::EPAD;
     GF_LDS uint16_t* reg = (GF_LDS uint16_t*)(smem + wave * (WR * LDW * 2));
 #pragma unroll
     for (int f = 0; f < FM; ++f)

@@ -411,6 +411,8 @@ int gemm_f16_grouped_tn(const void* A, const void* B, void* C, const int* offset
  * first, as w4_dequantize_f16 rounds it (one past the fp16 range to an infinity);
  * sums are in fp32 all the same.  Which way is taken depends on the sizes and the
  * operands' alignment alone, and results repeat bit for bit from run to run.
+ * gemm_w4_f16_nt_f32: the same sums unrounded, C M x N floats, 4-byte aligned
+ * (lora_add_f32 adds adapters to them).
  * gemm_w4_f16_grouped_nt: gemm_f16_grouped_nt with 4-bit weights, Q E x N x
  * K/8, S and Z E x N x G; offsets and rows as there.  Its weights may be rounded
  * so from a mean of 17 rows a group (T > 16 E) on.
@@ -426,6 +428,8 @@ int w4_dequantize_f16(const void* Q, const void* S, const void* Z, void* W, int 
                       void* stream);
 int gemm_w4_f16_nt(const void* A, const void* Q, const void* S, const void* Z, void* C, int M, int N, int K,
                    int group, void* stream);
+int gemm_w4_f16_nt_f32(const void* A, const void* Q, const void* S, const void* Z, float* C, int M, int N, int K,
+                       int group, void* stream);
 int gemv_w4_f16(const void* Q, const void* S, const void* Z, const void* x, void* y, int N, int K, int group,
                 void* stream);
 int gemm_w4_f16_grouped_nt(const void* A, const void* Q, const void* S, const void* Z, void* C,
