@@ -226,7 +226,7 @@ def _own(s):
         return [gf.dispatch_f16(s["X"], s["place"], A=s["A"]), gf.combine_f16(s["C"], s["place"], s["w"])]
     if case["bits"] == 16:
         return gf.gemm_f16_nt_lora(s["A"], s["B"], s["ids"], s["Down"], s["Up"], s["scales"])
-    C = gf.gemm_w4_f16_nt(s["A"], s["Q"], s["S"], s["Z"], group=case["group"])
+    C = gf.gemm_w4_f16_nt(s["A"], s["Q"], s["S"], s["Z"], group=case["group"], out_f32=True)   # rounded once, below
     return gf.lora_add_f16(s["A"], s["ids"], s["Down"], s["Up"], C, s["scales"])
 
 
