@@ -220,7 +220,7 @@ int vec(const LoraArgs& a, hipStream_t stream)
     const int64_t up_bytes = most * iters * WAVES * a.r * 2, sums = (int64_t)iters * WAVES * MV * 4;
     if (up_bytes > 100 * 1024 || sums > 64 * 1024 || (int64_t)MV * lora_vec_pad(a.K, UNROLL) * 16 > 128 * 1024)
         return GF_ERR_UNSUPPORTED;
-    const LoraVecLds at(MV, WAVES, a.K, a.r, UNROLL, iters * WAVES, (int)most);
+    const LoraVecLds at(MV, a.K, a.r, UNROLL, iters * WAVES, (int)most);
     if (at.total > 159 * 1024) return GF_ERR_UNSUPPORTED;
     if (most * a.r <= kVecSelf)
         return status(launch_lora_vec<MV, UNROLL, WAVES, true>(a, grid, iters, (int)most, at.total, stream));

@@ -418,14 +418,13 @@ __host__ __device__ constexpr int lora_vec_pad(int K, int unroll) { return ceil_
 
 struct LoraVecLds {
     int a, h, sums, up, total;
-    __host__ __device__ LoraVecLds(int MV, int waves, int K, int r, int unroll, int rows, int most)
+    __host__ __device__ LoraVecLds(int MV, int K, int r, int unroll, int rows, int most)
     {
         a = 0;
         h = a + MV * lora_vec_pad(K, unroll) * 16;
         sums = h + MV * r * 4;
         up = (sums + rows * MV * 4 + 15) / 16 * 16;
         total = up + ceil_div(most * rows * r * 2, 1024) * 1024;   // in whole loads
-        (void)waves;
     }
 };
 
@@ -443,7 +442,7 @@ __global__ __launch_bounds__(WAVES * kWave) void lora_vec_kernel(LoraArgs a, int
     const int nch = K / 8, spg = ceil_div(nch, STEP), npad = spg * STEP;
     const bool ragged = npad != nch;
     const int rows = iters * WAVES, n0 = blockIdx.x * WAVES, nstep = gridDim.x * WAVES;
-    const LoraVecLds at(MV, WAVES, K, r, UNROLL, rows, most);
+    const LoraVecLds at(MV, K, r, UNROLL, rows, most);
     GF_LDS char* smem = (GF_LDS char*)smem_raw;
     GF_LDS half8* as = (GF_LDS half8*)(smem + at.a);     // [MV][npad]
     GF_LDS float* H = (GF_LDS float*)(smem + at.h);      // [MV][r]

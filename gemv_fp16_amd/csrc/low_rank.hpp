@@ -126,56 +126,4 @@ struct LowRank {
     }
 };
 
-// The same for a wave's FM x FN blocks at the end of a tile.  Where all rows have one
-// adapter of up to KP steps of ranks, its operands are loaded before the first sum is
-// asked for; a block at a time, each would wait for its own.
-template <class MF, int MT, int KS, int FM, int FN, int KP, int SP>
-struct LowRankTile {
-    static constexpr int FB = FN < 2 ? 1 : 2;    // blocks a call: all FN beside 256 accumulators do not fit
-    half8 hi[FM][KP], lo[FM][KP], u[FN][KP];
-    bool ahead;
-
-    __device__ __forceinline__ void init(const LowRank& low, int row0, int col0, int M, int N)
-    {
-        const int lane = threadIdx.x % kWave, l = lane % MT, kq = lane / MT * 8;
-        const int first = __builtin_amdgcn_readfirstlane(low.adapter(row0, M));
-        bool same = first >= 0;
-#pragma unroll
-        for (int f = 0; f < FM; ++f) same &= low.adapter(row0 + f * MT + l, M) == first;
-        ahead = __ballot(same) == ~uint64_t(0) && low.r <= KP * KS;
-        if (!ahead) return;
-#pragma unroll
-        for (int p = 0; p < KP; ++p) {
-            const int k = min(p * KS + kq, low.r - 8);
-            const bool in = p * KS + kq < low.r;
-#pragma unroll
-            for (int g = 0; g < FN; ++g) {
-                const half8 v = *(const half8*)(low.Up + ((size_t)first * N + min(col0 + g * MT + l, N - 1)) * low.r + k);
-                u[g][p] = in ? v : half8{};
-            }
-#pragma unroll
-            for (int f = 0; f < FM; ++f) low.template pairs<SP>(min(row0 + f * MT + l, M - 1), k, hi[f][p], lo[f][p]);
-        }
-    }
-
-    // Blocks (f, g) .. (f, g + FB - 1).
-    template <int f, int g>
-    __device__ __forceinline__ void sums(const LowRank& low, typename MF::acc_t (&sum)[FB], int row0, int col0, int M, int N) const
-    {
-        if (ahead) {
-#pragma unroll
-            for (int b = 0; b < FB; ++b) {
-                sum[b] = typename MF::acc_t{};
-#pragma unroll
-                for (int p = 0; p < KP; ++p) {
-                    sum[b] = MF::run(hi[f][p], u[g + b][p], sum[b]);
-                    sum[b] = MF::run(lo[f][p], u[g + b][p], sum[b]);
-                }
-            }
-        } else {
-            low.template block<MF, MT, KS, FB, FM * FN == 1 ? 8 : 4, SP>(sum, row0 + f * MT, col0 + g * MT, M, N);
-        }
-    }
-};
-
 }  // namespace gf

@@ -75,11 +75,6 @@ __device__ __forceinline__ float wave_max(float v)
     return wave_reduce(v, -__builtin_inff(), [](float a, float b) { return __builtin_fmaxf(a, b); });
 }
 
-__device__ __forceinline__ double wave_max(double v)
-{
-    return wave_reduce(v, -__builtin_inf(), [](double a, double b) { return __builtin_fmax(a, b); });
-}
-
 template <class T>
 __device__ __forceinline__ T wave_sum(T v)
 {
