@@ -364,6 +364,7 @@ template <>
 struct Mfma<32> {
     typedef floatx16 acc_t;
     static constexpr int NACC = 16;
+    static constexpr bool ROW_IN_LANE = false;   // a lane's accumulators are of several rows
     static __device__ __forceinline__ acc_t run(half8 a, half8 b, acc_t c)
     {
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
@@ -380,6 +381,7 @@ template <>
 struct Mfma<16> {
     typedef floatx4 acc_t;
     static constexpr int NACC = 4;
+    static constexpr bool ROW_IN_LANE = false;
     static __device__ __forceinline__ acc_t run(half8 a, half8 b, acc_t c)
     {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);

@@ -185,6 +185,7 @@ __global__ __launch_bounds__(256) void lora_down_any_kernel(LoraArgs a)
 struct SwappedMfma {
     typedef floatx4 acc_t;
     static constexpr int NACC = 4;
+    static constexpr bool ROW_IN_LANE = true;    // all of a lane's accumulators are of one row
     static __device__ __forceinline__ acc_t run(half8 h, half8 u, acc_t c)
     {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(u, h, c, 0, 0, 0);
@@ -609,10 +610,11 @@ struct LoraBandCfg {
     static constexpr int MB = MB_, XB = XB_, RING = RING_, WAVES = 8, BK = 128, LOADS = 4, TASK_BYTES = 4096;
     static constexpr int ROWS = 16 * MB;
     static constexpr int RED_BYTES = 2 * WAVES * ROWS * 16 * 4;
-    // the rings, the waves' sums, the adapters in use and their rows, H's parts in whole loads
+    // the rings, the waves' sums, the adapters in use and their rows, the scales of H's rows,
+    // H's parts in whole loads
     static constexpr int lds_bytes(int h_floats)
     {
-        return WAVES * RING * TASK_BYTES + RED_BYTES + 2 * ROWS * 4 + ceil_div(h_floats * 4, 1024) * 1024;
+        return WAVES * RING * TASK_BYTES + RED_BYTES + 3 * ROWS * 4 + ceil_div(h_floats * 4, 1024) * 1024;
     }
 };
 
@@ -630,7 +632,8 @@ __global__ __launch_bounds__(Cfg::WAVES * 64) void lora_band_kernel(LoraArgs a, 
     GF_LDS float* red = (GF_LDS float*)((GF_LDS char*)smem_raw + WAVES * RING * Cfg::TASK_BYTES);
     GF_LDS int* used = (GF_LDS int*)((GF_LDS char*)red + Cfg::RED_BYTES);
     GF_LDS uint32_t* rows_of = (GF_LDS uint32_t*)(used + MR);
-    GF_LDS float* H = (GF_LDS float*)(rows_of + MR);     // S x M x r; then, 4 ranks to 16 bytes, their fp16 pairs
+    GF_LDS float* back = (GF_LDS float*)(rows_of + MR);  // what each row's scaled sums are multiplied by
+    GF_LDS float* H = back + MR;                         // S x M x r; then, 4 ranks to 16 bytes, their fp16 pairs
 
     const int nblk = ceil_div(K, Cfg::BK);
     const int b0 = wave * nblk / WAVES, nk = (wave + 1) * nblk / WAVES - b0;   // this wave's tasks of K
@@ -722,20 +725,30 @@ __global__ __launch_bounds__(Cfg::WAVES * 64) void lora_band_kernel(LoraArgs a, 
                 x[b][m] = *(const half8*)(k < K && b < 4 * nk ? (const void*)(src + k) : (const void*)g_zero16);
             }
         }
-    // H's parts to LDS, then each value as a pair of fp16 in its place (low_rank.hpp)
+    // H's parts to LDS, then each value as a scaled pair of fp16 in its place (low_rank.hpp),
+    // a wave a row (r <= 256: 4 ranks a lane)
     auto pack = [&](int parts) __attribute__((always_inline)) {
-        for (int i = threadIdx.x * 4; i < M * r; i += WAVES * kWave * 4) {
-            floatx4 v = *(const GF_LDS floatx4*)(H + i);
-            for (int p = 1; p < parts; ++p) v += *(const GF_LDS floatx4*)(H + p * M * r + i);
+        for (int m = wave; m < M; m += WAVES) {
+            const int i = m * r + lane * 4;
+            floatx4 v = {};
+            if (lane * 4 < r) {
+                v = *(const GF_LDS floatx4*)(H + i);
+                for (int p = 1; p < parts; ++p) v += *(const GF_LDS floatx4*)(H + p * M * r + i);
+            }
+            float most = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) most = LowRank::larger(most, v[e]);
+            const LowRank::Scale scale(wave_max(most));
             half8 pair;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 _Float16 hi, lo;
-                LowRank::split(v[e], hi, lo);
+                LowRank::split(v[e] * scale.up, hi, lo);
                 pair[e] = hi;
                 pair[e + 4] = lo;
             }
-            *(GF_LDS half8*)(H + i) = pair;
+            if (lane * 4 < r) *(GF_LDS half8*)(H + i) = pair;
+            if (lane == 0) back[m] = scale.down;
         }
         lds_barrier();
     };
@@ -852,13 +865,14 @@ __global__ __launch_bounds__(Cfg::WAVES * 64) void lora_band_kernel(LoraArgs a, 
                         p = h[0];
                         q = h[1];
                     }
+                    const floatx4 f = *(const GF_LDS floatx4*)(back + 16 * m + 4 * c4);
                     floatx4 t = {};
                     t = __builtin_amdgcn_mfma_f32_16x16x32_f16(
                         __builtin_shufflevector(p, q, 0, 1, 2, 3, 8, 9, 10, 11), w, t, 0, 0, 0);
                     t = __builtin_amdgcn_mfma_f32_16x16x32_f16(
                         __builtin_shufflevector(p, q, 4, 5, 6, 7, 12, 13, 14, 15), w, t, 0, 0, 0);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[m][e] += (mask >> (16 * m + 4 * c4 + e)) & 1 ? t[e] : 0.0f;
+                    for (int e = 0; e < 4; ++e) acc[m][e] += (mask >> (16 * m + 4 * c4 + e)) & 1 ? t[e] * f[e] : 0.0f;
                 }
             }
             next();

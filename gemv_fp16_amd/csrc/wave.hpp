@@ -69,6 +69,22 @@ __device__ __forceinline__ T row_reduce(T v, T id, Op op)
     return op(v, dpp_move<0x140, 0xF>(id, v));
 }
 
+// The largest over the lanes l, l + MT, l + 2 MT .. of each l, in all of them.
+template <int MT>
+__device__ __forceinline__ float rows_max(float v)
+{
+    const uint32_t b = __builtin_bit_cast(uint32_t, v);
+    auto larger = [](auto p) {
+        return __builtin_fmaxf(__builtin_bit_cast(float, (uint32_t)p[0]), __builtin_bit_cast(float, (uint32_t)p[1]));
+    };
+    v = larger(__builtin_amdgcn_permlane32_swap(b, b, false, false));
+    if constexpr (MT == 16) {
+        const uint32_t c = __builtin_bit_cast(uint32_t, v);
+        v = larger(__builtin_amdgcn_permlane16_swap(c, c, false, false));
+    }
+    return v;
+}
+
 // A NaN loses to any number.
 __device__ __forceinline__ float wave_max(float v)
 {

@@ -526,8 +526,9 @@ int combine_f16_bwd(const void* dY, const void* C, const int* place, const float
  * lora_add_f32: C[m] = base[m] + the same, rounded once, every row of C; base (M x N
  * floats, 4-byte aligned) is not changed and does not overlap C.
  *
- * fp32 accumulation; the scaled products by Down stay in fp32 (for the matrix cores as
- * two fp16 each, 22 bits together: one past fp16's range becomes an infinity there).
+ * fp32 accumulation; the scaled products by Down stay in fp32.  From 3 rows on the matrix
+ * cores take them as two fp16 each, scaled by a power of two: 22 bits of every one down
+ * to 2^-18 of its row's largest, below that an error of up to 2^-40 of the largest.
  * One rounding at the end.  An infinity or a NaN in an adapter reaches
  * the rows that have it and no others.  Ranks 1 <= r <= 256; K % 8 == 0, r % 8 == 0 and
  * 16-byte aligned operands are fastest, everything else runs a general form.  The

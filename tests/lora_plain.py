@@ -8,10 +8,11 @@ class Integers:
     products.  The base and the products by Down have more bits than fp16; every sum
     of magnitudes stays below 2^24 units, so that no order of additions rounds.
 
-    up: Up's unit and scale: the adapters' scale, powers of two; their product is what
-    one unit of the adapters' part is worth, and no less than the base's unit, 1."""
+    far: pairs of powers of two, one for each adapter in turn: its scale, and the unit of
+    its Up; the base is 0 then.  spread: ranks are worth 2^-spread to 1 in Down, and the
+    inverse in Up."""
 
-    def __init__(self, M, N, K, r, L, seed, scale=1.0, up=1.0, stray=True):
+    def __init__(self, M, N, K, r, L, seed, far=None, spread=0, stray=True):
         rng = np.random.default_rng(seed)
         ints = lambda most, *shape: rng.integers(-most, most + 1, shape)
         shrink = min(1.0, np.sqrt(512 / max(K, 1)))
@@ -24,10 +25,16 @@ class Integers:
             self.ids[rng.random(M) < 0.2] = -1
             self.ids[M // 2] = L
         sign = np.where(rng.random(L) < 0.5, -1, 1)
+        scale, up = (np.resize([f[i] for f in far or [(1.0, 1.0)]], L) for i in (0, 1))
+        if far:
+            b[:] = 0
+        worth = 2.0 ** -rng.integers(0, spread + 1, (L, r))
         self.scales = (sign * scale).astype(np.float32)
         self.A, self.B = a.astype(np.float16), b.astype(np.float16)
-        self.Down, self.Up = down.astype(np.float16), (u * up).astype(np.float16)
-        assert (self.Up.astype(np.float64) == u * up).all()
+        exact16 = lambda v: (v.astype(np.float16), (v.astype(np.float16) == v).all())
+        self.Down, down_ok = exact16(down * worth[:, :, None])
+        self.Up, up_ok = exact16(u * (up[:, None] / worth)[:, None, :])
+        assert down_ok and up_ok
         self.base = a.astype(np.float64) @ b.T.astype(np.float64)
         size = np.abs(a).astype(np.float64) @ np.abs(b).T.astype(np.float64)
         self.low, self.H = np.zeros((M, N)), np.zeros((M, r))
@@ -37,10 +44,12 @@ class Integers:
                 h = a[m].astype(np.float64) @ down[e].T.astype(np.float64)
                 assert np.abs(h).max(initial=0) < 2 ** 22
                 assert (np.abs(a[m]).astype(np.float64) @ np.abs(down[e]).T).max(initial=0) < 2 ** 24
-                self.H[m] = sign[e] * scale * h
-                self.low[m] = sign[e] * scale * up * (h @ u[e].T)
-                size[m] += scale * up * (np.abs(h) @ np.abs(u[e]).T)
-        assert size.max(initial=0) < 2 ** 24 * min(1.0, scale * up)
+                unit = scale[e] * up[e]
+                self.H[m] = sign[e] * scale[e] * worth[e] * h
+                self.low[m] = sign[e] * unit * (h @ u[e].T)
+                size[m] += unit * (np.abs(h) @ np.abs(u[e]).T)
+                assert size[m].max(initial=0) < 2 ** 24 * unit
+        assert far or size.max(initial=0) < 2 ** 24
         self.exact = self.base + self.low
 
     def once(self, base=None):
