@@ -855,7 +855,7 @@ __global__ __launch_bounds__(Cfg::WAVES * 64) void lora_band_kernel(LoraArgs a, 
                 if (u >= units) break;
                 const int k = u % rk * 32 + 8 * c4;
                 const uint32_t mask = __builtin_amdgcn_readfirstlane(rows_of[u / rk]);
-                const half8 w = *(const GF_LDS half8*)(buf + i * 1024 + r16 * 64 + c4 * 16);
+                const half8 w = *(const GF_LDS half8*)(buf + i * 1024 + r16 * 64 + c4 * 16), w1 = LowRank::finite(w);
 #pragma unroll
                 for (int m = 0; m < MB; ++m) {
                     if (((mask >> (16 * m)) & 0xFFFF) == 0) continue;
@@ -870,7 +870,7 @@ __global__ __launch_bounds__(Cfg::WAVES * 64) void lora_band_kernel(LoraArgs a, 
                     t = __builtin_amdgcn_mfma_f32_16x16x32_f16(
                         __builtin_shufflevector(p, q, 0, 1, 2, 3, 8, 9, 10, 11), w, t, 0, 0, 0);
                     t = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                        __builtin_shufflevector(p, q, 4, 5, 6, 7, 12, 13, 14, 15), w, t, 0, 0, 0);
+                        __builtin_shufflevector(p, q, 4, 5, 6, 7, 12, 13, 14, 15), w1, t, 0, 0, 0);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) acc[m][e] += (mask >> (16 * m + 4 * c4 + e)) & 1 ? t[e] * f[e] : 0.0f;
                 }

@@ -8,7 +8,10 @@
 // inverse: 22 bits of every value down to 2^-18 of the largest, 2^-40 of the largest
 // below, whatever the size of H.  A block of rows costs one pass for each adapter that it
 // has; where it has several, each one's sums are added to its own rows alone, so that
-// an infinity or a NaN in one adapter stays in the rows that have it.
+// an infinity or a NaN in one adapter stays in the rows that have it.  Infinities come out
+// as the formula has them: an infinite value has no second half, a second half does not
+// meet Up's infinities (0 times one would be a NaN), and ranks that are not there are 0 on
+// both sides.
 #pragma once
 #include "wave.hpp"
 
@@ -36,6 +39,13 @@ struct LowRank {
         lo = rest - rest == 0.0f ? (_Float16)rest : (_Float16)0.0f;   // none beside an infinity or a NaN
     }
 
+    // u with numbers for infinities and NaN: what the second halves are multiplied by.
+    static __device__ __forceinline__ half8 finite(half8 u)
+    {
+        const half8 most = (half8)(_Float16)65504.0f;
+        return __builtin_elementwise_min(__builtin_elementwise_max(u, -most), most);
+    }
+
     // The larger of m and |v|; an infinity or a NaN does not count.
     static __device__ __forceinline__ float larger(float m, float v)
     {
@@ -55,11 +65,11 @@ struct LowRank {
         }
     };
 
-    // k .. k + 7 of row m's H as scaled pairs, and the scale's inverse; k + 8 <= r.  SP:
-    // parts at most, their loads all in flight together.  The row's other ranks of this
-    // step are in the lanes MT further.  All lanes.
+    // k .. k + 7 of row m's H as scaled pairs (0 where not `in`), and the scale's inverse;
+    // k + 8 <= r.  SP: parts at most, their loads all in flight together.  The row's other
+    // ranks of this step are in the lanes MT further.  All lanes.
     template <int MT, int SP>
-    __device__ __forceinline__ float pairs(int m, int k, half8& hi, half8& lo) const
+    __device__ __forceinline__ float pairs(int m, int k, bool in, half8& hi, half8& lo) const
     {
         floatx4 a[SP][2];
 #pragma unroll
@@ -76,6 +86,7 @@ struct LowRank {
             v[i] = a[0][i / 4][i % 4];
 #pragma unroll
             for (int s = 1; s < SP; ++s) v[i] += a[s][i / 4][i % 4];
+            v[i] = in ? v[i] : 0.0f;
             most = larger(most, v[i]);
         }
         const Scale scale(rows_max<MT>(most));
@@ -123,17 +134,18 @@ struct LowRank {
             const uint16_t* up = Up + (size_t)first * N * r;
             for (int k0 = from; k0 < r; k0 += step) {
                 const int k = min(k0 + kq, r - 8);
+                const bool in = k0 + kq < r;
                 half8 hi, lo, u[FN];
 #pragma unroll
                 for (int g = 0; g < FN; ++g) u[g] = *(const half8*)(up + (size_t)min(col0 + g * MT + l, N - 1) * r + k);
-                const float down = pairs<MT, SP>(min(row0 + l, M - 1), k, hi, lo);
+                const float down = pairs<MT, SP>(min(row0 + l, M - 1), k, in, hi, lo);
                 const typename MF::acc_t f = beside_rows<MF>(down);
 #pragma unroll
                 for (int g = 0; g < FN; ++g) {
-                    const half8 v = k0 + kq < r ? u[g] : half8{};
+                    const half8 v = in ? u[g] : half8{};
                     typename MF::acc_t t = {};
                     t = MF::run(hi, v, t);
-                    t = MF::run(lo, v, t);
+                    t = MF::run(lo, finite(v), t);
 #pragma unroll
                     for (int i = 0; i < MF::NACC; ++i) sum[g][i] += t[i] * f[i];
                 }
@@ -145,7 +157,7 @@ struct LowRank {
                     const int k = min(k0 + kq, r - 8), col = min(col0 + g * MT + l, N - 1);
                     const bool in = k0 + kq < r;
                     half8 hi, lo;
-                    const float down = pairs<MT, SP>(min(row0 + l, M - 1), k, hi, lo);
+                    const float down = pairs<MT, SP>(min(row0 + l, M - 1), k, in, hi, lo);
                     const typename MF::acc_t f = beside_rows<MF>(down);
                     uint64_t left = some;
                     while (left) {
@@ -165,7 +177,7 @@ struct LowRank {
                             const half8 v = in ? u[n] : half8{};
                             typename MF::acc_t t = {};
                             t = MF::run(hi, v, t);
-                            t = MF::run(lo, v, t);
+                            t = MF::run(lo, finite(v), t);
 #pragma unroll
                             for (int i = 0; i < MF::NACC; ++i)
                                 sum[g][i] += ((uint32_t)rows[n] >> MF::row(i, lane)) & 1 ? t[i] * f[i] : 0.0f;
