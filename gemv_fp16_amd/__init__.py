@@ -864,8 +864,7 @@ def route_topk(logits, k: int, bias=None, score: str = "softmax", groups: int = 
     expert whose logit is -inf is never taken; where none is left the id is -1
     and the weight 0.  Returns (ids (T, k) int32, weights (T, k) fp32, offsets
     (E+1,) int32, place (T, k) int32): the experts' row groups, and each choice's
-    row when they are sorted by expert (None, None with rows=False).  Where none of
-    them is given, they are parts of one allocation."""
+    row when they are sorted by expert (None, None with rows=False)."""
     import torch
     if logits.dim() != 2 or not 1 <= k <= logits.shape[1]:
         raise ValueError("logits must be (T, E) and k 1 to E")
@@ -885,26 +884,25 @@ def route_topk(logits, k: int, bias=None, score: str = "softmax", groups: int = 
         b = _ptr(bias, f, "bias")
         tensors.append(bias)
     if rows and ids is weights is offsets is place is workspace is stream is None:
-        # all four and the workspace from one allocation, in rows of k: each of its own
-        # would cost as much as the rest of a call's checks
-        n, rest = T * k, (E + k + (need + 3) // 4) // k
-        buf = logits.new_empty((3 * T + rest, k), dtype=i32)
-        ids, place, weights, tail = torch.split_with_sizes(buf, (T, T, T, rest))
-        weights, offsets = weights.view(f), tail.as_strided((E + 1,), (1,))
-        i = buf.data_ptr()
-        p, g, o = i + 4 * n, i + 8 * n, i + 12 * n
-        w = o + 4 * (E + 1)
-    else:
-        ids = _out(ids, logits, (T, k), i32, stream, "ids")
-        weights = _out(weights, logits, (T, k), f, stream, "weights")
-        i, g = _ptr(ids, i32, "ids"), _ptr(weights, f, "weights")
-        tensors += (ids, weights)
-        if rows:
-            offsets = _out(offsets, logits, (E + 1,), i32, stream, "offsets")
-            place = _out(place, logits, (T, k), i32, stream, "place")
-            o, p = _ptr(offsets, i32, "offsets"), _ptr(place, i32, "place")
-            w, need, keep = _workspace(workspace, logits, need, stream)
-            tensors += (offsets, place) if keep is None else (offsets, place, keep)
+        # each an allocation of its own, without the checks of a caller's
+        ids = logits.new_empty((T, k), dtype=i32)
+        weights, place, offsets = torch.empty_like(ids, dtype=f), torch.empty_like(ids), ids.new_empty(E + 1)
+        i, g, o, p = ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(), place.data_ptr()
+        if need:
+            keep = ids.new_empty((need + 3) // 4)
+            w = keep.data_ptr()
+        _launch("route_topk", tensors, None, x, f32, b, T, E, k, cfg, i, g, o, p, w, need)
+        return ids, weights, offsets, place
+    ids = _out(ids, logits, (T, k), i32, stream, "ids")
+    weights = _out(weights, logits, (T, k), f, stream, "weights")
+    i, g = _ptr(ids, i32, "ids"), _ptr(weights, f, "weights")
+    tensors += (ids, weights)
+    if rows:
+        offsets = _out(offsets, logits, (E + 1,), i32, stream, "offsets")
+        place = _out(place, logits, (T, k), i32, stream, "place")
+        o, p = _ptr(offsets, i32, "offsets"), _ptr(place, i32, "place")
+        w, need, keep = _workspace(workspace, logits, need, stream)
+        tensors += (offsets, place) if keep is None else (offsets, place, keep)
     _launch("route_topk", tensors, stream, x, f32, b, T, E, k, cfg, i, g, o, p, w, need)
     return ids, weights, offsets, place
 
