@@ -39,8 +39,8 @@ int stride_of(int chunks) { return ceil_div(chunks, 8) * 8; }
 size_t counts_bytes(int T, int k, int E)
 {
     if (T <= kOneTokens && (int64_t)T * k <= kOneEntries) return 0;
-    const int by_tokens = k <= kRouteMaxTop ? ceil_div(T, chunk_of(T, k, kTokensLeast)) : 0;
-    const int by_entries = ceil_div(T * k, chunk_of(T * k, 1, kEntriesLeast));
+    const int by_tokens = k <= kRouteMaxTop ? ceil_div_large(T, chunk_of(T, k, kTokensLeast)) : 0;
+    const int by_entries = ceil_div_large(T * k, chunk_of(T * k, 1, kEntriesLeast));
     return (size_t)stride_of(by_tokens > by_entries ? by_tokens : by_entries) * E * sizeof(uint16_t);
 }
 
@@ -191,7 +191,7 @@ int route_rows(const int* ids, int T, int k, int E, int* offsets, int* place, vo
         return status(hipGetLastError());
     }
     constexpr int W = 8;
-    const int chunk = chunk_of(n, 1, kEntriesLeast), chunks = ceil_div(n, chunk);
+    const int chunk = chunk_of(n, 1, kEntriesLeast), chunks = ceil_div_large(n, chunk);
     auto kern = rank_kernel<W, false>;
     hipLaunchKernelGGL(kern, dim3(chunks), dim3(W * kWave), ((W + 2) * E + 1) * 4, s, ids, place, n, E, chunk,
                        (uint16_t*)workspace, stride_of(chunks), offsets);
