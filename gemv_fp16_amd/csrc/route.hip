@@ -88,9 +88,10 @@ hipError_t launch_route(const RouteArgs& a, bool quad, bool wide, bool f32, int 
 {
     return by_width(a.E, quad ? 16 : kWave, [&](auto v) {
         constexpr int VPT = decltype(v)::value;
-        if (quad)
-            return f32 ? launch_route<W, FINAL, VPT, float, true, true>(a, grid, stream)
-                       : launch_route<W, FINAL, VPT, float, false, true>(a, grid, stream);
+        if constexpr (VPT <= 8 || (W == kWaves && !FINAL))    // past 128 experts for many tokens alone
+            if (quad)
+                return f32 ? launch_route<W, FINAL, VPT, float, true, true>(a, grid, stream)
+                           : launch_route<W, FINAL, VPT, float, false, true>(a, grid, stream);
         if (wide)
             return f32 ? launch_route<W, FINAL, VPT, double, true, false>(a, grid, stream)
                        : launch_route<W, FINAL, VPT, double, false, false>(a, grid, stream);
