@@ -256,7 +256,7 @@ int band(const LoraArgs& a, hipStream_t stream)
         if (band_self(a)) return status(launch_lora_band<LoraBandCfg<MB, XB, RING>, true>(a, stream));
     const int rc = down(a, stream);
     if (rc) return rc;
-    // a smaller ring where H takes its place: 16 rows of rank 256, 32 of rank 248 on
+    // a smaller ring where H takes its place: 16 rows of rank 248 and 256, 32 of rank 256
     if (LoraBandCfg<MB, XB, RING>::lds_bytes(a.S * a.M * a.r) <= 160 * 1024)
         return status(launch_lora_band<LoraBandCfg<MB, XB, RING>, false>(a, stream));
     return status(launch_lora_band<LoraBandCfg<MB, XB, RING - 1>, false>(a, stream));
