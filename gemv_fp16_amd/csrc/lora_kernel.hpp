@@ -138,8 +138,8 @@ __global__ __launch_bounds__(Cfg::W * kWave) void lora_down_kernel(LoraArgs a, i
                 }
             }
         }
+        wait_vmcnt<0>();                         // rows of A that nobody wanted: the next ones go to their place
     }
-    wait_vmcnt<0>();                             // rows of A that nobody wanted
 #endif
 }
 

@@ -69,3 +69,24 @@ def test_onto_a_base_in_fp16_and_fp32(M, N, K, r, L):
     assert torch.equal(got, want), int((got != want).sum())
     got = gf.lora_add_f16(A, ids, Down, Up, dev(base.astype(np.float32)), scales)
     assert torch.equal(got, want), int((got != want).sum())
+
+
+def test_more_rows_than_workgroups():
+    """2^24 rows and some: the products by Down walk more blocks of 16 rows than there are
+    workgroups, most of them without an adapter."""
+    M, N, K, r, L = 2 ** 24 + 5003, 8, 8, 8, 3
+    g = torch.Generator(device="cuda").manual_seed(3)
+    ints = lambda most, *shape: torch.randint(-most, most + 1, shape, generator=g, device="cuda").half()
+    A, B, Down, Up, base = ints(7, M, K), ints(9, N, K), ints(9, L, r, K), ints(1, L, N, r), ints(900, M, N)
+    ids = torch.randint(0, 60, (M,), generator=g, device="cuda").int()         # a twentieth have one
+    scales = torch.tensor([1.0, -1.0, 2.0], device="cuda")
+    low = torch.zeros((M, N), device="cuda")
+    for e in range(L):
+        m = torch.where(ids == e)[0]
+        low[m] = scales[e] * ((A[m].float() @ Down[e].float().T) @ Up[e].float().T)
+    print("lora", M, N, K, r, flush=True)
+    C = gf.gemm_f16_nt_lora(A, B, ids, Down, Up, scales)
+    assert torch.equal(C, (A.float() @ B.float().T + low).half())
+    want = (base.float() + low).half()
+    assert torch.equal(gf.lora_add_f16(A, ids, Down, Up, base.float(), scales), want)
+    assert torch.equal(gf.lora_add_f16(A, ids, Down, Up, base, scales), want)
