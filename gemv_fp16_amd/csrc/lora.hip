@@ -48,14 +48,18 @@ int slices_of(int M, int N, int K)
 // Floats of n parts of the base, H's parts behind them 16-byte aligned.
 size_t base_floats(int n, int M, int N) { return ((size_t)n * M * N + 3) / 4 * 4; }
 
-// Where no fused form fits, the base comes in fp32: about 8 M floats of rows at a time,
-// and at least 64 rows, which are one tile's.
+// Where no fused form fits, the base comes in fp32, some 32 M floats of rows at a time (128
+// MB of workspace), in equal shares of whole tiles.  5000 rows of rank 4 at 4096 x 4096: 275
+// us, in rounds of 16 M 312; 1000 at 11008 x 4096 166, in rounds of 8 M 240.
 int base_rows(int M, int N)
 {
-    const int rows = (1 << 23) / N / 64 * 64;
-    return M < 64 || rows < 64 ? (M < 64 ? M : 64) : (rows < M ? rows : M);
+    const int64_t rounds = ((int64_t)M * N + (1 << 25) - 1) >> 25;
+    const int64_t rows = (M + rounds - 1) / rounds, whole = (rows + 127) / 128 * 128;
+    return (int)(whole < M ? whole : M);
 }
-// Its parts of K: up to 64 rows as many as make 256 tiles of 64 x 64.
+// Its parts of K: up to 64 rows as many as make 256 tiles of 64 x 64.  64 rows of 24
+// adapters at 4096 x 4096: 22.7 us with 4, 39.8 with 1, 28.3 with 2, 31.2 with 8; 32 rows at
+// 4096 x 14336 47, 103, 62, 52; but 64 at 11008 x 4096 46 with 1, 42 with 2.
 int base_parts(int M, int N, int K)
 {
     if (M > 64) return 1;
@@ -142,10 +146,10 @@ int up(const LoraArgs& a, hipStream_t stream)
         const int vec = (reinterpret_cast<uintptr_t>(a.C) & 7) == 0 && a.N % 4 == 0;
         const int64_t items = (int64_t)ceil_div(a.M, 16) * ceil_div(a.N, 16);
         // 64 columns a wave (a quarter of the loads of H, and of the waves), where there are
-        // many and most blocks of rows have one adapter: 512 rows of 8 adapters at 4096 x
-        // 4096 10.9 us against 16.8, 300 of them 13.1 against 13.9, 160 12.6 against 11.3;
-        // 300 rows of 300 adapters 56 against 29.
-        const bool wide = items > 8192 || (items > 4096 && a.L <= a.M / 16);
+        // many and an adapter has several rows: 512 rows of 8 adapters at 4096 x 512 8.5 us
+        // against 10.5 with 16 columns, 448 11.2 against 10.5; 1024 rows of 128 18.2 against
+        // 20.5, of 256 26.1 against 25.8, of 1024 61 against 45.
+        const bool wide = items >= 8192 && a.L <= a.M / 8;
         if (wide && a.S <= kLoraTileParts)
             hipLaunchKernelGGL((lora_up_kernel<kLoraTileParts, BASE>), dim3(grid_of((items / 4 + 3) / 4)), dim3(256), 0, stream, a, vec);
         else if (wide)
@@ -228,6 +232,9 @@ int vec(const LoraArgs& a, hipStream_t stream)
     return rc ? rc : status(launch_lora_vec<MV, UNROLL, WAVES, false>(a, grid, iters, (int)most, at.total, stream));
 }
 
+// Loads in flight by how they divide a row's: at 4096 x 4096 10.4 us with 8, 10.6 with 4,
+// 12.5 with 2; at K = 2048 8.6, 7.2, 7.7; at 1024 7.5, 6.6, 5.8 (but at 11008 25.7, 27.3,
+// 30.6).
 template <int MV>
 int vec(const LoraArgs& a, hipStream_t stream)
 {
@@ -330,7 +337,8 @@ int gemm_f16_nt_lora(const void* A, const void* B, const int* ids, const void* D
     }
     if (al && band_takes(M, N, K)) return band(a, (hipStream_t)stream);
     // From 33 to 64 rows the base in parts is ahead of tiles (64 rows of 24 adapters at
-    // 4096 x 4096: 23 us against 51).
+    // 4096 x 4096: 22.7 us against 43.0; of 8 at 16384 x 4096 52 against 63, at 11008 x 4096
+    // 46 against 44).
     if (al && on16(C) && M > 64) {
         rc = down(a, (hipStream_t)stream);
         return rc ? rc : tiles(a, (hipStream_t)stream);

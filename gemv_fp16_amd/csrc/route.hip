@@ -151,6 +151,9 @@ int route_topk(const void* logits, int logits_f32, const float* bias, int T, int
     a.scale = cfg->scale;
     a.offsets = offsets; a.place = place; a.counts = (uint16_t*)workspace; a.stride = 0;
     const bool wide = bias || (a.groups > 1 && a.group_best == 2);
+    // Four tokens a wave past 128 experts (16 logits a lane) where there are many: 8192 tokens
+    // of 256 experts 16.2 us against 19.9, 4096 15.4 against 16.2, 2048 15.3 against 15.0, 64
+    // 9.8 against 8.8 (but 1024 11.1 against 14.4).
     const bool quad = !wide && a.groups == 1 && k <= 16 && E <= (T < 4096 ? 128 : 256), f32 = logits_f32 != 0;
     hipStream_t s = (hipStream_t)stream;
     if (offsets && T <= (quad ? 4 : 1) * kOneTokens) {

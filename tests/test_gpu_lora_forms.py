@@ -35,7 +35,7 @@ CASES = {
               (2100, 2200, 264, 16, 3), (2100, 2200, 128, 40, 500), (2100, 4100, 2056, 16, 4), (2100, 4104, 2048, 72, 90),
               (4100, 4100, 1544, 16, 4), (4100, 4100, 1544, 8, 2000)],
     # operands, ranks or K of no such form, with many rows
-    "general": [(1, 2100, 4096, 4, 4), (70, 4100, 1030, 12, 3), (2100, 4100, 520, 4, 4), (300, 28700, 64, 4, 3)],
+    "general": [(1, 2100, 4096, 4, 4), (70, 4100, 1030, 12, 3), (2100, 4100, 520, 4, 4), (300, 28700, 64, 4, 3), (520, 66000, 64, 4, 3)],
 }
 
 

@@ -133,9 +133,11 @@ def test_refusals():
         assert f(**bad) == gf.GF_ERR_INVALID_ARG, bad
     assert f(M=0, base=NULL, ws=NULL, b=0) == gf.GF_OK
     # a round of rows, its base in fp32 and the products by Down are what a long call needs
-    one = L.lora_workspace_bytes(2048, 4096, 4096, 16)
-    assert 2048 * 4096 * 4 <= one <= 2048 * 4096 * 4 + 2 * 2048 * 16 * 4
-    assert L.lora_workspace_bytes(2 ** 17, 4096, 64, 16) <= 2048 * 4096 * 4 + 2 ** 17 * 16 * 4
+    one = L.lora_workspace_bytes(4096, 4096, 4096, 16)
+    assert 4096 * 4096 * 4 <= one <= 4096 * 4096 * 4 + 2 * 4096 * 16 * 4
+    assert L.lora_workspace_bytes(2 ** 17, 4096, 64, 16) <= 8192 * 4096 * 4 + 2 ** 17 * 16 * 4
+    assert L.lora_workspace_bytes(10000, 4096, 64, 16) <= 5120 * 4096 * 4 + 10000 * 16 * 4
+    assert L.lora_workspace_bytes(2, 2 ** 29, 2, 16) <= 2 * 2 ** 29 * 4 + 64 * 16 * 4
     assert L.lora_workspace_bytes(0, 8, 8, 8) == 0 and L.lora_workspace_bytes(8, 0, 8, 8) == 0
 
 
