@@ -90,3 +90,26 @@ def test_more_rows_than_workgroups():
     want = (base.float() + low).half()
     assert torch.equal(gf.lora_add_f16(A, ids, Down, Up, base.float(), scales), want)
     assert torch.equal(gf.lora_add_f16(A, ids, Down, Up, base, scales), want)
+
+
+@pytest.mark.parametrize("M,N,K,r,L", [(2, 264, 1024, 16, 3), (20, 264, 2048, 16, 3), (20, 264, 1024, 40, 3), (40, 264, 1024, 16, 3),
+                                       (100, 264, 1024, 24, 3), (300, 2100, 512, 16, 3)])
+@pytest.mark.parametrize("odd", ["A", "B", "Down", "Up", "C", "base"])
+def test_one_operand_off_the_16_byte_grid(M, N, K, r, L, odd):
+    p = Integers(M, N, K, r, L, M + K)
+
+    def place(name, v):
+        t = dev(v)
+        if name != odd:
+            return t
+        flat = torch.empty(t.numel() + 3, dtype=t.dtype, device="cuda")
+        flat[3:].copy_(t.view(-1))
+        return flat[3:].view(t.shape)
+    A, B, Down, Up, base = (place(n, v) for n, v in (("A", p.A), ("B", p.B), ("Down", p.Down), ("Up", p.Up),
+                                                     ("base", p.base.astype(np.float32))))
+    scales, ids, want = dev(p.scales), dev(p.ids), torch.from_numpy(p.once()).cuda()
+    print("lora off the grid", M, N, K, r, L, odd, flush=True)
+    for call in (lambda c: gf.gemm_f16_nt_lora(A, B, ids, Down, Up, scales, C=c),
+                 lambda c: gf.lora_add_f16(A, ids, Down, Up, base, scales, out=c)):
+        C = place("C", np.full((M, N), 7, dtype=np.float16))
+        assert torch.equal(call(C), want), int((C != want).sum())
