@@ -610,11 +610,11 @@ struct LoraBandCfg {
     static constexpr int MB = MB_, XB = XB_, RING = RING_, WAVES = 8, BK = 128, LOADS = 4, TASK_BYTES = 4096;
     static constexpr int ROWS = 16 * MB;
     static constexpr int RED_BYTES = 2 * WAVES * ROWS * 16 * 4;
-    // the rings, the waves' sums, the adapters in use and their rows, the scales of H's rows,
-    // H's parts in whole loads
+    // the rings, the waves' sums, the adapters in use and their rows, the largest of H's rows
+    // and their scales, H's parts in whole loads
     static constexpr int lds_bytes(int h_floats)
     {
-        return WAVES * RING * TASK_BYTES + RED_BYTES + 3 * ROWS * 4 + ceil_div(h_floats * 4, 1024) * 1024;
+        return WAVES * RING * TASK_BYTES + RED_BYTES + 4 * ROWS * 4 + ceil_div(h_floats * 4, 1024) * 1024;
     }
 };
 
@@ -632,9 +632,11 @@ __global__ __launch_bounds__(Cfg::WAVES * 64) void lora_band_kernel(LoraArgs a, 
     GF_LDS float* red = (GF_LDS float*)((GF_LDS char*)smem_raw + WAVES * RING * Cfg::TASK_BYTES);
     GF_LDS int* used = (GF_LDS int*)((GF_LDS char*)red + Cfg::RED_BYTES);
     GF_LDS uint32_t* rows_of = (GF_LDS uint32_t*)(used + MR);
-    GF_LDS float* back = (GF_LDS float*)(rows_of + MR);  // what each row's scaled sums are multiplied by
+    GF_LDS int* most_of = (GF_LDS int*)(rows_of + MR);   // the largest magnitude of each row of H
+    GF_LDS float* back = (GF_LDS float*)(most_of + MR);  // what its scaled sums are multiplied by
     GF_LDS float* H = back + MR;                         // S x M x r; then, 4 ranks to 16 bytes, their fp16 pairs
 
+    if (threadIdx.x < MR) most_of[threadIdx.x] = 0;      // (a barrier before the first pack())
     const int nblk = ceil_div(K, Cfg::BK);
     const int b0 = wave * nblk / WAVES, nk = (wave + 1) * nblk / WAVES - b0;   // this wave's tasks of K
     const int blocks = ceil_div(N, 16), part = blockIdx.x, parts = gridDim.x;
@@ -725,20 +727,25 @@ __global__ __launch_bounds__(Cfg::WAVES * 64) void lora_band_kernel(LoraArgs a, 
                 x[b][m] = *(const half8*)(k < K && b < 4 * nk ? (const void*)(src + k) : (const void*)g_zero16);
             }
         }
-    // H's parts to LDS, then each value as a scaled pair of fp16 in its place (low_rank.hpp),
-    // a wave a row (r <= 256: 4 ranks a lane)
+    // H's parts to LDS, then each value as a scaled pair of fp16 in its place (low_rank.hpp):
+    // the parts' sums and each row's largest, a barrier, the pairs.
     auto pack = [&](int parts) __attribute__((always_inline)) {
-        for (int m = wave; m < M; m += WAVES) {
-            const int i = m * r + lane * 4;
-            floatx4 v = {};
-            if (lane * 4 < r) {
-                v = *(const GF_LDS floatx4*)(H + i);
-                for (int p = 1; p < parts; ++p) v += *(const GF_LDS floatx4*)(H + p * M * r + i);
-            }
+        for (int i = threadIdx.x * 4; i < M * r; i += WAVES * kWave * 4) {
+            floatx4 v = *(const GF_LDS floatx4*)(H + i);
+            for (int p = 1; p < parts; ++p) v += *(const GF_LDS floatx4*)(H + p * M * r + i);
+            *(GF_LDS floatx4*)(H + i) = v;
             float most = 0.0f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) most = LowRank::larger(most, v[e]);
-            const LowRank::Scale scale(wave_max(most));
+            // magnitudes are ordered as integers, in whichever order they come
+            __hip_atomic_fetch_max(&most_of[i / r], __builtin_bit_cast(int, most), __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_WORKGROUP);
+        }
+        lds_barrier();
+        for (int i = threadIdx.x * 4; i < M * r; i += WAVES * kWave * 4) {
+            const floatx4 v = *(const GF_LDS floatx4*)(H + i);
+            const int m = i / r;
+            const LowRank::Scale scale(__builtin_bit_cast(float, most_of[m]));
             half8 pair;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -747,8 +754,8 @@ __global__ __launch_bounds__(Cfg::WAVES * 64) void lora_band_kernel(LoraArgs a, 
                 pair[e] = hi;
                 pair[e + 4] = lo;
             }
-            if (lane * 4 < r) *(GF_LDS half8*)(H + i) = pair;
-            if (lane == 0) back[m] = scale.down;
+            *(GF_LDS half8*)(H + i) = pair;
+            if (i == m * r) back[m] = scale.down;
         }
         lds_barrier();
     };
