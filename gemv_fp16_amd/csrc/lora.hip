@@ -18,9 +18,9 @@ int status(hipError_t e) { return e == hipSuccess ? GF_OK : GF_ERR_HIP; }
 // about 40 GB/s: up to 32 rows as many as make 256 workgroups of them (the streaming
 // form adds them in LDS, which holds all), beyond as many as make 128 of 16-row blocks,
 // but no more than the tiles' epilogue loads at once (100 rows of 8 adapters at 4096 x
-// 4096: 35 us with 4 parts, 40 with one).  Tiles and lora_add_f16 read H, all parts of
-// it, again for every 64 columns: 2048 rows of rank 64 took 99 us with 4 parts, 91 with
-// one, rank 16 77 either way.
+// 4096: 35.7 us with 4 parts, 38.4 with one).  Tiles and lora_add_f16 read H, all parts of
+// it, again for every 64 columns: 2048 rows of rank 64 took 99 us with 4 parts, 94 with
+// one, rank 16 81 and 79.
 constexpr int most_floats(int M) { return M <= 16 ? 3840 : 7936; }
 int parts_of(int M, int K, int r)
 {
@@ -33,10 +33,10 @@ int parts_of(int M, int K, int r)
 }
 
 // The form in slices of K: from 3 to 32 rows, of 4 to 8 slices of K, up to 8192 columns;
-// 0 elsewhere.  32 rows of 8 adapters, rank 16: 12.2 us at 1024 x 4096 (streaming 19.8),
-// 17.1 at 4096 x 4096 (21.7), 25.3 at 8192 x 4096 (26.3), 12.8 at 4096 x 2048 (16.2); but
-// 32.5 at 11008 x 4096 (29.9), 12.0 at 4096 x 512 (11.8).  3 rows of one adapter: 8.9 us
-// at 1024 x 4096 (12.8), 9.4 at 4096 x 2048 (10.0), 8.9 at 4096 x 1024 (7.6).  16 rows of
+// 0 elsewhere.  32 rows of 8 adapters, rank 16: 12.5 us at 1024 x 4096 (streaming 19.6),
+// 17.2 at 4096 x 4096 (22.1), 25.5 at 8192 x 4096 (26.7), 12.9 at 4096 x 2048 (16.7); but
+// 33.4 at 11008 x 4096 (31.0), 11.4 at 4096 x 512 (12.0).  3 rows of one adapter: 9.0 us
+// at 1024 x 4096 (13.1), 9.1 at 4096 x 2048 (10.1), 8.5 at 4096 x 1024 (7.9).  16 rows of
 // 8192 x 8192, 16 slices: 40.6 (37.5).
 constexpr int kSliceColumns = 8192;
 int slices_of(int M, int N, int K)
@@ -209,10 +209,10 @@ int tiles(const LoraArgs& a, hipStream_t stream)
 }
 
 // Base and adapters, B in vectors; GF_ERR_UNSUPPORTED where it does not fit.  Up to 2
-// rows (4096 x 4096, rank 16: 10.9 us for one and 14.8 for two, the streaming form
+// rows (4096 x 4096, rank 16: 10.5 us for one and 14.4 for two, the streaming form
 // 15.0 and 15.2; at 4 rows 18.6 against 15.1).  It works out H itself up to 64 ranks in
-// all: 10.9 us against 15.1 with a launch for it at one row, 14.8 against 17.0 at two,
-// 16.5 against 18.0 at rank 64; at 128 ranks 29 against 19.
+// all: 10.5 us against 15.1 with a launch for it at one row, 14.4 against 17.0 at two,
+// 15.8 against 18.0 at rank 64; at 128 ranks 29 against 19.
 constexpr int kVecRows = 2, kVecSelf = 64;
 
 template <int MV, int UNROLL>
@@ -247,8 +247,8 @@ int vec(const LoraArgs& a, hipStream_t stream)
 bool band_takes(int M, int N, int K) { return N >= 16 && ((M <= 16 && K <= 8192) || (M <= 32 && K <= 4096)); }
 
 // Whether the streaming form works out H itself: one adapter of up to 16 ranks (32
-// rows at 4096 x 2048: 13.2 us against 17.0 with a launch for it, 16 at 4096 x 4096
-// 17.6 against 19.0; with two blocks of ranks 18.4 against 15.2).
+// rows at 4096 x 1024: 10.5 us against 12.1 with a launch for it, 16 8.6 against 10.4; at
+// 16384 x 2048 and past even; with two blocks of ranks 18.4 against 15.2).
 bool band_self(const LoraArgs& a)
 {
     const int64_t most = a.M < a.L ? a.M : a.L;

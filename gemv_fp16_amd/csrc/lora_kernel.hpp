@@ -180,7 +180,7 @@ __global__ __launch_bounds__(256) void lora_down_any_kernel(LoraArgs a)
 // The operands are swapped (Up's rows in the place of A's), so that a lane holds four
 // neighbouring columns of one row.  C is asked for before the sums are worked out, which
 // takes a chain of loads out of it (lora_add_f16, 2048 rows of 8 adapters, rank 64, at
-// 4096 x 4096: 35 us, rank 16 21; a copy of C takes 6.5, the products by Down 7 to 14).
+// 4096 x 4096: 35.5 us, rank 16 21; a copy of C takes 6.5, the products by Down 7 to 14).
 // What bounds it past rank 16 are H's and Up's bytes through L2.
 struct SwappedMfma {
     typedef floatx4 acc_t;
@@ -197,7 +197,7 @@ struct SwappedMfma {
 // 32 ranks in turn, and the first adds what the others found, in order.  True for the
 // waves that have the sums.  All of a wave's adapters have their loads in flight: each
 // round of them is a chain of 3 us.  (lora_add_f16, 32 rows of 32 adapters, rank 64, at
-// 8192 x 4096: 23.7 us, with one wave to a block and 8 adapters at a time 27.0.)
+// 8192 x 4096: 22.2 us, with one wave to a block and 8 adapters at a time 27.0.)
 template <int J, int SP>
 __device__ __forceinline__ bool lora_join(const LowRank& low, floatx4 (&sum)[1], int row0, int col0, int M, int N)
 {
@@ -916,8 +916,8 @@ hipError_t launch_lora_band(const LoraArgs& a, hipStream_t stream)
 // blocks of B, and 16 ranks of Down at a time like any of them, through a ring of tasks
 // as above.  A slice's sums go to memory, part by part; a second launch adds the parts
 // and the adapters, and rounds once.  The parts are M / 128 of B's bytes, written and
-// read again.  32 rows of 24 adapters at 4096 x 4096, rank 16: 18.4 us, 11.5 of them the
-// first launch (2.9 TB/s) and 6 the second, a chain of three loads with 13 adapters
+// read again.  32 rows of 24 adapters at 4096 x 4096, rank 16: 19.2 us, 11.5 of them the
+// first launch (2.9 TB/s) and 7 the second, a chain of three loads with 13 adapters
 // for 16 rows; the base alone takes 12, the streaming form with the adapters 22.
 // K % 8 == 0, r % 8 == 0, N >= 16; A, B, Down and Up 16-byte aligned; M <= 16 * MB.
 constexpr int kLoraSlice = 512, kLoraSlices = 8;

@@ -209,8 +209,8 @@ def main(argv=None):
             for i in range(a.iters):
                 down, up = low[i % copies]
                 if bits == 4:
-                    gf.gemm_w4_f16_nt(A, *w[i % copies], C=C, group=64)
-                    gf.lora_add_f16(A, ids, down, up, C)
+                    sums = gf.gemm_w4_f16_nt(A, *w[i % copies], group=64, out_f32=True)
+                    gf.lora_add_f16(A, ids, down, up, sums, out=C)
                 else:
                     gf.gemm_f16_nt_lora(A, w[i % copies], ids, down, up, C=C)
     else:
