@@ -62,8 +62,6 @@ __device__ __forceinline__ void static_for(F&& f)
 }
 
 __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
-// The same for a that may be next to 2^31, b > 0.
-__host__ __device__ __forceinline__ int ceil_div_large(int a, int b) { return a / b + (a % b != 0); }
 
 // Dynamic LDS above 64 KiB must be opted into, per kernel and per device:
 // here on the device the launch's stream belongs to (the current device for

@@ -17,6 +17,9 @@ constexpr int kRouteMaxTokens = 1 << 30;
 constexpr int kOneTokens = 16, kOneEntries = 4096, kChunks = 256, kSmall = 1024;
 constexpr int kWaves = 16, kSmallWaves = 4;
 
+// ceil_div of an a that may be next to 2^31.
+int ceil_div_large(int a, int b) { return a / b + (a % b != 0); }
+
 // Units (tokens, or entries) a chunk, of n with k entries each.
 int chunk_of(int n, int k, int least)
 {
