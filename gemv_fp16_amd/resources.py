@@ -30,7 +30,9 @@ def load(path: str = RESOURCES) -> dict:
             rep = json.load(open(path))
         except (OSError, ValueError):
             rep = {}
-        res = {v["name"]: v for v in rep.values() if "name" in v}
+        # the plain products' kernels by gemm_kernel_name's name, without the arguments' type
+        res = {v["name"].replace(", gf::GemmArgs>(gf::GemmArgs)", ">(gf::GemmArgs)"): v
+               for v in rep.values() if "name" in v}
         if path != RESOURCES:
             return res
         _cache = res
