@@ -5,7 +5,7 @@
 // added here in order.  The matrix cores take fp16, so each value goes in as two, its
 // nearest fp16 and what that leaves, after a power of two that brings the largest of
 // the row's ranks in one step to 2^14 .. 2^15, and the step's sums are multiplied by its
-// inverse: 22 bits of every value down to 2^-18 of the largest, 2^-40 of the largest
+// inverse: 22 bits of every value down to 2^-17 of the largest, 2^-39 of the largest
 // below, whatever the size of H.  A block of rows costs one pass for each adapter that it
 // has; where it has several, each one's sums are added to its own rows alone, so that
 // an infinity or a NaN in one adapter stays in the rows that have it.  Infinities come out

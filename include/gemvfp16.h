@@ -528,7 +528,7 @@ int combine_f16_bwd(const void* dY, const void* C, const int* place, const float
  *
  * fp32 accumulation; the scaled products by Down stay in fp32.  From 3 rows on the matrix
  * cores take them as two fp16 each, scaled by a power of two: 22 bits of every one down
- * to 2^-18 of its row's largest, below that an error of up to 2^-40 of the largest.
+ * to 2^-17 of its row's largest, below that an error of up to 2^-39 of the largest.
  * One rounding at the end.  An infinity or a NaN in an adapter reaches
  * the rows that have it and no others.  Ranks 1 <= r <= 256; K % 8 == 0, r % 8 == 0 and
  * 16-byte aligned operands are fastest, everything else runs a general form.  The
