@@ -526,15 +526,16 @@ int combine_f16_bwd(const void* dY, const void* C, const int* place, const float
  * lora_add_f32: C[m] = base[m] + the same, rounded once, every row of C; base (M x N
  * floats, 4-byte aligned) is not changed and does not overlap C.
  *
- * fp32 accumulation; the scaled products by Down stay in fp32.  From 3 rows on the matrix
- * cores take them as two fp16 each, scaled by a power of two: 22 bits of every one down
- * to 2^-17 of its row's largest, below that an error of up to 2^-39 of the largest.
- * One rounding at the end.  An infinity or a NaN in an adapter reaches
- * the rows that have it and no others.  Ranks 1 <= r <= 256; K % 8 == 0, r % 8 == 0 and
+ * fp32 accumulation; the scaled products by Down stay in fp32.  The matrix cores (from 3
+ * rows on, and in lora_add_*) take them as two fp16 each, scaled by a power of two: 22
+ * bits of every one down to 2^-17 of its row's largest, below that an error of up to
+ * 2^-39 of the largest.  One rounding at the end.  An infinity or a NaN in an adapter
+ * reaches the rows that have it and no others.  Ranks 1 <= r <= 256; K % 8 == 0, r % 8 == 0 and
  * 16-byte aligned operands are fastest, everything else runs a general form.  The
  * adapters as a whole may pass 2^31 elements, one adapter's part and every other
  * operand may not; no size above 2^30.  workspace: caller-owned device memory, 16-byte
- * aligned, of at least lora_workspace_bytes(M, N, K, r) bytes.  M == 0 or N == 0 is a
+ * aligned, of at least lora_workspace_bytes(M, N, K, r) bytes: the products by Down, and
+ * rows of a base in fp32 (128 MB of them, or 128 rows, at most).  M == 0 or N == 0 is a
  * no-op.  Results repeat bit for bit.  GF_ERR_INVALID_ARG for sizes outside these,
  * NULL or misaligned pointers, or a short workspace.
  */
