@@ -535,7 +535,7 @@ int combine_f16_bwd(const void* dY, const void* C, const int* place, const float
  * adapters as a whole may pass 2^31 elements, one adapter's part and every other
  * operand may not; no size above 2^30.  workspace: caller-owned device memory, 16-byte
  * aligned, of at least lora_workspace_bytes(M, N, K, r) bytes: the products by Down, and
- * rows of a base in fp32 (128 MB of them, or 128 rows, at most).  M == 0 or N == 0 is a
+ * rows of a base in fp32 (about 128 MB of them, or 128 rows).  M == 0 or N == 0 is a
  * no-op.  Results repeat bit for bit.  GF_ERR_INVALID_ARG for sizes outside these,
  * NULL or misaligned pointers, or a short workspace.
  */
